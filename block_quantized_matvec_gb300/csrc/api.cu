@@ -5,6 +5,8 @@
 
 #include "common.cuh"
 #include "ffn_args.cuh"
+#include "kv4.cuh"
+#include "kv4_attention.cuh"
 
 namespace mmvq {
 int launch_quantize_q8_1(const float* x, int K, int ncols, int64_t ldx, void* xq, cudaStream_t s);
@@ -24,6 +26,12 @@ int launch_grouped(int type, const void* W, int n_experts, int64_t rows, int K,
 int launch_repack_planar(int type, const void* W, int64_t rows, int K, void* P, cudaStream_t s);
 int launch_gather_planar(const void* P, int64_t rows, int K, const int32_t* row_ids, int n,
                          void* out, int32_t* status, cudaStream_t s);
+int launch_kv4_append(const Kv4Batch& a, int D, int dtype, const void* k, const void* v,
+                      const int64_t (&strides)[4], cudaStream_t stream);
+int launch_kv4_read(const Kv4Batch& a, int D, int dtype, void* k, void* v, cudaStream_t stream);
+int launch_kv4_attention(const Kv4Batch& a, const Kv4Attention& p, int D, int dtype,
+                         cudaStream_t stream);
+int64_t kv4_attention_workspace_bytes(int D);
 int read_device_fault(int* fault, cudaStream_t stream);
 int launch_wait_timeout_selftest(uint32_t limit_us, cudaStream_t stream);
 int dense_shape(int type, int64_t rows, int K, int ncols, int32_t* info);
@@ -64,6 +72,7 @@ const char* mmvq_strerror(int code) {
     case MMVQ_ERR_SCRATCH:
       return "the layer's intermediates exceed the fixed scratch of mmvq_expert_ffn_noalloc "
              "(MMVQ_NOALLOC_SCRATCH_BYTES)";
+    case MMVQ_ERR_VALUE: return "a non-finite key or value was clamped as it was written";
   }
   return "unknown mmvq status";
 }
@@ -400,6 +409,124 @@ int mmvq_rmsnorm_quantize_q8_1(const float* x, const float* w, float eps, int K,
   if (!aligned(x, 4) || !aligned(w, 4) || !aligned(xq, 16) || (y_out && !aligned(y_out, 4)))
     return MMVQ_ERR_ALIGN;
   return mmvq::launch_rmsnorm_quantize(x, w, eps, K, ncols, ldx, xq, y_out, (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------ 4-bit key/value cache
+
+static bool kv4_dim(int D) { return D == 64 || D == 128 || D == 256; }
+
+static int kv4_dtype_bytes(int dtype) {
+  return dtype == MMVQ_F32 ? 4 : dtype == MMVQ_F16 || dtype == MMVQ_BF16 ? 2 : 0;
+}
+
+static bool kv4_cache_shape(int n_kv_heads, int head_dim, int page_tokens) {
+  return kv4_dim(head_dim) && n_kv_heads >= 1 && n_kv_heads <= 1024 &&
+         page_tokens >= mmvq::kKv4Tile && page_tokens <= 65536 &&
+         page_tokens % mmvq::kKv4Tile == 0;
+}
+
+int64_t mmvq_kv4_page_bytes(int n_kv_heads, int head_dim, int page_tokens) {
+  if (!kv4_cache_shape(n_kv_heads, head_dim, page_tokens)) return -1;
+  return (int64_t)n_kv_heads * (page_tokens / mmvq::kKv4Tile) * mmvq::kv4_tile_bytes(head_dim);
+}
+
+// The checks that every call on a cache makes, and its batch.
+static int kv4_batch(const void* cache, int64_t n_pages, int page_tokens, int n_kv_heads,
+                     int head_dim, const int32_t* page_table, int64_t ld_table,
+                     const int32_t* token_offsets, const int32_t* seq_lens, int n_seqs,
+                     int n_tokens, int dtype, int32_t* status, mmvq::Kv4Batch& a) {
+  if (!kv4_dtype_bytes(dtype)) return MMVQ_ERR_TYPE;
+  if (!cache || !page_table || !token_offsets || !seq_lens) return MMVQ_ERR_NULL;
+  if (!kv4_cache_shape(n_kv_heads, head_dim, page_tokens)) return MMVQ_ERR_SHAPE;
+  if (n_pages < 1 || n_pages > 0x7fffffffLL || ld_table < 1 || ld_table > 0x7fffffffLL / page_tokens)
+    return MMVQ_ERR_SHAPE;
+  if (n_seqs < 1 || n_seqs > mmvq::kKv4MaxSeqs || n_tokens < 0) return MMVQ_ERR_SHAPE;
+  if (!aligned(cache, 16) || !aligned(page_table, 4) || !aligned(token_offsets, 4) ||
+      !aligned(seq_lens, 4) || (status && !aligned(status, 4)))
+    return MMVQ_ERR_ALIGN;
+  a.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  a.n_pages = n_pages;
+  a.page_tokens = page_tokens;
+  a.n_kv_heads = n_kv_heads;
+  a.page_table = page_table;
+  a.ld_table = ld_table;
+  a.offsets = token_offsets;
+  a.lens = seq_lens;
+  a.n_seqs = n_seqs;
+  a.n_tokens = n_tokens;
+  a.status = status;
+  return MMVQ_OK;
+}
+
+int mmvq_kv4_append(int dtype, const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv,
+                    int64_t hv, void* cache, int64_t n_pages, int page_tokens, int n_kv_heads,
+                    int head_dim, const int32_t* page_table, int64_t ld_table,
+                    const int32_t* token_offsets, const int32_t* seq_lens, int n_seqs,
+                    int n_tokens, int32_t* status, mmvq_stream_t stream) {
+  mmvq::Kv4Batch a;
+  const int rc = kv4_batch(cache, n_pages, page_tokens, n_kv_heads, head_dim, page_table, ld_table,
+                           token_offsets, seq_lens, n_seqs, n_tokens, dtype, status, a);
+  if (rc) return rc;
+  if (n_tokens == 0) return MMVQ_OK;
+  if (!k || !v) return MMVQ_ERR_NULL;
+  if (ldk < 0 || hk < 0 || ldv < 0 || hv < 0) return MMVQ_ERR_SHAPE;
+  const int size = kv4_dtype_bytes(dtype);
+  if (!aligned(k, size) || !aligned(v, size)) return MMVQ_ERR_ALIGN;
+  const int64_t strides[4] = {ldk, hk, ldv, hv};
+  return mmvq::launch_kv4_append(a, head_dim, dtype, k, v, strides, (cudaStream_t)stream);
+}
+
+int mmvq_kv4_read(int dtype, void* k, void* v, const void* cache, int64_t n_pages, int page_tokens,
+                  int n_kv_heads, int head_dim, const int32_t* page_table, int64_t ld_table,
+                  const int32_t* token_offsets, const int32_t* seq_lens, int n_seqs, int n_tokens,
+                  int32_t* status, mmvq_stream_t stream) {
+  mmvq::Kv4Batch a;
+  const int rc = kv4_batch(cache, n_pages, page_tokens, n_kv_heads, head_dim, page_table, ld_table,
+                           token_offsets, seq_lens, n_seqs, n_tokens, dtype, status, a);
+  if (rc) return rc;
+  if (n_tokens == 0) return MMVQ_OK;
+  if (!k || !v) return MMVQ_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16)) return MMVQ_ERR_ALIGN;
+  return mmvq::launch_kv4_read(a, head_dim, dtype, k, v, (cudaStream_t)stream);
+}
+
+int64_t mmvq_kv4_attention_workspace_bytes(int head_dim) {
+  if (!kv4_dim(head_dim)) return -1;
+  return mmvq::kv4_attention_workspace_bytes(head_dim);
+}
+
+int mmvq_kv4_attention(int dtype, const void* q, int64_t ldq, int64_t hq, int n_heads, float scale,
+                       int window, int sinks, void* y, float* lse, const void* cache,
+                       int64_t n_pages, int page_tokens, int n_kv_heads, int head_dim,
+                       const int32_t* page_table, int64_t ld_table, const int32_t* token_offsets,
+                       const int32_t* seq_lens, int n_seqs, int n_tokens, void* workspace,
+                       int32_t* status, mmvq_stream_t stream) {
+  mmvq::Kv4Batch a;
+  const int rc = kv4_batch(cache, n_pages, page_tokens, n_kv_heads, head_dim, page_table, ld_table,
+                           token_offsets, seq_lens, n_seqs, n_tokens, dtype, status, a);
+  if (rc) return rc;
+  if (n_tokens == 0) return MMVQ_OK;
+  if (!q || !y || !workspace) return MMVQ_ERR_NULL;
+  if (n_heads < n_kv_heads || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 128 ||
+      ldq < 0 || hq < 0 || window < 0 || sinks < 0)
+    return MMVQ_ERR_SHAPE;
+  if (n_tokens > mmvq::kKv4MaxNew * n_seqs) return MMVQ_ERR_NCOLS;
+  if (!(scale > -INFINITY && scale < INFINITY)) return MMVQ_ERR_SHAPE;
+  if (!aligned(q, kv4_dtype_bytes(dtype)) || !aligned(y, 16) || (lse && !aligned(lse, 4)) ||
+      !aligned(workspace, 256))
+    return MMVQ_ERR_ALIGN;
+  mmvq::Kv4Attention p = {};
+  p.q = q;
+  p.ldq = ldq;
+  p.hq = hq;
+  p.n_heads = n_heads;
+  p.scale = scale;
+  p.window = window;
+  p.sinks = sinks;
+  p.y = y;
+  p.lse = lse;
+  p.workspace = workspace;
+  return mmvq::launch_kv4_attention(a, p, head_dim, dtype, (cudaStream_t)stream);
 }
 
 int mmvq_read_device_fault(int* fault, mmvq_stream_t stream) {

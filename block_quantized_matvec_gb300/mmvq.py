@@ -32,6 +32,7 @@ FLAG_XQ_STABLE = 1
 FLAG_TENSOR_CORE = 2
 ERR_TYPE, ERR_SHAPE, ERR_NCOLS, ERR_NULL, ERR_ALIGN, ERR_ROUTING, ERR_CUDA = -1, -2, -3, -4, -5, -6, -7
 ERR_SCRATCH = -8
+ERR_VALUE = -9
 NOALLOC_SCRATCH_BYTES = 2 << 20  # MMVQ_NOALLOC_SCRATCH_BYTES
 
 # name -> (restype, argtypes); mirrors include/mmvq.h
@@ -64,6 +65,13 @@ SIGNATURES = {
                                      _P, _P, _P, _P]),
     "mmvq_expert_ffn_shape": (_I, [_I, _I, _I, _I, _I, _I, _P]),
     "mmvq_selftest_grid_barrier_timeout": (_I, [_P, ctypes.c_uint, _P]),
+    "mmvq_kv4_page_bytes": (_I64, [_I, _I, _I]),
+    "mmvq_kv4_append": (_I, [_I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I, _I, _I, _P, _I64,
+                             _P, _P, _I, _I, _P, _P]),
+    "mmvq_kv4_read": (_I, [_I, _P, _P, _P, _I64, _I, _I, _I, _P, _I64, _P, _P, _I, _I, _P, _P]),
+    "mmvq_kv4_attention": (_I, [_I, _P, _I64, _I64, _I, ctypes.c_float, _I, _I, _P, _P, _P, _I64,
+                                _I, _I, _I, _P, _I64, _P, _P, _I, _I, _P, _P, _P]),
+    "mmvq_kv4_attention_workspace_bytes": (_I64, [_I]),
 }
 
 
@@ -455,3 +463,133 @@ def gather_planar_rows(W_planar: torch.Tensor, rows: int, K: int, row_ids: torch
     _check(lib().mmvq_gather_planar_rows(_ptr(W_planar), rows, K, _ptr(row_ids), n, _ptr(out),
                                          _ptr(status), _stream(stream)), "mmvq_gather_planar_rows")
     return out, status
+
+
+# ---------------------------------------------------- 4-bit key/value cache --
+
+KV4_TILE = 16  # tokens of a cache tile
+KV4_MAX_NEW = 8  # query tokens of a sequence in kv4_attention
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 30}  # mmvq_dtype
+
+
+def kv4_page_bytes(n_kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    n = lib().mmvq_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
+    if n < 0:
+        raise MMVQError(ERR_SHAPE, "mmvq_kv4_page_bytes")
+    return n
+
+
+def kv4_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int,
+              device) -> torch.Tensor:
+    """An empty 4-bit key/value cache: uint8 [n_pages, n_kv_heads, page_tokens/16, 20*head_dim]
+    (16-token tiles; the layout is in include/mmvq.h)."""
+    kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
+    return torch.zeros((n_pages, n_kv_heads, page_tokens // KV4_TILE, 20 * head_dim),
+                       dtype=torch.uint8, device=device)
+
+
+def _kv4_where(cache, page_table, offsets, lens):
+    """Checks the tensors of a batch: the cache's and the batch's arguments of the C calls."""
+    n_pages, n_kv, tiles, tile_bytes = cache.shape
+    n_seqs, ld = page_table.shape
+    if not (cache.is_cuda and cache.is_contiguous() and cache.dtype == torch.uint8):
+        raise ValueError("cache must be a contiguous CUDA uint8 tensor (kv4_cache)")
+    if tile_bytes % 20:
+        raise ValueError("cache tiles hold 20 * head_dim bytes")
+    for t, n, name in ((page_table, n_seqs * ld, "page_table"), (offsets, n_seqs + 1, "offsets"),
+                       (lens, n_seqs, "lens")):
+        if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.int32 and t.numel() == n):
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} values")
+    return ((cache.data_ptr(), n_pages, tiles * KV4_TILE, n_kv, tile_bytes // 20,
+             page_table.data_ptr(), ld, offsets.data_ptr(), lens.data_ptr(), n_seqs))
+
+
+def _kv4_rows(t, heads, dim, name):
+    """A [n, heads, dim] tensor with unit inner stride: its token and head strides."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
+            (t.stride(2) != 1 and t.numel()) or t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be a CUDA float32, float16 or bfloat16 tensor "
+                         f"[tokens, {heads}, {dim}] with unit inner stride")
+    return t.stride(0), t.stride(1)
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+               offsets: torch.Tensor, lens: torch.Tensor, status: torch.Tensor | None = None,
+               stream=None) -> None:
+    """Quantises keys and values [n, kv heads, head_dim] into the cache: rows
+    offsets[b]..offsets[b+1]-1 are the last tokens of sequence b, whose length with them is
+    lens[b]; position p of it lies in page page_table[b, p // page_tokens].  (mmvq_kv4_append)"""
+    where = _kv4_where(cache, page_table, offsets, lens)
+    n = k.shape[0]
+    ldk, hk = _kv4_rows(k, where[3], where[4], "k")
+    ldv, hv = _kv4_rows(v, where[3], where[4], "v")
+    if v.shape[0] != n or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same tokens and type")
+    _check(lib().mmvq_kv4_append(_DTYPES[k.dtype], k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv,
+                                 *where, n, _ptr(status), _stream(stream)), "mmvq_kv4_append")
+
+
+def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tensor,
+             lens: torch.Tensor, n_tokens: int, dtype: torch.dtype = torch.float32,
+             out: tuple[torch.Tensor, torch.Tensor] | None = None,
+             status: torch.Tensor | None = None, stream=None):
+    """(k, v), each [n_tokens, kv heads, head_dim] of dtype: the cached values of the last
+    offsets[b+1]-offsets[b] of the first lens[b] tokens of each sequence b.  (mmvq_kv4_read)"""
+    where = _kv4_where(cache, page_table, offsets, lens)
+    shape = (n_tokens, where[3], where[4])
+    if out is None:
+        out = (torch.empty(shape, dtype=dtype, device=cache.device),
+               torch.empty(shape, dtype=dtype, device=cache.device))
+    k, v = out
+    for t in out:
+        _dev(t, "out")
+        if t.shape != shape or t.dtype != dtype or dtype not in _DTYPES:
+            raise ValueError(f"out must be two tensors {list(shape)} of {dtype}")
+    _check(lib().mmvq_kv4_read(_DTYPES[dtype], k.data_ptr(), v.data_ptr(), *where, n_tokens,
+                               _ptr(status), _stream(stream)), "mmvq_kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace(head_dim: int, device) -> torch.Tensor:
+    """A zeroed workspace for kv4_attention (one per concurrently running call)."""
+    n = lib().mmvq_kv4_attention_workspace_bytes(head_dim)
+    if n < 0:
+        raise MMVQError(ERR_SHAPE, "mmvq_kv4_attention_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                  offsets: torch.Tensor, lens: torch.Tensor, *, scale: float | None = None,
+                  window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, with_lse: bool = False,
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                  stream=None):
+    """Attention of q [n, heads, head_dim] (1-8 query tokens a sequence, the batch as in
+    kv4_append) over the cache -> y [n, heads, head_dim], or (y, lse [n, heads] fp32) with
+    with_lse or lse.  A query sees the tokens up to its own position; with window > 0 only the
+    last `window` of them and the first `sinks` of the sequence.  scale defaults to
+    head_dim**-0.5; workspace: kv4_attention_workspace.  (mmvq_kv4_attention)"""
+    where = _kv4_where(cache, page_table, offsets, lens)
+    n_kv, dim = where[3], where[4]
+    n, heads = q.shape[0], q.shape[1]
+    ldq, hq = _kv4_rows(q, heads, dim, "q")
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape and type")
+    if lse is None and with_lse:
+        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    elif lse is not None and (lse.shape != (n, heads) or lse.dtype != torch.float32 or
+                              not lse.is_cuda or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous CUDA float32 tensor [tokens, heads]")
+    if workspace is None:
+        workspace = kv4_attention_workspace(dim, q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < \
+            lib().mmvq_kv4_attention_workspace_bytes(dim):
+        raise ValueError("workspace is too small: kv4_attention_workspace(head_dim, device)")
+    _check(lib().mmvq_kv4_attention(_DTYPES[q.dtype], q.data_ptr(), ldq, hq, heads,
+                                    dim ** -0.5 if scale is None else scale, window, sinks,
+                                    out.data_ptr(), _ptr(lse), *where, n, workspace.data_ptr(),
+                                    _ptr(status), _stream(stream)), "mmvq_kv4_attention")
+    return out if lse is None else (out, lse)

@@ -128,8 +128,12 @@ enum mmvq_status {
   MMVQ_ERR_ALIGN = -5,   /* a pointer breaks its alignment rule */
   MMVQ_ERR_ROUTING = -6, /* routing lists rejected (host-side limits) */
   MMVQ_ERR_CUDA = -7,    /* a CUDA launch or attribute call failed */
-  MMVQ_ERR_SCRATCH = -8  /* mmvq_expert_ffn_noalloc: intermediates exceed its fixed scratch */
+  MMVQ_ERR_SCRATCH = -8, /* mmvq_expert_ffn_noalloc: intermediates exceed its fixed scratch */
+  MMVQ_ERR_VALUE = -9    /* mmvq_kv4_append (*status): a non-finite input was clamped */
 };
+
+/* Element types of the plain tensors of the key/value cache calls (GGUF's numbers). */
+enum mmvq_dtype { MMVQ_F32 = 0, MMVQ_F16 = 1, MMVQ_BF16 = 30 };
 
 /* Version of this ABI (major*10000 + minor*100 + patch). */
 MMVQ_API int mmvq_version(void);
@@ -391,6 +395,103 @@ MMVQ_API int mmvq_expert_ffn_shape(int type, int n_experts, int H, int F, int T,
 MMVQ_API int mmvq_rmsnorm_quantize_q8_1(const float* x, const float* w, float eps, int K, int ncols,
                                         int64_t ldx, void* xq, float* y_out,
                                         mmvq_stream_t stream);
+
+/*
+ * The 4-bit paged key/value cache of the attention layers: keys and values
+ * quantised as they are written, read back, and attended to without ever
+ * being expanded in memory (the pages' engine keeps its own in 8 bits, PR
+ * #2746 "End-to-end performance"; they give no format).
+ *
+ * Block: 32 consecutive values of a head's vector, d = fp16((max - min)/15),
+ * z = fp16((max + min)/2) and 4-bit codes c = rint((x - z)/d + 7.5) clamped to
+ * 0..15 (0 where d = 0), fp32 arithmetic; a code stands for z + d*(c - 7.5).
+ * 20 bytes per 32 values.  Inputs are clamped to +-65504 first, and a NaN is
+ * written as 0; a non-finite input sets *status to MMVQ_ERR_VALUE.
+ *
+ * Cache: [n_pages][n_kv_heads][page_tokens/16] tiles of 16 tokens and
+ * 20*head_dim bytes (mmvq_kv4_page_bytes per page, the caller's memory, 16-byte
+ * aligned).  Inside a tile, with nb = head_dim/32, token t of the tile and
+ * word(j, lane) = 512*(j/4) + 16*lane + 4*(j%4), D = head_dim:
+ *   key codes    [0, 8D):    word(nb*(t/8) + b, 4*(t%8) + u) = values 32b + 8u
+ *                            .. +7 of token t, value i in bits 4i .. 4i+3
+ *   value codes  [8D, 16D):  word(nb*(t/8) + b, 4*g + (t%8)/2) = values 32b +
+ *                            4g .. +3 of token t (even: low half, odd: high),
+ *                            value i in bits 4i .. 4i+3 of the half
+ *   key d, z     [16D, 17D), [17D, 18D): fp16 [t][b]
+ *   value d, z   [18D, 19D), [19D, 20D): fp16 [(t%8)/2][t/8][b][t%2]
+ * No two tokens share a byte.
+ *
+ * Batch: rows token_offsets[b] .. token_offsets[b+1]-1 (int32 [n_seqs+1],
+ * nondecreasing) of the call's tensors are the LAST rows of sequence b, whose
+ * length, these rows included, is seq_lens[b]: row r stands at position
+ * seq_lens[b] - (token_offsets[b+1] - r).  So one set of arrays serves the
+ * append and the attention of a step, and any range of tokens is read back by
+ * the length at its end.  Rows outside every sequence are ignored.  Position
+ * p of sequence b lies in page page_table[b*ld_table + p/page_tokens].
+ * Device-side checks: a page id outside [0, n_pages) or a position past the
+ * table sets *status (optional) to MMVQ_ERR_ROUTING; the token is not written,
+ * reads as zeros, and is not attended to.  Rows at negative positions (a
+ * length below the row count) are not written, read as zeros and attend to
+ * nothing.
+ * Limits: head_dim 64, 128 or 256; page_tokens a multiple of 16 up to 65536;
+ * 1 <= n_kv_heads <= 1024; 1 <= n_seqs <= 4096; ld_table*page_tokens < 2^31;
+ * n_tokens >= 0 rows in all (0: nothing happens).  dtype: mmvq_dtype of the
+ * plain tensors (else MMVQ_ERR_TYPE), each aligned to its element.
+ */
+MMVQ_API int64_t mmvq_kv4_page_bytes(int n_kv_heads, int head_dim, int page_tokens);
+
+/* Writes keys and values ([n_tokens][n_kv_heads][head_dim], ldk/ldv elements
+ * from token to token, hk/hv from head to head, >= 0, the values of a head
+ * contiguous) to the cache.  Only the bytes of the written tokens change. */
+MMVQ_API int mmvq_kv4_append(int dtype, const void* k, int64_t ldk, int64_t hk, const void* v,
+                             int64_t ldv, int64_t hv, void* cache, int64_t n_pages,
+                             int page_tokens, int n_kv_heads, int head_dim,
+                             const int32_t* page_table, int64_t ld_table,
+                             const int32_t* token_offsets, const int32_t* seq_lens, int n_seqs,
+                             int n_tokens, int32_t* status, mmvq_stream_t stream);
+
+/* Reads tokens back: k and v, contiguous [n_tokens][n_kv_heads][head_dim] of
+ * dtype, 16-byte aligned, get z + d*(c - 7.5) in fp32, rounded once to dtype. */
+MMVQ_API int mmvq_kv4_read(int dtype, void* k, void* v, const void* cache, int64_t n_pages,
+                           int page_tokens, int n_kv_heads, int head_dim,
+                           const int32_t* page_table, int64_t ld_table,
+                           const int32_t* token_offsets, const int32_t* seq_lens, int n_seqs,
+                           int n_tokens, int32_t* status, mmvq_stream_t stream);
+
+/*
+ * Attention of the batch's rows, 1 to 8 query tokens a sequence (PR #2207's 1
+ * to 8 columns: a decode step or a verify window), over the cache.  q:
+ * [n_tokens][n_heads][head_dim], ldq elements from token to token and hq from
+ * head to head; query head j reads kv head j / (n_heads/n_kv_heads).  A query
+ * at position p sees the tokens j <= p; with window > 0 only those with
+ * j > p - window or j < sinks (the first tokens that stay visible), and pages
+ * that no query sees are not read, so their table entries need not be valid.
+ * y ([n_tokens][n_heads][head_dim] of dtype, contiguous) = sum softmax(scale *
+ * q.k) v over the seen tokens, zeros where there are none; lse (may be NULL):
+ * fp32 [n_tokens][n_heads], log(sum(exp(scale * q.k))), -inf where there are
+ * none.  Scores, the softmax and the sums are fp32; for fp32 q the products
+ * keep about 22 bits of q and of the probabilities.
+ * Arithmetic on masked places never reaches y: what lies in the cache past a
+ * sequence's length may hold anything.
+ * workspace: mmvq_kv4_attention_workspace_bytes(head_dim) bytes, 256-byte
+ * aligned, zeroed once before the first call and left ready by every call;
+ * calls that may run at the same time need separate ones.
+ * Sequences of more than 8 rows set *status to MMVQ_ERR_NCOLS, their rows of y
+ * and lse are not written; n_tokens > 8*n_seqs is rejected (MMVQ_ERR_NCOLS).
+ * n_heads: a multiple of n_kv_heads, at most 128 times as many.  y 16-byte
+ * aligned.
+ */
+MMVQ_API int mmvq_kv4_attention(int dtype, const void* q, int64_t ldq, int64_t hq, int n_heads,
+                                float scale, int window, int sinks, void* y, float* lse,
+                                const void* cache, int64_t n_pages, int page_tokens,
+                                int n_kv_heads, int head_dim, const int32_t* page_table,
+                                int64_t ld_table, const int32_t* token_offsets,
+                                const int32_t* seq_lens, int n_seqs, int n_tokens,
+                                void* workspace, int32_t* status, mmvq_stream_t stream);
+
+/* Bytes of the workspace of mmvq_kv4_attention, whatever the batch; -1 on a
+ * bad head_dim.  Host-only. */
+MMVQ_API int64_t mmvq_kv4_attention_workspace_bytes(int head_dim);
 
 /* Bytes of the planar form of a rows x K matrix of `type` (MMVQ_Q6_K,
  * MMVQ_Q5_K or MMVQ_Q4_K); -1 on a bad type or shape. */
