@@ -1,102 +1,732 @@
-// Attention of 1-8 query tokens a sequence over the 4-bit cache: a CTA per
-// query row, a warp per cached token, running maximum and sum in fp32.
+// Attention of 1-8 query tokens a sequence over the 4-bit cache.
+//
+// Mathematics.  A warp takes tiles of 16 cached tokens.  Scores come as
+// S^T[tokens x rows] = K Q^T from m16n8k16 f16 products whose A operand is the
+// tile's codes: a code c masked out of its word stands, as the bits of an
+// fp16, for c * 2^-24 (low nibble of a byte) or c * 2^-20 (high nibble), exact
+// subnormals, so a key costs no conversion at all; the rows of Q are scaled by
+// a power of two each, and by 16 more where they meet low nibbles.  Per block
+// of 32 the accumulator starts at -7.5 sum(q) and is multiplied by the block's
+// d in fp32; sum(z sum(q)) over the blocks is one more product, sum(q) in two
+// fp16 parts.  Probabilities p = 2^(s - m + 6) use a reference m that is only
+// moved when a score exceeds it by 8 (in log2 units): the result does not
+// depend on m, and most tiles skip the maximum across lanes and the rescaling.
+// O^T[values x rows] += V^T P': A = the codes less 7.5 (one fp16 operation on
+// the subnormals, exact), B = p d per block of 32 (d scaled by a power of two
+// 2^F that keeps it in fp16's middle), and sum(p z) one more product.
+//
+// Precision.  fp32 q enters as two fp16 parts (22 bits), and for fp32 and fp16
+// the products p d do too; bf16 keeps 11 bits of p d, finer than its own 8.
+// Every sum is fp32 (in the tensor core or outside).
 #include "kv4.cuh"
 #include "kv4_attention.cuh"
 
 namespace mmvq {
 namespace {
 
-template <int D, typename T>
-__global__ void __launch_bounds__(128) kv4_attention_kernel(Kv4Batch a, Kv4Attention p) {
-  constexpr int nb = D / 32, kOwn = D / 32;  // values of a lane: lane + 32 i
-  __shared__ float acc_s[4][D], max_s[4], sum_s[4];
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x, hq = blockIdx.y;
-  const int h = hq / (p.n_heads / a.n_kv_heads);
-  int b, pos;
-  if (!kv4_place(a, r, lane, b, pos)) return;
-  const int first = __ldg(a.offsets + b), end = __ldg(a.offsets + b + 1);
-  if (end - first > kKv4MaxNew) {
-    if (threadIdx.x == 0) kv4_set_status(a.status, MMVQ_ERR_NCOLS);
-    return;
-  }
-  float q[kOwn], o[kOwn], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    q[i] = kv4_load(static_cast<const T*>(p.q) + r * p.ldq + hq * p.hq + lane + 32 * i);
-    o[i] = 0.0f;
-  }
-  const int64_t hs = kv4_head_stride(a, kv4_tile_bytes(D));
-  for (int64_t key = warp; key <= pos; key += 4) {
-    if (p.window > 0 && key <= (int64_t)pos - p.window && key >= p.sinks) continue;
-    const uint8_t* tile = kv4_tile(a, kv4_tile_bytes(D), b, (int)(key / kKv4Tile));
-    if (!tile) {
-      if (lane == 0) kv4_set_status(a.status, MMVQ_ERR_ROUTING);
-      continue;
-    }
-    tile += h * hs;
-    const int t = (int)(key % kKv4Tile);
-    float s = 0.0f, v[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const int j = nb * (t >> 3) + i;
-      const uint8_t kc = tile[kv4_word(j, 4 * (t & 7) + lane / 8) + (lane % 8) / 2];
-      const uint8_t vc = tile[8 * D + kv4_word(j, 4 * (lane / 4) + (t & 7) / 2) + 2 * (t & 1) + lane % 4 / 2];
-      const uint16_t* ks = reinterpret_cast<const uint16_t*>(tile + kv4_key_scale(D, t, i));
-      const uint16_t* vs = reinterpret_cast<const uint16_t*>(tile + kv4_value_scale(D, t, i));
-      const int sh = 4 * (lane & 1);
-      s = fmaf(q[i], kv4_value((kc >> sh) & 15u, half_bits_to_float(ks[0]), half_bits_to_float(ks[D / 2])), s);
-      v[i] = kv4_value((vc >> sh) & 15u, half_bits_to_float(vs[0]), half_bits_to_float(vs[D / 2]));
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale;
-    const float m2 = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.0f : expf(m - m2), e = s == -INFINITY ? 0.0f : expf(s - m2);
-    l = l * f + e;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) o[i] = o[i] * f + e * v[i];
-    m = m2;
-  }
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) acc_s[warp][lane + 32 * i] = o[i];
-  if (lane == 0) max_s[warp] = m, sum_s[warp] = l;
-  __syncthreads();
-  float top = -INFINITY, total = 0.0f;
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, max_s[w]);
-  float f[4];
-  for (int w = 0; w < 4; ++w) {
-    f[w] = max_s[w] == -INFINITY ? 0.0f : expf(max_s[w] - top);
-    total += f[w] * sum_s[w];
-  }
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float y = 0.0f;
-    for (int w = 0; w < 4; ++w) y += f[w] * acc_s[w][d];
-    kv4_store(static_cast<T*>(p.y) + ((int64_t)r * p.n_heads + hq) * D + d,
-              total == 0.0f ? 0.0f : y / total);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(int64_t)r * p.n_heads + hq] = total == 0.0f ? -INFINITY : top + logf(total);
+constexpr int kStages = 4;
+constexpr float kLazy = 8.0f;    // slack of the reference, log2 units
+constexpr float kBoost = 6.0f;   // p is at most 2^(kLazy + kBoost) = 2^14, below fp16's largest
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <typename T>
-int attention_typed(const Kv4Batch& a, const Kv4Attention& p, int D, cudaStream_t stream) {
-  const dim3 grid(a.n_tokens, p.n_heads), block(128);
-  if (D == 64) return launch_pdl(kv4_attention_kernel<64, T>, grid, block, 0, stream, a, p);
-  if (D == 128) return launch_pdl(kv4_attention_kernel<128, T>, grid, block, 0, stream, a, p);
-  return launch_pdl(kv4_attention_kernel<256, T>, grid, block, 0, stream, a, p);
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+
+// Transposes an 8 x 8 matrix of fp16 held two of a row a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  return u32(__hmul2_rn(h2(a), h2(b)));
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  return u32(__hfma2(h2(a), h2(b), h2(c)));
+}
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+  return u32(__hadd2_rn(h2(a), h2(b)));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 2^e as an fp16 pair, -15 <= e <= 15 (2^-15 is a subnormal).
+__device__ __forceinline__ uint32_t pow2_pair(int e) {
+  const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : 0x0200u;
+  return h | (h << 16);
+}
+
+template <int D, int NT, bool QS>
+struct Smem {
+  static constexpr int nb = D / 32;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kQ = nb * 2 * NT * 32 * (QS ? 16 : 8);
+  static constexpr int kRing = kStages * kv4_tile_bytes(D);  // of a warp
+  uint8_t ring[kKv4Warps][kRing];   // tiles; afterwards the warps' results [row][D]
+  uint8_t q[kQ];                    // [block][half][row tile][lane]: fp16 parts, b0 b1 (b0 b1)
+  float q_start[nb][kRows];         // -7.5 sum(q) of a block, in the accumulators' units
+  __half q_sum[kRows][2][nb];       // sum(q) of a block, in two parts
+  float row_factor[kRows];
+  int row_pos[kRows];
+  float ref[kKv4Warps][kRows], sum[kKv4Warps][kRows];
+  int64_t before[kKv4Warps * 32];   // units before each thread's sequences
+  int64_t warp_units[kKv4Warps];
+  uint32_t present[kKv4Warps][kStages];
+  int last;
+  static_assert(kRing >= kRows * D * 4, "a warp's results fit its ring");
+};
+
+// The query rows of a block into q, q_start, q_sum, row_factor and row_pos.
+template <int D, int NT, bool QS, typename T>
+__device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attention& p,
+                                             Smem<D, NT, QS>& sm, const Kv4Seq& s, int head,
+                                             int row0, int tid) {
+  constexpr int kPer = 16 / NT, kOwn = D / kPer;  // threads a row, values a thread
+  const int row = tid / kPer, sub = tid % kPer;
+  const int group = p.n_heads / a.n_kv_heads;
+  const int r = row0 + row;
+  const bool on = r < s.n_new * group;
+  const int t = on ? r / group : 0;
+  float q[kOwn], top = 0.0f;
+  if (on) {
+    const T* src = static_cast<const T*>(p.q) + (int64_t)(s.first + t) * p.ldq +
+                   (int64_t)(head * group + r - t * group) * p.hq + sub * kOwn;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) q[i] = kv4_load(src + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) q[i] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) top = fmaxf(top, fabsf(q[i]));
+#pragma unroll
+  for (int o = 1; o < kPer; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // largest |q| into [2^9, 2^10): with the factor 16, sums of 32 stay below fp16's largest
+  int e = top > 0.0f && top < INFINITY ? 9 - ilogbf(top) : 0;
+  e = min(e, 126);
+  const float f = ldexpf(1.0f, e);
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) q[i] *= f;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int d = sub * kOwn + i, b = d / 32, u = d % 32 / 8, n = d % 8;
+    const float x = (n & 1) ? q[i] : 16.0f * q[i];
+    const __half hi = __float2half_rn(x);
+    uint8_t* at = sm.q + (size_t)(((b * 2 + (n & 3) / 2) * NT + row / 8) * 32 + (row % 8) * 4 + u) * (QS ? 16 : 8) +
+                  (n & 1) * 4 + (n >> 2) * 2;
+    *reinterpret_cast<__half*>(at) = hi;
+    if (QS) *reinterpret_cast<__half*>(at + 8) = __float2half_rn(x - __half2float(hi));
+  }
+  constexpr int kBlk = kOwn >= 32 ? 1 : 32 / kOwn;  // threads a block
+#pragma unroll
+  for (int b0 = 0; b0 < (kOwn >= 32 ? kOwn / 32 : 1); ++b0) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (kOwn >= 32 ? 32 : kOwn); ++i) sum += q[32 * b0 + i];
+#pragma unroll
+    for (int o = 1; o < kBlk; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int b = sub * kOwn / 32 + b0;
+    if (sub % kBlk == 0) {
+      const __half hi = __float2half_rn(sum);
+      sm.q_sum[row][0][b] = hi;
+      sm.q_sum[row][1][b] = __float2half_rn(sum - __half2float(hi));
+      sm.q_start[b][row] = -7.5f * 0x1p-20f * sum;
+    }
+  }
+  if (sub == 0) {
+    sm.row_factor[row] = ldexpf(p.scale * 1.4426950408889634f, 20 - e);
+    sm.row_pos[row] = on ? s.len - s.n_new + t : -1;
+  }
+}
+
+template <int D, int NT, bool QS, bool PS, typename T>
+__global__ void __launch_bounds__(kKv4Warps * 32)
+    kv4_attention_kernel(const Kv4Batch a, const Kv4Attention p) {
+  using S = Smem<D, NT, QS>;
+  constexpr int nb = D / 32, kRows = 8 * NT, kBytes = kv4_tile_bytes(D);
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  grid_dependency_wait();
+
+  // ---- the batch's units, and this CTA's share of them
+  const int chunk = (a.n_seqs + kKv4Warps * 32 - 1) / (kKv4Warps * 32);
+  int error = 0;
+  int64_t mine = 0;
+  for (int b = tid * chunk; b < min(a.n_seqs, (tid + 1) * chunk); ++b)
+    mine += kv4_seq(a, p, kRows, b, &error).units;
+  if (error && blockIdx.x == 0) kv4_set_status(a.status, error);
+  int64_t up_to = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, up_to, o);
+    if (lane >= o) up_to += x;
+  }
+  if (lane == 31) sm.warp_units[warp] = up_to;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kKv4Warps; ++w) {
+    if (w < warp) up_to += sm.warp_units[w];
+    total += sm.warp_units[w];
+  }
+  sm.before[tid] = up_to - mine;
+  __syncthreads();
+  const int n_ctas = (int)min((int64_t)gridDim.x, (total + kKv4MinUnits - 1) / kKv4MinUnits);
+  const int cta = blockIdx.x;
+  if (cta >= n_ctas) return;
+  const int64_t lo = total * cta / n_ctas, hi = total * (cta + 1) / n_ctas;
+  const int group = p.n_heads / a.n_kv_heads;
+  const int per_page = a.page_tokens / kKv4Tile;
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kKv4CounterBytes);
+  uint32_t* counters = static_cast<uint32_t*>(p.workspace);
+
+  for (int64_t unit = lo; unit < hi;) {
+    // ---- the item of this unit
+    int th = 0;
+#pragma unroll
+    for (int o = kKv4Warps * 16; o > 0; o >>= 1)
+      if (sm.before[th + o] <= unit) th += o;
+    int b = th * chunk;
+    int64_t at = sm.before[th];
+    Kv4Seq s = kv4_seq(a, p, kRows, b, &error);
+    while (at + s.units <= unit) {
+      at += s.units;
+      s = kv4_seq(a, p, kRows, ++b, &error);
+    }
+    const int item = (int)((unit - at) / s.tiles);
+    const int64_t item0 = at + (int64_t)item * s.tiles, item1 = item0 + s.tiles;
+    const int tile0 = (int)(unit - item0), tile1 = (int)(min(hi, item1) - item0);
+    const int head = item / s.blocks, row0 = (item - head * s.blocks) * kRows;
+    const int n_rows = min(kRows, s.n_new * group - row0);
+
+    __syncthreads();  // the block before is done with the shared memory
+    load_queries<D, NT, QS, T>(a, p, sm, s, head, row0, tid);
+    __syncthreads();
+
+    // ---- what a lane keeps of the queries: columns 2c, 2c + 1 of each row tile
+    float fac[NT][2];
+    int pos[NT][2];
+    uint32_t qz[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fac[n][e] = sm.row_factor[8 * n + 2 * c + e];
+        pos[n][e] = sm.row_pos[8 * n + 2 * c + e];
+      }
+      const uint32_t* qs = reinterpret_cast<const uint32_t*>(sm.q_sum[8 * n + g]);
+      if (nb == 8) {
+        qz[n][0] = qs[c];
+        qz[n][1] = qs[nb / 2 + c];
+      } else {  // k positions: the blocks' first parts, then their second, then nothing
+        qz[n][0] = c < nb ? qs[c] : 0u;
+        qz[n][1] = 0u;
+      }
+    }
+    float o[NT][2 * nb][4], oz[NT][4], m[NT][2], l[NT][2];
+    int F = 15;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2 * nb; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oz[n][e] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+
+    // ---- tiles tile0 + warp, + 4, ... through the warp's ring
+    const uint8_t* head_base = a.cache + (int64_t)head * per_page * kBytes;
+    const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kBytes;
+    const int32_t* table = a.page_table + (int64_t)b * a.ld_table;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
+    const int pos_lo = s.len - s.n_new;  // of the sequence's rows
+    auto tile_of = [&](int i) { return i + (i >= s.sink_tiles ? s.skip : 0); };
+    auto fetch = [&](int i, int stage) {
+      if (i < tile1) {
+        const int tile = tile_of(i);
+        const int pi = (int)(((uint64_t)(uint32_t)tile * p.page_mul) >> p.page_shift);
+        const int64_t page = pi < a.ld_table && tile * (int64_t)kKv4Tile < s.len ? __ldg(table + pi) : -1;
+        const bool present = page >= 0 && page < a.n_pages;
+        if (lane == 0) sm.present[warp][stage] = present;
+        if (present) {
+          const uint8_t* src = head_base + page * page_bytes + (int64_t)(tile - pi * per_page) * kBytes + lane * 16;
+          const uint32_t dst = ring + stage * kBytes + lane * 16;
+#pragma unroll
+          for (int k = 0; k < (kBytes + 511) / 512; ++k)
+            if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes) cp_async16(dst + k * 512, src + k * 512);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(tile0 + warp + k * kKv4Warps, k);
+    int stage = 0;
+    for (int i = tile0 + warp; i < tile1; i += kKv4Warps) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      fetch(i + (kStages - 1) * kKv4Warps, (stage + kStages - 1) % kStages);
+      const uint8_t* tp = sm.ring[warp] + stage * kBytes;
+      const bool present = sm.present[warp][stage];
+      stage = (stage + 1) % kStages;
+      const int key0 = tile_of(i) * kKv4Tile;
+      if (!present) {
+        if (lane == 0 && key0 < s.len) kv4_set_status(a.status, MMVQ_ERR_ROUTING);
+        continue;
+      }
+
+      // ---- scores
+      uint32_t kw[2 * nb], kd[2][nb / 2];
+#pragma unroll
+      for (int k = 0; k < nb / 2; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(tp + 512 * k + 16 * lane);
+        kw[4 * k] = v.x, kw[4 * k + 1] = v.y, kw[4 * k + 2] = v.z, kw[4 * k + 3] = v.w;
+      }
+      uint32_t kz[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int k = 0; k < nb / 2; ++k)
+          kd[h][k] = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g + 8 * h, 0) + 4 * k);
+        kz[h] = *reinterpret_cast<const uint32_t*>(tp + D + kv4_key_scale(D, g + 8 * h, 0) +
+                                                   4 * (nb == 8 ? c : nb == 4 ? c & 1 : 0));
+      }
+      float x[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (nb == 8) mma16(z, kz[0], kz[1], kz[0], kz[1], qz[n][0], qz[n][1]);
+        else mma8(z, kz[0], kz[1], qz[n][0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = z[e] * 0x1p-20f;
+      }
+#pragma unroll
+      for (int b2 = 0; b2 < nb; ++b2) {
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 st = *reinterpret_cast<const float2*>(&sm.q_start[b2][8 * n + 2 * c]);
+          acc[n][0] = acc[n][2] = st.x;
+          acc[n][1] = acc[n][3] = st.y;
+        }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t w0 = kw[b2] >> (8 * hh), w1 = kw[nb + b2] >> (8 * hh);
+          const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u,
+                         a3 = w1 & 0x00f000f0u;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint8_t* qp = sm.q + (size_t)(((b2 * 2 + hh) * NT + n) * 32 + lane) * (QS ? 16 : 8);
+            if (QS) {
+              const uint4 q = *reinterpret_cast<const uint4*>(qp);
+              mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
+              mma16(acc[n], a0, a1, a2, a3, q.z, q.w);
+            } else {
+              const uint2 q = *reinterpret_cast<const uint2*>(qp);
+              mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
+            }
+          }
+        }
+        const float d0 = __half2float(((b2 & 1) ? __high2half : __low2half)(h2(kd[0][b2 / 2])));
+        const float d1 = __half2float(((b2 & 1) ? __high2half : __low2half)(h2(kd[1][b2 / 2])));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          x[n][0] = fmaf(d0, acc[n][0], x[n][0]);
+          x[n][1] = fmaf(d0, acc[n][1], x[n][1]);
+          x[n][2] = fmaf(d1, acc[n][2], x[n][2]);
+          x[n][3] = fmaf(d1, acc[n][3], x[n][3]);
+        }
+      }
+
+      // ---- values: steps of the lane's token pairs (2c, 2c + 1) + 8 h, midpoints of block g
+      uint32_t vd[2 * nb], vz[2];
+#pragma unroll
+      for (int k = 0; k < nb / 2; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(tp + 18 * D + 8 * nb * c + 16 * k);
+        vd[4 * k] = v.x, vd[4 * k + 1] = v.y, vd[4 * k + 2] = v.z, vd[4 * k + 3] = v.w;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        vz[h] = g < nb ? *reinterpret_cast<const uint32_t*>(tp + 19 * D + 8 * nb * c + 4 * (h * nb + g)) : 0u;
+
+      // ---- masks: a tile that every row sees in full needs none
+      const bool all = key0 + kKv4Tile - 1 <= pos_lo &&
+                       (p.window == 0 || key0 > (int64_t)s.len - 1 - p.window || key0 + kKv4Tile <= p.sinks);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] *= fac[n][e & 1];
+      if (!all) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + g + 8 * (e >> 1), q = pos[n][e & 1];
+            const bool see = key <= q && (p.window == 0 || key > (int64_t)q - p.window || key < p.sinks);
+            if (!see) x[n][e] = -INFINITY;
+          }
+        // values that no row sees may be anything: their steps and midpoints become zero
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + 8 * h + 2 * c + e;
+            if (key < s.len && (p.window == 0 || key > (int64_t)pos_lo - p.window || key < p.sinks))
+              keep |= 0xffffu << (16 * e);
+          }
+#pragma unroll
+          for (int k = 0; k < nb; ++k) vd[h * nb + k] &= keep;
+          vz[h] &= keep;
+        }
+      }
+      uint32_t ds[2 * nb], large = 0;
+      const uint32_t f2 = pow2_pair(F);
+#pragma unroll
+      for (int k = 0; k < 2 * nb; ++k) {
+        ds[k] = mul2(vd[k], f2);
+        large |= ds[k];
+      }
+      bool move = (large & 0x40004000u) != 0;  // a scaled step of 2 or more
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + kLazy;
+      if (__any_sync(0xffffffffu, move)) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 2 * nb; ++k) top = max(top, max(vd[k] & 0xffffu, vd[k] >> 16));
+        top = __reduce_max_sync(0xffffffffu, top);
+        float fo = 1.0f;
+        const float d = half_bits_to_float((uint16_t)top);
+        if (d > 0.0f && ldexpf(d, F) >= 2.0f) {
+          const int F2 = max(-15, min(15, -2 - ilogbf(d)));
+          fo = ldexpf(1.0f, F2 - F);
+          F = F2;
+          const uint32_t g2 = pow2_pair(F);
+#pragma unroll
+          for (int k = 0; k < 2 * nb; ++k) ds[k] = mul2(vd[k], g2);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float fr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = fmaxf(x[n][e], x[n][e + 2]);
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            t = fmaxf(t, m[n][e]);
+            fr[e] = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - t);
+            m[n][e] = t;
+            l[n][e] *= fr[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            oz[n][e] *= fr[e & 1];
+#pragma unroll
+            for (int k = 0; k < 2 * nb; ++k) o[n][k][e] *= fr[e & 1] * fo;
+          }
+        }
+      }
+
+      // ---- probabilities, turned into the B operand
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1] - kBoost;
+          pr[e] = ex2(x[n][e] - ref);
+        }
+        l[n][0] += pr[0] + pr[2];
+        l[n][1] += pr[1] + pr[3];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __half2 hi2 = __floats2half2_rn(pr[2 * h], pr[2 * h + 1]);
+          ph[n][h] = transpose8(u32(hi2));
+          if (PS) {
+            const float2 back = __half22float2(hi2);
+            pl[n][h] = transpose8(u32(__floats2half2_rn(pr[2 * h] - back.x, pr[2 * h + 1] - back.y)));
+          }
+        }
+        mma16(oz[n], vz[0], 0u, vz[1], 0u, ph[n][0], ph[n][1]);
+        if (PS) mma16(oz[n], vz[0], 0u, vz[1], 0u, pl[n][0], pl[n][1]);
+      }
+      // ---- weighted values
+      uint32_t vw[2 * nb];
+#pragma unroll
+      for (int k = 0; k < nb / 2; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(tp + 8 * D + 512 * k + 16 * lane);
+        vw[4 * k] = v.x, vw[4 * k + 1] = v.y, vw[4 * k + 2] = v.z, vw[4 * k + 3] = v.w;
+      }
+#pragma unroll
+      for (int b2 = 0; b2 < nb; ++b2) {
+        uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t d = ds[h * nb + b2];
+            bh[n][h] = mul2(ph[n][h], d);
+            if (PS) bl[n][h] = fma2(pl[n][h], d, fma2(ph[n][h], d, bh[n][h] ^ 0x80008000u));
+          }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
+          // (2 c - 15) 2^-24 and (16 c - 120) 2^-24: the low and the high nibbles less 7.5
+          const uint32_t a0 = fma2(w0 & 0x000f000fu, 0x40004000u, 0x800f800fu);
+          const uint32_t a1 = add2(w0 & 0x00f000f0u, 0x80788078u);
+          const uint32_t a2 = fma2(w1 & 0x000f000fu, 0x40004000u, 0x800f800fu);
+          const uint32_t a3 = add2(w1 & 0x00f000f0u, 0x80788078u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bh[n][0], bh[n][1]);
+            if (PS) mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bl[n][0], bl[n][1]);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // ---- the warp's result, in its ring: [row][D], in units of 2^(ref)
+    float* res = reinterpret_cast<float*>(sm.ring[warp]);
+    const float u0 = ldexpf(1.0f, 23 - F), u1 = ldexpf(1.0f, 20 - F);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = l[n][e];
+        t += __shfl_xor_sync(0xffffffffu, t, 4);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        const int row = 8 * n + 2 * c + e;
+        if (g == 0) {
+          sm.ref[warp][row] = m[n][e] - kBoost;
+          sm.sum[warp][row] = t;
+        }
+#pragma unroll
+        for (int b2 = 0; b2 < nb; ++b2) {
+          const float z = __shfl_sync(0xffffffffu, oz[n][e], 4 * b2 + c);
+          float4 v;
+          v.x = fmaf(o[n][2 * b2][e], u0, z);
+          v.y = fmaf(o[n][2 * b2][e + 2], u1, z);
+          v.z = fmaf(o[n][2 * b2 + 1][e], u0, z);
+          v.w = fmaf(o[n][2 * b2 + 1][e + 2], u1, z);
+          *reinterpret_cast<float4*>(res + row * D + 32 * b2 + 4 * g) = v;
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- the CTA's result: to the outputs, or to a slot of the workspace
+    auto store_row = [&](int row, int d4, float4 v, float ref, float sum) {
+      const int r = row0 + row, t = r / group;
+      const int64_t out = (int64_t)(s.first + t) * p.n_heads + head * group + (r - t * group);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* y = static_cast<T*>(p.y) + out * D + 4 * d4;
+      kv4_store(y, v.x * inv);
+      kv4_store(y + 1, v.y * inv);
+      kv4_store(y + 2, v.z * inv);
+      kv4_store(y + 3, v.w * inv);
+      if (p.lse && d4 == 0)
+        p.lse[out] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+    };
+    // the CTA that has unit u: the largest i with total * i / n_ctas <= u
+    auto cta_of = [&](int64_t u) { return (int)(((u + 1) * n_ctas - 1) / total); };
+    const int first = cta_of(item0), last = cta_of(item1 - 1), parts = last - first + 1;
+    // CTA i's part of this item: the second slot where CTA i has earlier items, else the first
+    auto slot_of = [&](int i) {
+      return slots + (2 * (int64_t)i + (total * i / n_ctas < item0 ? 1 : 0)) * kv4_slot_floats(D);
+    };
+    float* slot = parts > 1 ? slot_of(cta) : nullptr;
+    for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Warps * 32) {
+      const int row = idx / (D / 4), d4 = idx - row * (D / 4);
+      float ref = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKv4Warps; ++w) ref = fmaxf(ref, sm.ref[w][row]);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kKv4Warps; ++w) {
+        const float f = sm.ref[w][row] == -INFINITY ? (sm.sum[w][row] == 0.0f ? 0.0f : 1.0f) : ex2(sm.ref[w][row] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + row * D + 4 * d4);
+        sum = fmaf(f, sm.sum[w][row], sum);
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+      }
+      if (parts == 1) {
+        store_row(row, d4, v, ref, sum);
+      } else {
+        *reinterpret_cast<float4*>(slot + row * D + 4 * d4) = v;
+        if (d4 == 0) {
+          slot[kRows * D + 2 * row] = ref;
+          slot[kRows * D + 2 * row + 1] = sum;
+        }
+      }
+    }
+
+    // ---- joining the parts of a split item: groups of about sqrt(parts) by the last CTA of a group to
+    // arrive, then the groups by the last group's; always added in the order of the CTAs
+    if (parts > 1) {
+      auto arrive = [&](uint32_t* counter, int n) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          const bool is_last = atomicAdd(counter, 1u) == (uint32_t)n - 1u;
+          if (is_last) *counter = 0u;
+          sm.last = is_last;
+        }
+        __syncthreads();
+        __threadfence();
+        return sm.last != 0;
+      };
+      auto join = [&](int from, int step, int n, bool final) {
+        for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Warps * 32) {
+          const int row = idx / (D / 4), d4 = idx - row * (D / 4);
+          float ref = -INFINITY, sum = 0.0f;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int k = 0; k < n; ++k) {
+            const float* sl = slot_of(from + k * step);
+            const float2 rs = __ldcg(reinterpret_cast<const float2*>(sl + kRows * D + 2 * row));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(sl + row * D + 4 * d4));
+            const float top = fmaxf(ref, rs.x);
+            const float fa = ref == -INFINITY ? 0.0f : ex2(ref - top);
+            const float fb = rs.x == -INFINITY ? (rs.y == 0.0f ? 0.0f : 1.0f) : ex2(rs.x - top);
+            ref = top;
+            sum = fmaf(fb, rs.y, sum * fa);
+            v.x = fmaf(fb, x.x, v.x * fa);
+            v.y = fmaf(fb, x.y, v.y * fa);
+            v.z = fmaf(fb, x.z, v.z * fa);
+            v.w = fmaf(fb, x.w, v.w * fa);
+          }
+          if (final) {
+            store_row(row, d4, v, ref, sum);
+          } else {
+            float* sl = slot_of(from);
+            *reinterpret_cast<float4*>(sl + row * D + 4 * d4) = v;
+            if (d4 == 0) {  // written after every thread of the row has read it: see below
+              sm.ref[0][row] = ref;
+              sm.sum[0][row] = sum;
+            }
+          }
+        }
+        if (!final) {
+          __syncthreads();
+          if (tid < n_rows) {
+            float* sl = slot_of(from) + kRows * D + 2 * tid;
+            sl[0] = sm.ref[0][tid];
+            sl[1] = sm.sum[0][tid];
+          }
+        }
+      };
+      int per = 1;
+      while (per * per < parts) ++per;
+      if (parts <= 12) per = parts;
+      const int grp = (cta - first) / per, from = first + grp * per;
+      const int n_groups = (parts + per - 1) / per;
+      if (arrive(counters + 2 * from + (grp == 0 ? 1 : 0), min(per, last + 1 - from))) {
+        join(from, 1, min(per, last + 1 - from), n_groups == 1);
+        if (n_groups > 1 && arrive(counters + 2 * kKv4MaxCtas + first, n_groups)) join(first, per, n_groups, true);
+      }
+    }
+    unit = item0 + tile1;
+  }
+}
+
+template <int D, int NT, bool QS, bool PS, typename T>
+int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
+  auto kern = kv4_attention_kernel<D, NT, QS, PS, T>;
+  constexpr int kSmem = (int)sizeof(Smem<D, NT, QS>);
+  static int per_device[64];  // CTAs of a full launch, by device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MMVQ_ERR_CUDA;
+  int ctas = __atomic_load_n(&per_device[dev], __ATOMIC_ACQUIRE);
+  if (ctas == 0) {
+    int sms = 0, per_sm = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kKv4Warps * 32, kSmem) != cudaSuccess ||
+        per_sm < 1)
+      return MMVQ_ERR_CUDA;
+    ctas = min(sms * per_sm, kKv4MaxCtas);
+    __atomic_store_n(&per_device[dev], ctas, __ATOMIC_RELEASE);
+  }
+  // no more CTAs than the longest sequences that the table can hold would use
+  const int rows = p.n_heads / a.n_kv_heads * kKv4MaxNew;
+  const int64_t units = (int64_t)a.n_seqs * a.n_kv_heads * ((rows + 8 * NT - 1) / (8 * NT)) *
+                        (a.ld_table * (a.page_tokens / kKv4Tile));
+  const int64_t most = (units + kKv4MinUnits - 1) / kKv4MinUnits;
+  const int grid = (int)(most < ctas ? most : ctas);
+  return launch_pdl(kern, dim3(grid), dim3(kKv4Warps * 32), kSmem, stream, a, p);
+}
+
+template <int D, bool QS, bool PS, typename T>
+int launch_rows(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
+  // rows that share a kv head, if the sequences have equally many new tokens
+  const int rows = p.n_heads / a.n_kv_heads * ((a.n_tokens + a.n_seqs - 1) / a.n_seqs);
+  if (rows <= 8) return launch<D, 1, QS, PS, T>(a, p, stream);
+  return launch<D, 2, QS, PS, T>(a, p, stream);
+}
+
+template <bool QS, bool PS, typename T>
+int launch_typed(const Kv4Batch& a, const Kv4Attention& p, int D, cudaStream_t stream) {
+  if (D == 64) return launch_rows<64, QS, PS, T>(a, p, stream);
+  if (D == 128) return launch_rows<128, QS, PS, T>(a, p, stream);
+  return launch_rows<256, QS, PS, T>(a, p, stream);
 }
 
 }  // namespace
 
-int launch_kv4_attention(const Kv4Batch& a, const Kv4Attention& p, int D, int dtype,
+int launch_kv4_attention(const Kv4Batch& a, const Kv4Attention& args, int D, int dtype,
                          cudaStream_t stream) {
-  if (dtype == MMVQ_F32) return attention_typed<float>(a, p, D, stream);
-  if (dtype == MMVQ_F16) return attention_typed<__half>(a, p, D, stream);
-  return attention_typed<__nv_bfloat16>(a, p, D, stream);
+  Kv4Attention p = args;
+  // tiles are below 2^27: with the shift, the rounded-up reciprocal gives the exact quotient
+  const uint64_t per_page = (uint64_t)(a.page_tokens / kKv4Tile);
+  p.page_shift = per_page < 16 ? 36 : 40;
+  p.page_mul = ((1ull << p.page_shift) + per_page - 1) / per_page;
+  if (dtype == MMVQ_F32) return launch_typed<true, true, float>(a, p, D, stream);
+  if (dtype == MMVQ_F16) return launch_typed<false, true, __half>(a, p, D, stream);
+  return launch_typed<false, false, __nv_bfloat16>(a, p, D, stream);
 }
 
-int64_t kv4_attention_workspace_bytes(int) { return 256; }
+int64_t kv4_attention_workspace_bytes(int D) {
+  return kKv4CounterBytes + 2 * kKv4MaxCtas * kv4_slot_floats(D) * 4;
+}
 
 }  // namespace mmvq
