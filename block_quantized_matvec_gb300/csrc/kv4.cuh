@@ -106,6 +106,19 @@ __device__ __forceinline__ void kv4_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void kv4_store(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void kv4_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Four values to p, aligned to four elements.
+__device__ __forceinline__ void kv4_store4(float* p, float x, float y, float z, float w) {
+  *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+}
+__device__ __forceinline__ void kv4_store4(__half* p, float x, float y, float z, float w) {
+  __half2 v[2] = {__floats2half2_rn(x, y), __floats2half2_rn(z, w)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
+}
+__device__ __forceinline__ void kv4_store4(__nv_bfloat16* p, float x, float y, float z, float w) {
+  __nv_bfloat162 v[2] = {__floats2bfloat162_rn(x, y), __floats2bfloat162_rn(z, w)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
+}
+
 // The value a code stands for: (c - 7.5) * d is exact in fp32.
 __device__ __forceinline__ float kv4_value(uint32_t c, float d, float z) {
   return fmaf((float)c - 7.5f, d, z);

@@ -26,6 +26,8 @@ namespace {
 
 constexpr int kStages = 4;
 constexpr float kLazy = 8.0f;    // slack of the reference, log2 units
+constexpr int kJoin = 32;        // parts that are joined at a time: sqrt(kKv4MaxCtas)
+constexpr int kJoinAtOnce = 12;  // more are joined in two steps
 constexpr float kBoost = 6.0f;   // p is at most 2^(kLazy + kBoost) = 2^14, below fp16's largest
 
 __device__ __forceinline__ float ex2(float x) {
@@ -92,25 +94,45 @@ struct Smem {
   static constexpr int kQ = nb * 2 * NT * 32 * (QS ? 16 : 8);
   static constexpr int kRing = kStages * kv4_tile_bytes(D);  // of a warp
   uint8_t ring[kKv4Warps][kRing];   // tiles; afterwards the warps' results [row][D]
-  uint8_t q[kQ];                    // [block][half][row tile][lane]: fp16 parts, b0 b1 (b0 b1)
-  float q_start[nb][kRows];         // -7.5 sum(q) of a block, in the accumulators' units
-  __half q_sum[kRows][2][nb];       // sum(q) of a block, in two parts
+  uint8_t q[kQ];                    // [block][half][row tile][lane]: b0 b1 (and their second parts)
+  __half q_sum[kRows][4][nb];       // sum(q) of a block and -7.5 sum(q), in two parts each
   float row_factor[kRows];
   int row_pos[kRows];
   float ref[kKv4Warps][kRows], sum[kKv4Warps][kRows];
-  int64_t before[kKv4Warps * 32];   // units before each thread's sequences
+  float factor[kJoin][kRows], row_ref[kRows], row_sum[kRows];
+  int64_t before[kKv4Threads];      // units before each thread's sequences
   int64_t warp_units[kKv4Warps];
-  uint32_t present[kKv4Warps][kStages];
+  Kv4Seq seq[kKv4Threads];          // where each thread has one sequence
   int last;
   static_assert(kRing >= kRows * D * 4, "a warp's results fit its ring");
 };
 
-// The query rows of a block into q, q_start, q_sum, row_factor and row_pos.
+// N values from src in fp32; `vector`: src is 16-byte aligned.
+template <int N, typename T>
+__device__ __forceinline__ void load_values(const T* src, bool vector, float (&q)[N]) {
+  constexpr int kEach = 16 / sizeof(T);
+  if constexpr (N % kEach == 0) {
+    if (vector) {
+#pragma unroll
+      for (int k = 0; k < N / kEach; ++k) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) q[kEach * k + i] = kv4_load(e + i);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) q[i] = kv4_load(src + i);
+}
+
+// The query rows of a block into q, q_sum, row_factor and row_pos.
 template <int D, int NT, bool QS, typename T>
 __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attention& p,
                                              Smem<D, NT, QS>& sm, const Kv4Seq& s, int head,
                                              int row0, int tid) {
-  constexpr int kPer = 16 / NT, kOwn = D / kPer;  // threads a row, values a thread
+  constexpr int kPer = 32 / NT, kOwn = D / kPer;  // threads a row, values a thread
   const int row = tid / kPer, sub = tid % kPer;
   const int group = p.n_heads / a.n_kv_heads;
   const int r = row0 + row;
@@ -118,10 +140,9 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   const int t = on ? r / group : 0;
   float q[kOwn], top = 0.0f;
   if (on) {
-    const T* src = static_cast<const T*>(p.q) + (int64_t)(s.first + t) * p.ldq +
-                   (int64_t)(head * group + r - t * group) * p.hq + sub * kOwn;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) q[i] = kv4_load(src + i);
+    load_values(static_cast<const T*>(p.q) + (int64_t)(s.first + t) * p.ldq +
+                    (int64_t)(head * group + r - t * group) * p.hq + sub * kOwn,
+                p.q_vector, q);
   } else {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) q[i] = 0.0f;
@@ -130,8 +151,8 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   for (int i = 0; i < kOwn; ++i) top = fmaxf(top, fabsf(q[i]));
 #pragma unroll
   for (int o = 1; o < kPer; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // largest |q| into [2^9, 2^10): with the factor 16, sums of 32 stay below fp16's largest
-  int e = top > 0.0f && top < INFINITY ? 9 - ilogbf(top) : 0;
+  // largest |q| into [2^6, 2^7): 16 q, and 7.5 times a sum of 32, stay below fp16's largest
+  int e = top > 0.0f && top < INFINITY ? 6 - ilogbf(top) : 0;
   e = min(e, 126);
   const float f = ldexpf(1.0f, e);
 #pragma unroll
@@ -146,21 +167,20 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
     *reinterpret_cast<__half*>(at) = hi;
     if (QS) *reinterpret_cast<__half*>(at + 8) = __float2half_rn(x - __half2float(hi));
   }
-  constexpr int kBlk = kOwn >= 32 ? 1 : 32 / kOwn;  // threads a block
+  constexpr int kBlk = 32 / kOwn;  // threads a block
+  static_assert(kOwn <= 32, "a block is of one thread or more");
+  float sum = 0.0f;
 #pragma unroll
-  for (int b0 = 0; b0 < (kOwn >= 32 ? kOwn / 32 : 1); ++b0) {
-    float sum = 0.0f;
+  for (int i = 0; i < kOwn; ++i) sum += q[i];
 #pragma unroll
-    for (int i = 0; i < (kOwn >= 32 ? 32 : kOwn); ++i) sum += q[32 * b0 + i];
-#pragma unroll
-    for (int o = 1; o < kBlk; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int b = sub * kOwn / 32 + b0;
-    if (sub % kBlk == 0) {
-      const __half hi = __float2half_rn(sum);
-      sm.q_sum[row][0][b] = hi;
-      sm.q_sum[row][1][b] = __float2half_rn(sum - __half2float(hi));
-      sm.q_start[b][row] = -7.5f * 0x1p-20f * sum;
-    }
+  for (int o = 1; o < kBlk; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (sub % kBlk == 0) {
+    const int b = sub / kBlk;
+    const __half hi = __float2half_rn(sum), mid = __float2half_rn(-7.5f * sum);
+    sm.q_sum[row][0][b] = hi;
+    sm.q_sum[row][1][b] = __float2half_rn(sum - __half2float(hi));
+    sm.q_sum[row][2][b] = mid;
+    sm.q_sum[row][3][b] = __float2half_rn(fmaf(-7.5f, sum, -__half2float(mid)));
   }
   if (sub == 0) {
     sm.row_factor[row] = ldexpf(p.scale * 1.4426950408889634f, 20 - e);
@@ -168,22 +188,54 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   }
 }
 
+// Of N 32-bit words in shared memory, by the widest loads that their alignment allows.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * k);
+      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + 8 * k);
+      w[2 * k] = v.x, w[2 * k + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = *reinterpret_cast<const uint32_t*>(p + 4 * k);
+  }
+}
+
+__device__ __forceinline__ float half_of(uint32_t pair, int i) {
+  return __half2float(i ? __high2half(h2(pair)) : __low2half(h2(pair)));
+}
+
+// At most 128 registers (two CTAs an SM) where the accumulators leave room for it.
 template <int D, int NT, bool QS, bool PS, typename T>
-__global__ void __launch_bounds__(kKv4Warps * 32)
+__global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 ? 2 : 1)
     kv4_attention_kernel(const Kv4Batch a, const Kv4Attention p) {
   using S = Smem<D, NT, QS>;
   constexpr int nb = D / 32, kRows = 8 * NT, kBytes = kv4_tile_bytes(D);
+  // Codes less 7.5 before the product, or -7.5 sum(p d) after it: a rounding of p d counts with c - 7.5 or
+  // with c.  With p d in two parts and an fp16 output the latter is far below the output's rounding.
+  constexpr bool kCentre = QS || !PS;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   grid_dependency_wait();
 
   // ---- the batch's units, and this CTA's share of them
-  const int chunk = (a.n_seqs + kKv4Warps * 32 - 1) / (kKv4Warps * 32);
+  const int chunk = (a.n_seqs + kKv4Threads - 1) / kKv4Threads;
   int error = 0;
   int64_t mine = 0;
-  for (int b = tid * chunk; b < min(a.n_seqs, (tid + 1) * chunk); ++b)
-    mine += kv4_seq(a, p, kRows, b, &error).units;
+  for (int b = tid * chunk; b < min(a.n_seqs, (tid + 1) * chunk); ++b) {
+    const Kv4Seq s = kv4_seq(a, p, kRows, b, &error);
+    if (chunk == 1) sm.seq[tid] = s;
+    mine += (int64_t)a.n_kv_heads * s.blocks * s.item_units();
+  }
   if (error && blockIdx.x == 0) kv4_set_status(a.status, error);
   int64_t up_to = mine;
 #pragma unroll
@@ -209,34 +261,75 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
   const int per_page = a.page_tokens / kKv4Tile;
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kKv4CounterBytes);
   uint32_t* counters = static_cast<uint32_t*>(p.workspace);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]) + lane * 16;
 
   for (int64_t unit = lo; unit < hi;) {
-    // ---- the item of this unit
+    // ---- the item of this unit: its sequence by a search over the threads' sums
     int th = 0;
 #pragma unroll
-    for (int o = kKv4Warps * 16; o > 0; o >>= 1)
+    for (int o = kKv4Threads / 2; o > 0; o >>= 1)
       if (sm.before[th + o] <= unit) th += o;
     int b = th * chunk;
     int64_t at = sm.before[th];
-    Kv4Seq s = kv4_seq(a, p, kRows, b, &error);
-    while (at + s.units <= unit) {
-      at += s.units;
+    Kv4Seq s = chunk == 1 ? sm.seq[th] : kv4_seq(a, p, kRows, b, &error);
+    for (;;) {
+      const int64_t units = (int64_t)a.n_kv_heads * s.blocks * s.item_units();
+      if (at + units > unit) break;
+      at += units;
       s = kv4_seq(a, p, kRows, ++b, &error);
     }
-    const int item = (int)((unit - at) / s.tiles);
-    const int64_t item0 = at + (int64_t)item * s.tiles, item1 = item0 + s.tiles;
-    const int tile0 = (int)(unit - item0), tile1 = (int)(min(hi, item1) - item0);
+    const int item = (int)((unit - at) / s.item_units());
+    const int64_t item0 = at + (int64_t)item * s.item_units(), item1 = item0 + s.item_units();
+    // its units from kKv4ItemUnits on are its tiles
+    const int64_t tiles0 = item0 + kKv4ItemUnits;
+    const int tile0 = (int)max(unit - tiles0, (int64_t)0), tile1 = (int)(min(hi, item1) - tiles0);
+    unit = min(hi, item1);
+    if (tile1 <= tile0) continue;
     const int head = item / s.blocks, row0 = (item - head * s.blocks) * kRows;
     const int n_rows = min(kRows, s.n_new * group - row0);
 
-    __syncthreads();  // the block before is done with the shared memory
+    __syncthreads();  // the item before is done with the shared memory
+
+    // ---- tiles tile0 + warp, + 8, ... through the warp's ring; the page of the next is looked up
+    // a tile ahead, and the last bits of `present` say which of the fetched tiles are there
+    const uint8_t* head_base = a.cache + (int64_t)head * per_page * kBytes + lane * 16;
+    const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kBytes;
+    const int32_t* table = a.page_table + (int64_t)b * a.ld_table;
+    const int pos_lo = s.len - s.n_new;  // of the sequence's rows
+    auto tile_of = [&](int i) { return i + (i >= s.sink_tiles ? s.skip : 0); };
+    uint32_t present = 0;
+    int next = tile0 + warp, next_page = -1, next_at = 0;
+    auto look_up = [&]() {
+      const int tile = tile_of(next);
+      const int pi = (int)(((uint64_t)(uint32_t)tile * p.page_mul) >> p.page_shift);
+      next_at = tile - pi * per_page;
+      next_page = next < tile1 && pi < a.ld_table && (int64_t)tile * kKv4Tile < s.len ? __ldg(table + pi) : -1;
+    };
+    auto fetch = [&](int stage) {
+      const bool there = next_page >= 0 && next_page < a.n_pages;
+      present = present << 1 | (there ? 1u : 0u);
+      if (there) {
+        const uint8_t* src = head_base + next_page * page_bytes + next_at * kBytes;
+        const uint32_t dst = ring + stage * kBytes;
+#pragma unroll
+        for (int k = 0; k < (kBytes + 511) / 512; ++k)
+          if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes) cp_async16(dst + k * 512, src + k * 512);
+      }
+      cp_async_commit();
+      next += kKv4Warps;
+      look_up();
+    };
+    look_up();
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(k);
+
     load_queries<D, NT, QS, T>(a, p, sm, s, head, row0, tid);
     __syncthreads();
 
     // ---- what a lane keeps of the queries: columns 2c, 2c + 1 of each row tile
     float fac[NT][2];
     int pos[NT][2];
-    uint32_t qz[NT][2];
+    uint32_t qz[NT][4];  // B operands of the products with midpoints and steps
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -244,16 +337,13 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
         fac[n][e] = sm.row_factor[8 * n + 2 * c + e];
         pos[n][e] = sm.row_pos[8 * n + 2 * c + e];
       }
+      // k positions 2c, 2c + 1: of 8 blocks, the first parts, then the second; of 4, both parts,
+      // then the same of -7.5 sum(q); of 2, all four
       const uint32_t* qs = reinterpret_cast<const uint32_t*>(sm.q_sum[8 * n + g]);
-      if (nb == 8) {
-        qz[n][0] = qs[c];
-        qz[n][1] = qs[nb / 2 + c];
-      } else {  // k positions: the blocks' first parts, then their second, then nothing
-        qz[n][0] = c < nb ? qs[c] : 0u;
-        qz[n][1] = 0u;
-      }
+#pragma unroll
+      for (int k = 0; k < (nb == 8 ? 4 : nb == 4 ? 2 : 1); ++k) qz[n][k] = qs[4 * k + c];
     }
-    float o[NT][2 * nb][4], oz[NT][4], m[NT][2], l[NT][2];
+    float o[NT][2 * nb][4], oz[NT][4], m[NT][2], ref[NT][2], l[NT][2];
     int F = 15;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -264,71 +354,52 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
 #pragma unroll
       for (int e = 0; e < 4; ++e) oz[n][e] = 0.0f;
       m[n][0] = m[n][1] = -INFINITY;
+      ref[n][0] = ref[n][1] = 0.0f;
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    // ---- tiles tile0 + warp, + 4, ... through the warp's ring
-    const uint8_t* head_base = a.cache + (int64_t)head * per_page * kBytes;
-    const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kBytes;
-    const int32_t* table = a.page_table + (int64_t)b * a.ld_table;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
-    const int pos_lo = s.len - s.n_new;  // of the sequence's rows
-    auto tile_of = [&](int i) { return i + (i >= s.sink_tiles ? s.skip : 0); };
-    auto fetch = [&](int i, int stage) {
-      if (i < tile1) {
-        const int tile = tile_of(i);
-        const int pi = (int)(((uint64_t)(uint32_t)tile * p.page_mul) >> p.page_shift);
-        const int64_t page = pi < a.ld_table && tile * (int64_t)kKv4Tile < s.len ? __ldg(table + pi) : -1;
-        const bool present = page >= 0 && page < a.n_pages;
-        if (lane == 0) sm.present[warp][stage] = present;
-        if (present) {
-          const uint8_t* src = head_base + page * page_bytes + (int64_t)(tile - pi * per_page) * kBytes + lane * 16;
-          const uint32_t dst = ring + stage * kBytes + lane * 16;
-#pragma unroll
-          for (int k = 0; k < (kBytes + 511) / 512; ++k)
-            if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes) cp_async16(dst + k * 512, src + k * 512);
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(tile0 + warp + k * kKv4Warps, k);
     int stage = 0;
     for (int i = tile0 + warp; i < tile1; i += kKv4Warps) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      fetch(i + (kStages - 1) * kKv4Warps, (stage + kStages - 1) % kStages);
+      const bool there = present >> (kStages - 2) & 1;
+      fetch((stage + kStages - 1) % kStages);
       const uint8_t* tp = sm.ring[warp] + stage * kBytes;
-      const bool present = sm.present[warp][stage];
       stage = (stage + 1) % kStages;
       const int key0 = tile_of(i) * kKv4Tile;
-      if (!present) {
+      if (!there) {
         if (lane == 0 && key0 < s.len) kv4_set_status(a.status, MMVQ_ERR_ROUTING);
         continue;
       }
 
       // ---- scores
-      uint32_t kw[2 * nb], kd[2][nb / 2];
+      uint32_t kw[2 * nb], kd[2][nb / 2], kz[2];
 #pragma unroll
       for (int k = 0; k < nb / 2; ++k) {
         const uint4 v = *reinterpret_cast<const uint4*>(tp + 512 * k + 16 * lane);
         kw[4 * k] = v.x, kw[4 * k + 1] = v.y, kw[4 * k + 2] = v.z, kw[4 * k + 3] = v.w;
       }
-      uint32_t kz[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int k = 0; k < nb / 2; ++k)
-          kd[h][k] = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g + 8 * h, 0) + 4 * k);
-        kz[h] = *reinterpret_cast<const uint32_t*>(tp + D + kv4_key_scale(D, g + 8 * h, 0) +
-                                                   4 * (nb == 8 ? c : nb == 4 ? c & 1 : 0));
+        load_words(tp + kv4_key_scale(D, g + 8 * h, 0), kd[h]);
+        // the blocks that this lane's k positions stand for
+        kz[h] = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g + 8 * h, 0) +
+                                                   (nb == 2 ? (c < 2 ? D : 0) : D + 4 * (nb == 8 ? c : c & 1)));
       }
       float x[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (nb == 8) mma16(z, kz[0], kz[1], kz[0], kz[1], qz[n][0], qz[n][1]);
-        else mma8(z, kz[0], kz[1], qz[n][0]);
+        if constexpr (nb == 8) {
+          const uint32_t d0 = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g, 0) + 4 * c);
+          const uint32_t d1 = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g + 8, 0) + 4 * c);
+          mma16(z, kz[0], kz[1], kz[0], kz[1], qz[n][0], qz[n][1]);
+          mma16(z, d0, d1, d0, d1, qz[n][2], qz[n][3]);
+        } else if constexpr (nb == 4) {
+          mma16(z, kz[0], kz[1], (c & 1) ? kd[0][1] : kd[0][0], (c & 1) ? kd[1][1] : kd[1][0], qz[n][0], qz[n][1]);
+        } else {
+          mma8(z, kz[0], kz[1], qz[n][0]);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n][e] = z[e] * 0x1p-20f;
       }
@@ -336,11 +407,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
       for (int b2 = 0; b2 < nb; ++b2) {
         float acc[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 st = *reinterpret_cast<const float2*>(&sm.q_start[b2][8 * n + 2 * c]);
-          acc[n][0] = acc[n][2] = st.x;
-          acc[n][1] = acc[n][3] = st.y;
-        }
+        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = kw[b2] >> (8 * hh), w1 = kw[nb + b2] >> (8 * hh);
@@ -349,18 +416,17 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint8_t* qp = sm.q + (size_t)(((b2 * 2 + hh) * NT + n) * 32 + lane) * (QS ? 16 : 8);
-            if (QS) {
+            if constexpr (QS) {
               const uint4 q = *reinterpret_cast<const uint4*>(qp);
-              mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
               mma16(acc[n], a0, a1, a2, a3, q.z, q.w);
+              mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
             } else {
               const uint2 q = *reinterpret_cast<const uint2*>(qp);
               mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
             }
           }
         }
-        const float d0 = __half2float(((b2 & 1) ? __high2half : __low2half)(h2(kd[0][b2 / 2])));
-        const float d1 = __half2float(((b2 & 1) ? __high2half : __low2half)(h2(kd[1][b2 / 2])));
+        const float d0 = half_of(kd[0][b2 / 2], b2 & 1), d1 = half_of(kd[1][b2 / 2], b2 & 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           x[n][0] = fmaf(d0, acc[n][0], x[n][0]);
@@ -371,52 +437,48 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
       }
 
       // ---- values: steps of the lane's token pairs (2c, 2c + 1) + 8 h, midpoints of block g
-      uint32_t vd[2 * nb], vz[2];
-#pragma unroll
-      for (int k = 0; k < nb / 2; ++k) {
-        const uint4 v = *reinterpret_cast<const uint4*>(tp + 18 * D + 8 * nb * c + 16 * k);
-        vd[4 * k] = v.x, vd[4 * k + 1] = v.y, vd[4 * k + 2] = v.z, vd[4 * k + 3] = v.w;
-      }
+      uint32_t ds[2 * nb], vz[2], f2 = pow2_pair(F);
+      load_words(tp + 18 * D + 8 * nb * c, ds);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         vz[h] = g < nb ? *reinterpret_cast<const uint32_t*>(tp + 19 * D + 8 * nb * c + 4 * (h * nb + g)) : 0u;
-
-      // ---- masks: a tile that every row sees in full needs none
-      const bool all = key0 + kKv4Tile - 1 <= pos_lo &&
-                       (p.window == 0 || key0 > (int64_t)s.len - 1 - p.window || key0 + kKv4Tile <= p.sinks);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n][e] *= fac[n][e & 1];
+
+      // ---- masks: a tile that every row sees in full needs none
+      const bool all = key0 + kKv4Tile - 1 <= pos_lo &&
+                       (p.window == 0 || key0 > s.len - 1 - p.window || key0 + kKv4Tile <= p.sinks);
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
       if (!all) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + g + 8 * (e >> 1), q = pos[n][e & 1];
-            const bool see = key <= q && (p.window == 0 || key > (int64_t)q - p.window || key < p.sinks);
+            const bool see = key <= q && (p.window == 0 || key > q - p.window || key < p.sinks);
             if (!see) x[n][e] = -INFINITY;
           }
         // values that no row sees may be anything: their steps and midpoints become zero
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t keep = 0;
+          keep[h] = 0;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = key0 + 8 * h + 2 * c + e;
-            if (key < s.len && (p.window == 0 || key > (int64_t)pos_lo - p.window || key < p.sinks))
-              keep |= 0xffffu << (16 * e);
+            if (key < s.len && (p.window == 0 || key > pos_lo - p.window || key < p.sinks))
+              keep[h] |= 0xffffu << (16 * e);
           }
 #pragma unroll
-          for (int k = 0; k < nb; ++k) vd[h * nb + k] &= keep;
-          vz[h] &= keep;
+          for (int k = 0; k < nb; ++k) ds[h * nb + k] &= keep[h];
+          vz[h] &= keep[h];
         }
       }
-      uint32_t ds[2 * nb], large = 0;
-      const uint32_t f2 = pow2_pair(F);
+      uint32_t large = 0;
 #pragma unroll
       for (int k = 0; k < 2 * nb; ++k) {
-        ds[k] = mul2(vd[k], f2);
+        ds[k] = mul2(ds[k], f2);
         large |= ds[k];
       }
       bool move = (large & 0x40004000u) != 0;  // a scaled step of 2 or more
@@ -425,9 +487,13 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
 #pragma unroll
         for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + kLazy;
       if (__any_sync(0xffffffffu, move)) {
-        uint32_t top = 0;
+        uint32_t vd[2 * nb], top = 0;
+        load_words(tp + 18 * D + 8 * nb * c, vd);
 #pragma unroll
-        for (int k = 0; k < 2 * nb; ++k) top = max(top, max(vd[k] & 0xffffu, vd[k] >> 16));
+        for (int k = 0; k < 2 * nb; ++k) {
+          vd[k] &= keep[k / nb];
+          top = max(top, max(vd[k] & 0xffffu, vd[k] >> 16));
+        }
         top = __reduce_max_sync(0xffffffffu, top);
         float fo = 1.0f;
         const float d = half_bits_to_float((uint16_t)top);
@@ -435,9 +501,9 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
           const int F2 = max(-15, min(15, -2 - ilogbf(d)));
           fo = ldexpf(1.0f, F2 - F);
           F = F2;
-          const uint32_t g2 = pow2_pair(F);
+          f2 = pow2_pair(F);
 #pragma unroll
-          for (int k = 0; k < 2 * nb; ++k) ds[k] = mul2(vd[k], g2);
+          for (int k = 0; k < 2 * nb; ++k) ds[k] = mul2(vd[k], f2);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -451,40 +517,47 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
             t = fmaxf(t, m[n][e]);
             fr[e] = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - t);
             m[n][e] = t;
+            ref[n][e] = t == -INFINITY ? 0.0f : t - kBoost;
             l[n][e] *= fr[e];
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            oz[n][e] *= fr[e & 1];
+            oz[n][e] *= fr[e & 1] * (e >= 2 ? fo : 1.0f);
 #pragma unroll
             for (int k = 0; k < 2 * nb; ++k) o[n][k][e] *= fr[e & 1] * fo;
           }
         }
       }
 
-      // ---- probabilities, turned into the B operand
+      // ---- probabilities, turned into the B operand; their products with the midpoints (rows 0 to 7) and,
+      // where the codes are not centred, with the scaled steps (rows 8 to 15)
+      uint32_t vs[2] = {0u, 0u};
+      if constexpr (!kCentre) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w = g < nb ? *reinterpret_cast<const uint32_t*>(tp + 18 * D + 8 * nb * c + 4 * (h * nb + g)) : 0u;
+          vs[h] = mul2(w & keep[h], f2);
+        }
+      }
       uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float pr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1] - kBoost;
-          pr[e] = ex2(x[n][e] - ref);
-        }
+        for (int e = 0; e < 4; ++e) pr[e] = ex2(x[n][e] - ref[n][e & 1]);
         l[n][0] += pr[0] + pr[2];
         l[n][1] += pr[1] + pr[3];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const __half2 hi2 = __floats2half2_rn(pr[2 * h], pr[2 * h + 1]);
           ph[n][h] = transpose8(u32(hi2));
-          if (PS) {
+          if constexpr (PS) {
             const float2 back = __half22float2(hi2);
             pl[n][h] = transpose8(u32(__floats2half2_rn(pr[2 * h] - back.x, pr[2 * h + 1] - back.y)));
           }
         }
-        mma16(oz[n], vz[0], 0u, vz[1], 0u, ph[n][0], ph[n][1]);
-        if (PS) mma16(oz[n], vz[0], 0u, vz[1], 0u, pl[n][0], pl[n][1]);
+        mma16(oz[n], vz[0], vs[0], vz[1], vs[1], ph[n][0], ph[n][1]);
+        if constexpr (PS) mma16(oz[n], vz[0], vs[0], vz[1], vs[1], pl[n][0], pl[n][1]);
       }
       // ---- weighted values
       uint32_t vw[2 * nb];
@@ -502,20 +575,23 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
           for (int h = 0; h < 2; ++h) {
             const uint32_t d = ds[h * nb + b2];
             bh[n][h] = mul2(ph[n][h], d);
-            if (PS) bl[n][h] = fma2(pl[n][h], d, fma2(ph[n][h], d, bh[n][h] ^ 0x80008000u));
+            if constexpr (PS) bl[n][h] = fma2(pl[n][h], d, fma2(ph[n][h], d, bh[n][h] ^ 0x80008000u));
           }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
-          // (2 c - 15) 2^-24 and (16 c - 120) 2^-24: the low and the high nibbles less 7.5
-          const uint32_t a0 = fma2(w0 & 0x000f000fu, 0x40004000u, 0x800f800fu);
-          const uint32_t a1 = add2(w0 & 0x00f000f0u, 0x80788078u);
-          const uint32_t a2 = fma2(w1 & 0x000f000fu, 0x40004000u, 0x800f800fu);
-          const uint32_t a3 = add2(w1 & 0x00f000f0u, 0x80788078u);
+          uint32_t a0 = w0 & 0x000f000fu, a1 = w0 & 0x00f000f0u, a2 = w1 & 0x000f000fu, a3 = w1 & 0x00f000f0u;
+          if constexpr (kCentre) {
+            // (2 c - 15) 2^-24 and (16 c - 120) 2^-24: the low and the high nibbles less 7.5
+            a0 = fma2(a0, 0x40004000u, 0x800f800fu);
+            a1 = add2(a1, 0x80788078u);
+            a2 = fma2(a2, 0x40004000u, 0x800f800fu);
+            a3 = add2(a3, 0x80788078u);
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bh[n][0], bh[n][1]);
-            if (PS) mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bl[n][0], bl[n][1]);
+            if constexpr (PS) mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bl[n][0], bl[n][1]);
           }
         }
       }
@@ -525,7 +601,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
 
     // ---- the warp's result, in its ring: [row][D], in units of 2^(ref)
     float* res = reinterpret_cast<float*>(sm.ring[warp]);
-    const float u0 = ldexpf(1.0f, 23 - F), u1 = ldexpf(1.0f, 20 - F);
+    const float u0 = ldexpf(1.0f, (kCentre ? 23 : 24) - F), u1 = ldexpf(1.0f, 20 - F), us = ldexpf(-7.5f, -F);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -539,9 +615,10 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
           sm.ref[warp][row] = m[n][e] - kBoost;
           sm.sum[warp][row] = t;
         }
+        const float z0 = kCentre ? oz[n][e] : fmaf(us, oz[n][e + 2], oz[n][e]);
 #pragma unroll
         for (int b2 = 0; b2 < nb; ++b2) {
-          const float z = __shfl_sync(0xffffffffu, oz[n][e], 4 * b2 + c);
+          const float z = __shfl_sync(0xffffffffu, z0, 4 * b2 + c);
           float4 v;
           v.x = fmaf(o[n][2 * b2][e], u0, z);
           v.y = fmaf(o[n][2 * b2][e + 2], u1, z);
@@ -553,56 +630,63 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
     }
     __syncthreads();
 
-    // ---- the CTA's result: to the outputs, or to a slot of the workspace
-    auto store_row = [&](int row, int d4, float4 v, float ref, float sum) {
+    // A row's parts (ref, sum), k = 0 .. n - 1: the row's ref and sum, and the factor of each part.  A part
+    // without a finite score has ref -inf and sum 0 (or NaN, which must stay).
+    auto weigh = [&](int row, int n, auto part) {
+      float top = -INFINITY, sum = 0.0f;
+      for (int k = 0; k < n; ++k) top = fmaxf(top, part(k).x);
+      for (int k = 0; k < n; ++k) {
+        const float2 rs = part(k);
+        const float f = rs.x == -INFINITY ? (rs.y == 0.0f ? 0.0f : 1.0f) : ex2(rs.x - top);
+        sm.factor[k][row] = f;
+        sum = fmaf(f, rs.y, sum);
+      }
+      sm.row_ref[row] = top;
+      sm.row_sum[row] = sum;
+    };
+    auto store_row = [&](int row, int d4, float4 v) {
       const int r = row0 + row, t = r / group;
       const int64_t out = (int64_t)(s.first + t) * p.n_heads + head * group + (r - t * group);
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      T* y = static_cast<T*>(p.y) + out * D + 4 * d4;
-      kv4_store(y, v.x * inv);
-      kv4_store(y + 1, v.y * inv);
-      kv4_store(y + 2, v.z * inv);
-      kv4_store(y + 3, v.w * inv);
+      const float sum = sm.row_sum[row], inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+      kv4_store4(static_cast<T*>(p.y) + out * D + 4 * d4, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
       if (p.lse && d4 == 0)
-        p.lse[out] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+        p.lse[out] = sum == 0.0f ? -INFINITY : (sm.row_ref[row] + log2f(sum)) * 0.6931471805599453f;
     };
+
+    // ---- the CTA's result: to the outputs, or to a slot of the workspace
+    if (tid < n_rows) weigh(tid, kKv4Warps, [&](int k) { return make_float2(sm.ref[k][tid], sm.sum[k][tid]); });
+    __syncthreads();
     // the CTA that has unit u: the largest i with total * i / n_ctas <= u
     auto cta_of = [&](int64_t u) { return (int)(((u + 1) * n_ctas - 1) / total); };
-    const int first = cta_of(item0), last = cta_of(item1 - 1), parts = last - first + 1;
+    const int first = cta_of(tiles0), last = cta_of(item1 - 1), parts = last - first + 1;
     // CTA i's part of this item: the second slot where CTA i has earlier items, else the first
     auto slot_of = [&](int i) {
       return slots + (2 * (int64_t)i + (total * i / n_ctas < item0 ? 1 : 0)) * kv4_slot_floats(D);
     };
     float* slot = parts > 1 ? slot_of(cta) : nullptr;
-    for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Warps * 32) {
+    for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Threads) {
       const int row = idx / (D / 4), d4 = idx - row * (D / 4);
-      float ref = -INFINITY, sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) ref = fmaxf(ref, sm.ref[w][row]);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kKv4Warps; ++w) {
-        const float f = sm.ref[w][row] == -INFINITY ? (sm.sum[w][row] == 0.0f ? 0.0f : 1.0f) : ex2(sm.ref[w][row] - ref);
+        const float f = sm.factor[w][row];
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + row * D + 4 * d4);
-        sum = fmaf(f, sm.sum[w][row], sum);
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
         v.z = fmaf(f, x.z, v.z);
         v.w = fmaf(f, x.w, v.w);
       }
       if (parts == 1) {
-        store_row(row, d4, v, ref, sum);
+        store_row(row, d4, v);
       } else {
         *reinterpret_cast<float4*>(slot + row * D + 4 * d4) = v;
-        if (d4 == 0) {
-          slot[kRows * D + 2 * row] = ref;
-          slot[kRows * D + 2 * row + 1] = sum;
-        }
+        if (d4 == 0)
+          *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(sm.row_ref[row], sm.row_sum[row]);
       }
     }
 
-    // ---- joining the parts of a split item: groups of about sqrt(parts) by the last CTA of a group to
-    // arrive, then the groups by the last group's; always added in the order of the CTAs
+    // ---- joining the parts of a split item: in groups by the last CTA of a group to arrive, then the
+    // groups by the last group's; always added in the order of the CTAs
     if (parts > 1) {
       auto arrive = [&](uint32_t* counter, int n) {
         __threadfence();
@@ -616,56 +700,50 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
         __threadfence();
         return sm.last != 0;
       };
+      // parts of CTAs from, from + step, ...: n of them, at most kJoin
       auto join = [&](int from, int step, int n, bool final) {
-        for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Warps * 32) {
+        if (tid < n_rows)
+          weigh(tid, n, [&](int k) {
+            return __ldcg(reinterpret_cast<const float2*>(slot_of(from + k * step) + kRows * D + 2 * tid));
+          });
+        __syncthreads();
+        const float* base = slot_of(from);
+        const float* rest = slot_of(from + step);  // the others lie at equal distances: their first slots
+        const int64_t stride = 2 * (int64_t)step * kv4_slot_floats(D);
+        for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Threads) {
           const int row = idx / (D / 4), d4 = idx - row * (D / 4);
-          float ref = -INFINITY, sum = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int k = 0; k < n; ++k) {
-            const float* sl = slot_of(from + k * step);
-            const float2 rs = __ldcg(reinterpret_cast<const float2*>(sl + kRows * D + 2 * row));
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(sl + row * D + 4 * d4));
-            const float top = fmaxf(ref, rs.x);
-            const float fa = ref == -INFINITY ? 0.0f : ex2(ref - top);
-            const float fb = rs.x == -INFINITY ? (rs.y == 0.0f ? 0.0f : 1.0f) : ex2(rs.x - top);
-            ref = top;
-            sum = fmaf(fb, rs.y, sum * fa);
-            v.x = fmaf(fb, x.x, v.x * fa);
-            v.y = fmaf(fb, x.y, v.y * fa);
-            v.z = fmaf(fb, x.z, v.z * fa);
-            v.w = fmaf(fb, x.w, v.w * fa);
+          const int64_t off = row * D + 4 * d4;
+          float4 v = __ldcg(reinterpret_cast<const float4*>(base + off));
+          const float f0 = sm.factor[0][row];
+          v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll 8
+          for (int k = 1; k < n; ++k) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(rest + (k - 1) * stride + off));
+            const float f = sm.factor[k][row];
+            v.x = fmaf(f, x.x, v.x);
+            v.y = fmaf(f, x.y, v.y);
+            v.z = fmaf(f, x.z, v.z);
+            v.w = fmaf(f, x.w, v.w);
           }
-          if (final) {
-            store_row(row, d4, v, ref, sum);
-          } else {
-            float* sl = slot_of(from);
-            *reinterpret_cast<float4*>(sl + row * D + 4 * d4) = v;
-            if (d4 == 0) {  // written after every thread of the row has read it: see below
-              sm.ref[0][row] = ref;
-              sm.sum[0][row] = sum;
-            }
-          }
+          if (final) store_row(row, d4, v);
+          else *reinterpret_cast<float4*>(slot_of(from) + off) = v;
         }
-        if (!final) {
-          __syncthreads();
-          if (tid < n_rows) {
-            float* sl = slot_of(from) + kRows * D + 2 * tid;
-            sl[0] = sm.ref[0][tid];
-            sl[1] = sm.sum[0][tid];
-          }
-        }
+        if (!final && tid < n_rows)
+          *reinterpret_cast<float2*>(slot_of(from) + kRows * D + 2 * tid) =
+              make_float2(sm.row_ref[tid], sm.row_sum[tid]);
       };
-      int per = 1;
-      while (per * per < parts) ++per;
-      if (parts <= 12) per = parts;
-      const int grp = (cta - first) / per, from = first + grp * per;
+      int per = parts;
+      if (parts > kJoinAtOnce) {
+        per = 1;
+        while (per * per < parts) ++per;
+      }
+      const int grp = (cta - first) / per, from = first + grp * per, n = min(per, last + 1 - from);
       const int n_groups = (parts + per - 1) / per;
-      if (arrive(counters + 2 * from + (grp == 0 ? 1 : 0), min(per, last + 1 - from))) {
-        join(from, 1, min(per, last + 1 - from), n_groups == 1);
+      if (arrive(counters + 2 * from + (grp == 0 ? 1 : 0), n)) {
+        join(from, 1, n, n_groups == 1);
         if (n_groups > 1 && arrive(counters + 2 * kKv4MaxCtas + first, n_groups)) join(first, per, n_groups, true);
       }
     }
-    unit = item0 + tile1;
   }
 }
 
@@ -681,7 +759,7 @@ int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
     int sms = 0, per_sm = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kKv4Warps * 32, kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kKv4Threads, kSmem) != cudaSuccess ||
         per_sm < 1)
       return MMVQ_ERR_CUDA;
     ctas = min(sms * per_sm, kKv4MaxCtas);
@@ -690,10 +768,10 @@ int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
   // no more CTAs than the longest sequences that the table can hold would use
   const int rows = p.n_heads / a.n_kv_heads * kKv4MaxNew;
   const int64_t units = (int64_t)a.n_seqs * a.n_kv_heads * ((rows + 8 * NT - 1) / (8 * NT)) *
-                        (a.ld_table * (a.page_tokens / kKv4Tile));
+                        (a.ld_table * (a.page_tokens / kKv4Tile) + kKv4ItemUnits);
   const int64_t most = (units + kKv4MinUnits - 1) / kKv4MinUnits;
   const int grid = (int)(most < ctas ? most : ctas);
-  return launch_pdl(kern, dim3(grid), dim3(kKv4Warps * 32), kSmem, stream, a, p);
+  return launch_pdl(kern, dim3(grid), dim3(kKv4Threads), kSmem, stream, a, p);
 }
 
 template <int D, bool QS, bool PS, typename T>
@@ -720,6 +798,8 @@ int launch_kv4_attention(const Kv4Batch& a, const Kv4Attention& args, int D, int
   const uint64_t per_page = (uint64_t)(a.page_tokens / kKv4Tile);
   p.page_shift = per_page < 16 ? 36 : 40;
   p.page_mul = ((1ull << p.page_shift) + per_page - 1) / per_page;
+  const int64_t size = dtype == MMVQ_F32 ? 4 : 2;
+  p.q_vector = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.ldq * size) | (uintptr_t)(p.hq * size)) & 15) == 0;
   if (dtype == MMVQ_F32) return launch_typed<true, true, float>(a, p, D, stream);
   if (dtype == MMVQ_F16) return launch_typed<false, true, __half>(a, p, D, stream);
   return launch_typed<false, false, __nv_bfloat16>(a, p, D, stream);

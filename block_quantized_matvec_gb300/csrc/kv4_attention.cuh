@@ -2,12 +2,13 @@
 //
 // The rows of a sequence's query tokens that share a kv head (tokens x heads
 // of the group, token-major) are taken in blocks of 8 * NT; such a block and
-// its kv head are an item, and a unit is an item and one of the 16-token tiles
-// that any of its rows may see.  All units of the batch, in order of
-// (sequence, kv head, row block, tile), are divided evenly over the grid's
-// CTAs: whatever the lengths, every CTA gets the same number of tiles, and
-// the host needs to know no length.  A CTA's share covers whole items and up
-// to two parts of items; parts are joined by the CTA that finishes last.
+// its kv head are an item.  Its work is its 16-token tiles that any of its
+// rows may see, and kKv4ItemUnits tiles' time for beginning and ending it.
+// The units of the batch's items, in order of (sequence, kv head, row block,
+// tile), are divided evenly over the grid's CTAs: whatever the lengths, every
+// CTA gets the same work, and the host needs to know no length.  A CTA's
+// share covers whole items and up to two parts of items; parts are joined by
+// the CTA that finishes last.
 #pragma once
 #include "kv4.cuh"
 
@@ -23,14 +24,17 @@ struct Kv4Attention {
   void* y;          // [n_tokens][n_heads][D]
   float* lse;       // [n_tokens][n_heads], may be NULL
   void* workspace;
+  bool q_vector;    // the rows of q lie on 16-byte boundaries
   uint64_t page_mul;  // tile / (tiles per page) = tile * page_mul >> page_shift
   int page_shift;
 };
 
-constexpr int kKv4Warps = 4;          // warps of an attention CTA
+constexpr int kKv4Warps = 8;          // warps of an attention CTA
+constexpr int kKv4Threads = 32 * kKv4Warps;
 constexpr int kKv4MaxRows = 16;       // rows of a block (NT = 2)
 constexpr int kKv4MaxCtas = 1024;     // of a launch
-constexpr int kKv4MinUnits = 8;       // of a CTA: below, fewer CTAs take part
+constexpr int kKv4ItemUnits = 16;     // what an item costs besides its tiles
+constexpr int kKv4MinUnits = 24;      // of a CTA: below, fewer CTAs take part
 
 // Workspace: join counters (two per CTA for the groups of a split item, one for
 // the groups' results), then two partial results per CTA.
@@ -44,10 +48,11 @@ struct Kv4Seq {
   int len;     // cached tokens
   int sink_tiles, skip, tiles;  // tile i of `tiles` is i + (i >= sink_tiles ? skip : 0)
   int blocks;  // row blocks
-  int64_t units;
+  __device__ __forceinline__ int item_units() const { return tiles + kKv4ItemUnits; }
 };
 
 // A sequence without visible tokens still counts a tile, so that its zeros get written.
+// Errors only ever set *error.
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Batch& a, const Kv4Attention& p, int rows_block,
                                           int b, int* error) {
   Kv4Seq s;
@@ -70,7 +75,6 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Batch& a, const Kv4Attention&
   s.tiles = max(1, end_tile - s.skip);
   const int group = p.n_heads / a.n_kv_heads;
   s.blocks = (s.n_new * group + rows_block - 1) / rows_block;
-  s.units = (int64_t)a.n_kv_heads * s.blocks * s.tiles;
   return s;
 }
 

@@ -492,25 +492,33 @@ def _kv4_where(cache, page_table, offsets, lens):
     """Checks the tensors of a batch: the cache's and the batch's arguments of the C calls."""
     n_pages, n_kv, tiles, tile_bytes = cache.shape
     n_seqs, ld = page_table.shape
-    if not (cache.is_cuda and cache.is_contiguous() and cache.dtype == torch.uint8):
-        raise ValueError("cache must be a contiguous CUDA uint8 tensor (kv4_cache)")
-    if tile_bytes % 20:
-        raise ValueError("cache tiles hold 20 * head_dim bytes")
-    for t, n, name in ((page_table, n_seqs * ld, "page_table"), (offsets, n_seqs + 1, "offsets"),
-                       (lens, n_seqs, "lens")):
-        if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.int32 and t.numel() == n):
-            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} values")
-    return ((cache.data_ptr(), n_pages, tiles * KV4_TILE, n_kv, tile_bytes // 20,
-             page_table.data_ptr(), ld, offsets.data_ptr(), lens.data_ptr(), n_seqs))
+    if cache.dtype is not torch.uint8 or not cache.is_cuda or not cache.is_contiguous() or \
+            tile_bytes % 20:
+        raise ValueError("cache must be a contiguous CUDA uint8 tensor [pages, kv heads, "
+                         "page_tokens/16, 20*head_dim] (kv4_cache)")
+    i32 = torch.int32
+    if page_table.dtype is not i32 or not page_table.is_cuda or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous CUDA int32 tensor")
+    if offsets.dtype is not i32 or not offsets.is_cuda or not offsets.is_contiguous() or \
+            offsets.numel() != n_seqs + 1:
+        raise ValueError(f"offsets must be a contiguous CUDA int32 tensor of {n_seqs + 1} values")
+    if lens.dtype is not i32 or not lens.is_cuda or not lens.is_contiguous() or \
+            lens.numel() != n_seqs:
+        raise ValueError(f"lens must be a contiguous CUDA int32 tensor of {n_seqs} values")
+    return (cache.data_ptr(), n_pages, tiles * KV4_TILE, n_kv, tile_bytes // 20,
+            page_table.data_ptr(), ld, offsets.data_ptr(), lens.data_ptr(), n_seqs)
 
 
 def _kv4_rows(t, heads, dim, name):
-    """A [n, heads, dim] tensor with unit inner stride: its token and head strides."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
-            (t.stride(2) != 1 and t.numel()) or t.dtype not in _DTYPES:
+    """A [n, heads, dim] tensor with unit inner stride: its type's number, tokens, and the token and
+    head strides."""
+    n, h, d = t.shape
+    ld, hs, one = t.stride()
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None or not t.is_cuda or (heads and h != heads) or d != dim or (one != 1 and n):
         raise ValueError(f"{name} must be a CUDA float32, float16 or bfloat16 tensor "
-                         f"[tokens, {heads}, {dim}] with unit inner stride")
-    return t.stride(0), t.stride(1)
+                         f"[tokens, {heads or 'heads'}, {dim}] with unit inner stride")
+    return dtype, n, h, ld, hs
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
@@ -520,13 +528,12 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table
     offsets[b]..offsets[b+1]-1 are the last tokens of sequence b, whose length with them is
     lens[b]; position p of it lies in page page_table[b, p // page_tokens].  (mmvq_kv4_append)"""
     where = _kv4_where(cache, page_table, offsets, lens)
-    n = k.shape[0]
-    ldk, hk = _kv4_rows(k, where[3], where[4], "k")
-    ldv, hv = _kv4_rows(v, where[3], where[4], "v")
-    if v.shape[0] != n or v.dtype != k.dtype:
+    dtype, n, _, ldk, hk = _kv4_rows(k, where[3], where[4], "k")
+    dtype_v, n_v, _, ldv, hv = _kv4_rows(v, where[3], where[4], "v")
+    if n_v != n or dtype_v != dtype:
         raise ValueError("k and v must have the same tokens and type")
-    _check(lib().mmvq_kv4_append(_DTYPES[k.dtype], k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv,
-                                 *where, n, _ptr(status), _stream(stream)), "mmvq_kv4_append")
+    _check(lib().mmvq_kv4_append(dtype, k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv, *where, n,
+                                 _ptr(status), _stream(stream)), "mmvq_kv4_append")
 
 
 def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tensor,
@@ -536,16 +543,19 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tenso
     """(k, v), each [n_tokens, kv heads, head_dim] of dtype: the cached values of the last
     offsets[b+1]-offsets[b] of the first lens[b] tokens of each sequence b.  (mmvq_kv4_read)"""
     where = _kv4_where(cache, page_table, offsets, lens)
+    number = _DTYPES.get(dtype)
+    if number is None:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
     shape = (n_tokens, where[3], where[4])
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=cache.device),
-               torch.empty(shape, dtype=dtype, device=cache.device))
-    k, v = out
-    for t in out:
-        _dev(t, "out")
-        if t.shape != shape or t.dtype != dtype or dtype not in _DTYPES:
-            raise ValueError(f"out must be two tensors {list(shape)} of {dtype}")
-    _check(lib().mmvq_kv4_read(_DTYPES[dtype], k.data_ptr(), v.data_ptr(), *where, n_tokens,
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        k, v = out
+        for t in out:
+            if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous CUDA tensors {list(shape)} of {dtype}")
+    _check(lib().mmvq_kv4_read(number, k.data_ptr(), v.data_ptr(), *where, n_tokens,
                                _ptr(status), _stream(stream)), "mmvq_kv4_read")
     return k, v
 
@@ -570,9 +580,8 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     last `window` of them and the first `sinks` of the sequence.  scale defaults to
     head_dim**-0.5; workspace: kv4_attention_workspace.  (mmvq_kv4_attention)"""
     where = _kv4_where(cache, page_table, offsets, lens)
-    n_kv, dim = where[3], where[4]
-    n, heads = q.shape[0], q.shape[1]
-    ldq, hq = _kv4_rows(q, heads, dim, "q")
+    dim = where[4]
+    dtype, n, heads, ldq, hq = _kv4_rows(q, 0, dim, "q")
     if out is None:
         out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not out.is_contiguous():
@@ -585,10 +594,9 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     if workspace is None:
         workspace = kv4_attention_workspace(dim, q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < \
-            lib().mmvq_kv4_attention_workspace_bytes(dim):
+            workspace.nbytes < lib().mmvq_kv4_attention_workspace_bytes(dim):
         raise ValueError("workspace is too small: kv4_attention_workspace(head_dim, device)")
-    _check(lib().mmvq_kv4_attention(_DTYPES[q.dtype], q.data_ptr(), ldq, hq, heads,
+    _check(lib().mmvq_kv4_attention(dtype, q.data_ptr(), ldq, hq, heads,
                                     dim ** -0.5 if scale is None else scale, window, sinks,
                                     out.data_ptr(), _ptr(lse), *where, n, workspace.data_ptr(),
                                     _ptr(status), _stream(stream)), "mmvq_kv4_attention")
