@@ -2,18 +2,17 @@
 //
 // Mathematics.  A warp takes tiles of 16 cached tokens.  Scores come as
 // S^T[tokens x rows] = K Q^T from m16n8k16 f16 products whose A operand is the
-// tile's codes: a code c masked out of its word stands, as the bits of an
-// fp16, for c * 2^-24 (low nibble of a byte) or c * 2^-20 (high nibble), exact
-// subnormals, so a key costs no conversion at all; the rows of Q are scaled by
-// a power of two each, and by 16 more where they meet low nibbles.  Per block
-// of 32 the accumulator starts at -7.5 sum(q) and is multiplied by the block's
-// d in fp32; sum(z sum(q)) over the blocks is one more product, sum(q) in two
-// fp16 parts.  Probabilities p = 2^(s - m + 6) use a reference m that is only
-// moved when a score exceeds it by 8 (in log2 units): the result does not
-// depend on m, and most tiles skip the maximum across lanes and the rescaling.
-// O^T[values x rows] += V^T P': A = the codes less 7.5 (one fp16 operation on
-// the subnormals, exact), B = p d per block of 32 (d scaled by a power of two
-// 2^F that keeps it in fp16's middle), and sum(p z) one more product.
+// tile's codes: masked out of its word a code c stands, as the bits of an
+// fp16, for c * 2^-24 (low nibble of a byte) or c * 2^-20 (high nibble), so a
+// key costs no conversion; for fp32 queries it becomes c - 8 (centre() below).
+// The rows of Q are scaled by a power of two each, and by 16 more where they
+// meet low nibbles.  Per block of 32 the sum is multiplied by the block's d in
+// fp32; sum(z sum(q)) and sum(d sum(q)) (the codes' offset) over the blocks
+// are one more product, sum(q) in two fp16 parts.  Probabilities
+// p = 2^(s - m + 12) use a reference m that is only moved when a score exceeds
+// it by 2 (in log2 units): the result does not depend on m, and most tiles skip
+// the maximum across lanes and the rescaling.  O^T[values x rows] += V^T P':
+// A = the codes, B = p d per block of 32; sum(p z) and sum(p d) one more product.
 //
 // Precision.  fp32 q enters as two fp16 parts (22 bits), and for fp32 and fp16
 // the products p d do too; bf16 keeps 11 bits of p d, finer than its own 8.
@@ -25,10 +24,10 @@ namespace mmvq {
 namespace {
 
 constexpr int kStages = 4;
-constexpr float kLazy = 8.0f;    // slack of the reference, log2 units
+constexpr float kLazy = 2.0f;    // slack of the reference, log2 units
 constexpr int kJoin = 32;        // parts that are joined at a time: sqrt(kKv4MaxCtas)
 constexpr int kJoinAtOnce = 12;  // more are joined in two steps
-constexpr float kBoost = 6.0f;   // p is at most 2^(kLazy + kBoost) = 2^14, below fp16's largest
+constexpr float kBoost = 12.0f;  // p is at most 2^(kLazy + kBoost) = 2^14, below fp16's largest
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -81,30 +80,74 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 2^e as an fp16 pair, -15 <= e <= 15 (2^-15 is a subnormal).
-__device__ __forceinline__ uint32_t pow2_pair(int e) {
-  const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : 0x0200u;
-  return h | (h << 16);
+// 2^e, -126 <= e <= 127, and the exponent of a positive normal x.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }
+
+// a / b of unsigned numbers: most fit 32 bits, whose division is several times shorter.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
-template <int D, int NT, bool QS>
-struct Smem {
-  static constexpr int nb = D / 32;
+// The division of `total` units among n CTAs: the first `more` have share + 1.
+struct Shares {
+  int64_t share, more;
+  __device__ __forceinline__ Shares(int64_t total, int n) : share(divide(total, n)), more(total - share * n) {}
+  __device__ __forceinline__ int64_t begin(int i) const { return i * share + min((int64_t)i, more); }
+  __device__ __forceinline__ int cta_of(int64_t unit) const {
+    const int64_t large = more * (share + 1);
+    return (int)(unit < large ? divide(unit, share + 1) : more + divide(unit - large, share));
+  }
+};
+
+// Codes masked out of a word, low nibbles in a0 and a1, high ones in a2 and a3, become c - 8 and 16 (c - 8):
+// set below 1024 as the mantissa's last bits, exactly, then 1024 and the centre are taken off.  The tensor core
+// aligns a subnormal by its nominal exponent and cuts off what lies far below it (sums then keep about 17 bits);
+// these are normal numbers.
+__device__ __forceinline__ void centre(uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
+  a0 = add2(a0 | 0x64006400u, 0xe408e408u);  // - 1032
+  a1 = add2(a1 | 0x64006400u, 0xe408e408u);
+  a2 = add2(a2 | 0x64006400u, 0xe480e480u);  // - 1152
+  a3 = add2(a3 | 0x64006400u, 0xe480e480u);
+}
+
+// a b - c, rounded once: what a product c = a b lost in rounding, exactly.
+__device__ __forceinline__ uint32_t residue2(uint32_t a, uint32_t b, uint32_t c) {
+  return u32(__hfma2(h2(a), h2(b), __hneg2(h2(c))));
+}
+
+// A kernel's instance: heads of D values, NT tiles of 8 rows, QS: fp32 queries in two parts.
+template <int D_, int NT_, bool QS_>
+struct Shape {
+  static constexpr int D = D_, NT = NT_;
+  static constexpr bool QS = QS_;
+  static constexpr int nb = D / 32, kGroups = nb > 4 ? nb / 4 : 1, kOfGroup = nb / kGroups;  // blocks
   static constexpr int kRows = 8 * NT;
-  static constexpr int kQ = nb * 2 * NT * 32 * (QS ? 16 : 8);
-  static constexpr int kRing = kStages * kv4_tile_bytes(D);  // of a warp
-  uint8_t ring[kKv4Warps][kRing];   // tiles; afterwards the warps' results [row][D]
-  uint8_t q[kQ];                    // [block][half][row tile][lane]: b0 b1 (and their second parts)
-  __half q_sum[kRows][4][nb];       // sum(q) of a block and -7.5 sum(q), in two parts each
-  float row_factor[kRows];
-  int row_pos[kRows];
-  float ref[kKv4Warps][kRows], sum[kKv4Warps][kRows];
-  float factor[kJoin][kRows], row_ref[kRows], row_sum[kRows];
-  int64_t before[kKv4Threads];      // units before each thread's sequences
-  int64_t warp_units[kKv4Warps];
-  Kv4Seq seq[kKv4Threads];          // where each thread has one sequence
+  // two CTAs of 8 warps and 128 registers a thread; one of 12 and 168 or of 8 and 255 where the accumulators
+  // (4 registers per 16 values and row tile) need them
+  static constexpr int kWarps = D == 128 && NT == 2 ? 12 : 8;
+  static constexpr int kCtas = D * NT <= 128 ? 2 : 1;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kBytes = kv4_tile_bytes(D);
+};
+
+template <typename S>
+struct Smem {
+  static constexpr int kRing = kStages * S::kBytes;  // of a warp
+  uint8_t ring[S::kWarps][kRing];   // tiles; afterwards the warps' results [row][D]
+  // [block][part][row tile][lane]: the B operands of a block's two products
+  uint8_t q[S::nb * (S::QS ? 2 : 1) * S::NT * 32 * 16];
+  __half q_sum[S::kRows][S::kGroups][4][S::kOfGroup];  // sum(q) of a block, and its multiple for d, in two parts each
+  float row_factor[S::kRows];
+  int row_pos[S::kRows];
+  float ref[kJoin][S::kRows], sum[kJoin][S::kRows], factor[kJoin][S::kRows];  // of the warps, or of an item's parts
+  float row_ref[S::kRows], row_sum[S::kRows];
+  int64_t before[S::kThreads];      // units before each thread's sequences
+  int64_t warp_units[S::kWarps];
+  Kv4Seq seq[S::kThreads];          // where each thread has one sequence
   int last;
-  static_assert(kRing >= kRows * D * 4, "a warp's results fit its ring");
+  static_assert(kRing >= S::kRows * S::D * 4, "a warp's results fit its ring");
 };
 
 // N values from src in fp32; `vector`: src is 16-byte aligned.
@@ -127,12 +170,14 @@ __device__ __forceinline__ void load_values(const T* src, bool vector, float (&q
   for (int i = 0; i < N; ++i) q[i] = kv4_load(src + i);
 }
 
-// The query rows of a block into q, q_sum, row_factor and row_pos.
-template <int D, int NT, bool QS, typename T>
-__device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attention& p,
-                                             Smem<D, NT, QS>& sm, const Kv4Seq& s, int head,
-                                             int row0, int tid) {
+// The query rows of a block into q, q_sum, row_factor and row_pos, by the first 8 warps.
+template <typename S, typename T>
+__device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attention& p, Smem<S>& sm,
+                                             const Kv4Seq& s, int head, int row0, int tid) {
+  constexpr int D = S::D, NT = S::NT;
+  constexpr bool QS = S::QS;
   constexpr int kPer = 32 / NT, kOwn = D / kPer;  // threads a row, values a thread
+  if (tid >= 256) return;
   const int row = tid / kPer, sub = tid % kPer;
   const int group = p.n_heads / a.n_kv_heads;
   const int r = row0 + row;
@@ -152,9 +197,8 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
 #pragma unroll
   for (int o = 1; o < kPer; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   // largest |q| into [2^6, 2^7): 16 q, and 7.5 times a sum of 32, stay below fp16's largest
-  int e = top > 0.0f && top < INFINITY ? 6 - ilogbf(top) : 0;
-  e = min(e, 126);
-  const float f = ldexpf(1.0f, e);
+  const int e = top > 0.0f && top < INFINITY ? min(6 - exponent(top), 126) : 0;
+  const float f = pow2(e);
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) q[i] *= f;
 #pragma unroll
@@ -162,10 +206,10 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
     const int d = sub * kOwn + i, b = d / 32, u = d % 32 / 8, n = d % 8;
     const float x = (n & 1) ? q[i] : 16.0f * q[i];
     const __half hi = __float2half_rn(x);
-    uint8_t* at = sm.q + (size_t)(((b * 2 + (n & 3) / 2) * NT + row / 8) * 32 + (row % 8) * 4 + u) * (QS ? 16 : 8) +
-                  (n & 1) * 4 + (n >> 2) * 2;
+    uint8_t* at = sm.q + (size_t)((b * (QS ? 2 : 1) * NT + row / 8) * 32 + (row % 8) * 4 + u) * 16 +
+                  ((n & 3) / 2) * 8 + (n & 1) * 4 + (n >> 2) * 2;
     *reinterpret_cast<__half*>(at) = hi;
-    if (QS) *reinterpret_cast<__half*>(at + 8) = __float2half_rn(x - __half2float(hi));
+    if (QS) *reinterpret_cast<__half*>(at + NT * 32 * 16) = __float2half_rn(x - __half2float(hi));
   }
   constexpr int kBlk = 32 / kOwn;  // threads a block
   static_assert(kOwn <= 32, "a block is of one thread or more");
@@ -176,14 +220,19 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   for (int o = 1; o < kBlk; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (sub % kBlk == 0) {
     const int b = sub / kBlk;
-    const __half hi = __float2half_rn(sum), mid = __float2half_rn(-7.5f * sum);
-    sm.q_sum[row][0][b] = hi;
-    sm.q_sum[row][1][b] = __float2half_rn(sum - __half2float(hi));
-    sm.q_sum[row][2][b] = mid;
-    sm.q_sum[row][3][b] = __float2half_rn(fmaf(-7.5f, sum, -__half2float(mid)));
+    constexpr float kOff = QS ? 0.5f : -7.5f;  // the codes enter less 8, or as they are
+    const __half hi = __float2half_rn(sum), mid = __float2half_rn(kOff * sum);
+    auto& out = sm.q_sum[row][b / S::kOfGroup];
+    out[0][b % S::kOfGroup] = hi;
+    out[1][b % S::kOfGroup] = __float2half_rn(sum - __half2float(hi));
+    out[2][b % S::kOfGroup] = mid;
+    out[3][b % S::kOfGroup] = __float2half_rn(fmaf(kOff, sum, -__half2float(mid)));
   }
   if (sub == 0) {
-    sm.row_factor[row] = ldexpf(p.scale * 1.4426950408889634f, 20 - e);
+    // a power of two in two steps: it can pass fp32's range where the product does not
+    constexpr int kUnit = QS ? -4 : 20;
+    const int f2 = kUnit - e;
+    sm.row_factor[row] = p.scale * 1.4426950408889634f * pow2(f2 / 2) * pow2(f2 - f2 / 2);
     sm.row_pos[row] = on ? s.len - s.n_new + t : -1;
   }
 }
@@ -213,22 +262,25 @@ __device__ __forceinline__ float half_of(uint32_t pair, int i) {
   return __half2float(i ? __high2half(h2(pair)) : __low2half(h2(pair)));
 }
 
-// At most 128 registers (two CTAs an SM) where the accumulators leave room for it.
-template <int D, int NT, bool QS, bool PS, typename T>
-__global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 ? 2 : 1)
+template <typename S, bool PS, typename T>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas)
     kv4_attention_kernel(const Kv4Batch a, const Kv4Attention p) {
-  using S = Smem<D, NT, QS>;
-  constexpr int nb = D / 32, kRows = 8 * NT, kBytes = kv4_tile_bytes(D);
-  // Codes less 7.5 before the product, or -7.5 sum(p d) after it: a rounding of p d counts with c - 7.5 or
-  // with c.  With p d in two parts and an fp16 output the latter is far below the output's rounding.
+  constexpr int D = S::D, NT = S::NT, nb = S::nb, kRows = S::kRows, kBytes = S::kBytes;
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kGroups = S::kGroups;
+  constexpr bool QS = S::QS;
+  // Value codes less 8 before the product, and 0.5 sum(p d) after it, or -7.5 sum(p d) after it: a rounding of
+  // p d counts with c - 8 or with c.  With p d in two parts and an fp16 output the latter is far below the
+  // output's rounding.
   constexpr bool kCentre = QS || !PS;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  S& sm = *reinterpret_cast<S*>(smem_raw);
+  Smem<S>& sm = *reinterpret_cast<Smem<S>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   grid_dependency_wait();
+  // The next kernel may be launched now: whatever it is, it waits for this one's results
+  grid_launch_dependents();
 
   // ---- the batch's units, and this CTA's share of them
-  const int chunk = (a.n_seqs + kKv4Threads - 1) / kKv4Threads;
+  const int chunk = (a.n_seqs + kThreads - 1) / kThreads;
   int error = 0;
   int64_t mine = 0;
   for (int b = tid * chunk; b < min(a.n_seqs, (tid + 1) * chunk); ++b) {
@@ -247,7 +299,7 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kKv4Warps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) up_to += sm.warp_units[w];
     total += sm.warp_units[w];
   }
@@ -256,19 +308,20 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
   const int n_ctas = (int)min((int64_t)gridDim.x, (total + kKv4MinUnits - 1) / kKv4MinUnits);
   const int cta = blockIdx.x;
   if (cta >= n_ctas) return;
-  const int64_t lo = total * cta / n_ctas, hi = total * (cta + 1) / n_ctas;
+  const Shares shares(total, n_ctas);
+  const int64_t lo = shares.begin(cta), hi = shares.begin(cta + 1);
   const int group = p.n_heads / a.n_kv_heads;
   const int per_page = a.page_tokens / kKv4Tile;
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kKv4CounterBytes);
   uint32_t* counters = static_cast<uint32_t*>(p.workspace);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]) + lane * 16;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
 
   for (int64_t unit = lo; unit < hi;) {
     // ---- the item of this unit: its sequence by a search over the threads' sums
     int th = 0;
 #pragma unroll
-    for (int o = kKv4Threads / 2; o > 0; o >>= 1)
-      if (sm.before[th + o] <= unit) th += o;
+    for (int o = 256; o > 0; o >>= 1)
+      if (th + o < kThreads && sm.before[th + o] <= unit) th += o;
     int b = th * chunk;
     int64_t at = sm.before[th];
     Kv4Seq s = chunk == 1 ? sm.seq[th] : kv4_seq(a, p, kRows, b, &error);
@@ -278,7 +331,7 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
       at += units;
       s = kv4_seq(a, p, kRows, ++b, &error);
     }
-    const int item = (int)((unit - at) / s.item_units());
+    const int item = (int)divide(unit - at, s.item_units());
     const int64_t item0 = at + (int64_t)item * s.item_units(), item1 = item0 + s.item_units();
     // its units from kKv4ItemUnits on are its tiles
     const int64_t tiles0 = item0 + kKv4ItemUnits;
@@ -290,10 +343,10 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
 
     __syncthreads();  // the item before is done with the shared memory
 
-    // ---- tiles tile0 + warp, + 8, ... through the warp's ring; the page of the next is looked up
+    // ---- tiles tile0 + warp, + kWarps, ... through the warp's ring; the page of the next is looked up
     // a tile ahead, and the last bits of `present` say which of the fetched tiles are there
-    const uint8_t* head_base = a.cache + (int64_t)head * per_page * kBytes + lane * 16;
-    const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kBytes;
+    const uint8_t* head_base = a.cache + (int64_t)head * per_page * kv4_tile_bytes(D);
+    const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kv4_tile_bytes(D);
     const int32_t* table = a.page_table + (int64_t)b * a.ld_table;
     const int pos_lo = s.len - s.n_new;  // of the sequence's rows
     auto tile_of = [&](int i) { return i + (i >= s.sink_tiles ? s.skip : 0); };
@@ -309,27 +362,28 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
       const bool there = next_page >= 0 && next_page < a.n_pages;
       present = present << 1 | (there ? 1u : 0u);
       if (there) {
-        const uint8_t* src = head_base + next_page * page_bytes + next_at * kBytes;
+        const uint8_t* src = head_base + next_page * page_bytes + next_at * kv4_tile_bytes(D);
         const uint32_t dst = ring + stage * kBytes;
 #pragma unroll
         for (int k = 0; k < (kBytes + 511) / 512; ++k)
-          if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes) cp_async16(dst + k * 512, src + k * 512);
+          if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes)
+            cp_async16(dst + k * 512 + lane * 16, src + k * 512 + lane * 16);
       }
       cp_async_commit();
-      next += kKv4Warps;
+      next += kWarps;
       look_up();
     };
     look_up();
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(k);
 
-    load_queries<D, NT, QS, T>(a, p, sm, s, head, row0, tid);
+    load_queries<S, T>(a, p, sm, s, head, row0, tid);
     __syncthreads();
 
     // ---- what a lane keeps of the queries: columns 2c, 2c + 1 of each row tile
     float fac[NT][2];
     int pos[NT][2];
-    uint32_t qz[NT][4];  // B operands of the products with midpoints and steps
+    uint32_t qz[NT][kGroups][2];  // B operands of the products with midpoints and steps
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -337,14 +391,16 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
         fac[n][e] = sm.row_factor[8 * n + 2 * c + e];
         pos[n][e] = sm.row_pos[8 * n + 2 * c + e];
       }
-      // k positions 2c, 2c + 1: of 8 blocks, the first parts, then the second; of 4, both parts,
-      // then the same of -7.5 sum(q); of 2, all four
-      const uint32_t* qs = reinterpret_cast<const uint32_t*>(sm.q_sum[8 * n + g]);
+      // k positions: of 4 blocks, both parts of sum(q), then both of -7.5 sum(q); of 2, all four at once
 #pragma unroll
-      for (int k = 0; k < (nb == 8 ? 4 : nb == 4 ? 2 : 1); ++k) qz[n][k] = qs[4 * k + c];
+      for (int k = 0; k < kGroups; ++k) {
+        const uint32_t* qs = reinterpret_cast<const uint32_t*>(sm.q_sum[8 * n + g][k]);
+        qz[n][k][0] = qs[c];
+        qz[n][k][1] = nb == 2 ? 0u : qs[4 + c];
+      }
     }
     float o[NT][2 * nb][4], oz[NT][4], m[NT][2], ref[NT][2], l[NT][2];
-    int F = 15;
+    int E = 0;  // p is smaller by 2^E where steps reach 2^(E + 1): p d stays in fp16's range
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -359,7 +415,7 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
     }
 
     int stage = 0;
-    for (int i = tile0 + warp; i < tile1; i += kKv4Warps) {
+    for (int i = tile0 + warp; i < tile1; i += kWarps) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
       const bool there = present >> (kStages - 2) & 1;
@@ -373,58 +429,60 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
       }
 
       // ---- scores
-      uint32_t kw[2 * nb], kd[2][nb / 2], kz[2];
+      uint32_t kw[2 * nb], kd[2][nb / 2];
 #pragma unroll
       for (int k = 0; k < nb / 2; ++k) {
         const uint4 v = *reinterpret_cast<const uint4*>(tp + 512 * k + 16 * lane);
         kw[4 * k] = v.x, kw[4 * k + 1] = v.y, kw[4 * k + 2] = v.z, kw[4 * k + 3] = v.w;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        load_words(tp + kv4_key_scale(D, g + 8 * h, 0), kd[h]);
-        // the blocks that this lane's k positions stand for
-        kz[h] = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g + 8 * h, 0) +
-                                                   (nb == 2 ? (c < 2 ? D : 0) : D + 4 * (nb == 8 ? c : c & 1)));
-      }
+      for (int h = 0; h < 2; ++h) load_words(tp + kv4_key_scale(D, g + 8 * h, 0), kd[h]);
       float x[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (nb == 8) {
-          const uint32_t d0 = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g, 0) + 4 * c);
-          const uint32_t d1 = *reinterpret_cast<const uint32_t*>(tp + kv4_key_scale(D, g + 8, 0) + 4 * c);
-          mma16(z, kz[0], kz[1], kz[0], kz[1], qz[n][0], qz[n][1]);
-          mma16(z, d0, d1, d0, d1, qz[n][2], qz[n][3]);
-        } else if constexpr (nb == 4) {
-          mma16(z, kz[0], kz[1], (c & 1) ? kd[0][1] : kd[0][0], (c & 1) ? kd[1][1] : kd[1][0], qz[n][0], qz[n][1]);
-        } else {
-          mma8(z, kz[0], kz[1], qz[n][0]);
+      for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {  // midpoints and steps of this lane's k positions
+        uint32_t az[2], ad[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* at = tp + kv4_key_scale(D, g + 8 * h, 4 * k);
+          az[h] = *reinterpret_cast<const uint32_t*>(at + (nb == 2 ? (c < 2 ? D : 0) : D + 4 * (c & 1)));
+          ad[h] = nb == 2 ? 0u : (c & 1) ? kd[h][nb == 2 ? 0 : 2 * k + 1] : kd[h][2 * k];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] = z[e] * 0x1p-20f;
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (nb == 2) mma8(x[n], az[0], az[1], qz[n][k][0]);
+          else mma16(x[n], az[0], az[1], ad[0], ad[1], qz[n][k][0], qz[n][k][1]);
+        }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] *= QS ? 0x1p+4f : 0x1p-20f;
 #pragma unroll
       for (int b2 = 0; b2 < nb; ++b2) {
         float acc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+        uint32_t ka[2][4];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = kw[b2] >> (8 * hh), w1 = kw[nb + b2] >> (8 * hh);
-          const uint32_t a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu, a2 = w0 & 0x00f000f0u,
-                         a3 = w1 & 0x00f000f0u;
+          ka[hh][0] = w0 & 0x000f000fu, ka[hh][1] = w1 & 0x000f000fu;
+          ka[hh][2] = w0 & 0x00f000f0u, ka[hh][3] = w1 & 0x00f000f0u;
+          if constexpr (QS) centre(ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint8_t* qp = sm.q + (size_t)(((b2 * 2 + hh) * NT + n) * 32 + lane) * (QS ? 16 : 8);
-            if constexpr (QS) {
-              const uint4 q = *reinterpret_cast<const uint4*>(qp);
-              mma16(acc[n], a0, a1, a2, a3, q.z, q.w);
-              mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
-            } else {
-              const uint2 q = *reinterpret_cast<const uint2*>(qp);
-              mma16(acc[n], a0, a1, a2, a3, q.x, q.y);
-            }
+        for (int n = 0; n < NT; ++n) {
+          const uint8_t* qp = sm.q + (size_t)((b2 * (QS ? 2 : 1) * NT + n) * 32 + lane) * 16;
+          if constexpr (QS) {
+            const uint4 q = *reinterpret_cast<const uint4*>(qp + NT * 32 * 16);
+            mma16(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
+            mma16(acc[n], ka[1][0], ka[1][1], ka[1][2], ka[1][3], q.z, q.w);
           }
+          const uint4 q = *reinterpret_cast<const uint4*>(qp);
+          mma16(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
+          mma16(acc[n], ka[1][0], ka[1][1], ka[1][2], ka[1][3], q.z, q.w);
         }
         const float d0 = half_of(kd[0][b2 / 2], b2 & 1), d1 = half_of(kd[1][b2 / 2], b2 & 1);
 #pragma unroll
@@ -437,11 +495,14 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
       }
 
       // ---- values: steps of the lane's token pairs (2c, 2c + 1) + 8 h, midpoints of block g
-      uint32_t ds[2 * nb], vz[2], f2 = pow2_pair(F);
+      uint32_t ds[2 * nb], vz[2], vs[2] = {0u, 0u};  // and the steps of block g
       load_words(tp + 18 * D + 8 * nb * c, ds);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        vz[h] = g < nb ? *reinterpret_cast<const uint32_t*>(tp + 19 * D + 8 * nb * c + 4 * (h * nb + g)) : 0u;
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* at = tp + 18 * D + 8 * nb * c + 4 * (h * nb + g);
+        vs[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+        vz[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at + D) : 0u;
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -450,7 +511,6 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
       // ---- masks: a tile that every row sees in full needs none
       const bool all = key0 + kKv4Tile - 1 <= pos_lo &&
                        (p.window == 0 || key0 > s.len - 1 - p.window || key0 + kKv4Tile <= p.sinks);
-      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
       if (!all) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -463,48 +523,35 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
         // values that no row sees may be anything: their steps and midpoints become zero
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          keep[h] = 0;
+          uint32_t keep = 0;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = key0 + 8 * h + 2 * c + e;
             if (key < s.len && (p.window == 0 || key > pos_lo - p.window || key < p.sinks))
-              keep[h] |= 0xffffu << (16 * e);
+              keep |= 0xffffu << (16 * e);
           }
 #pragma unroll
-          for (int k = 0; k < nb; ++k) ds[h * nb + k] &= keep[h];
-          vz[h] &= keep[h];
+          for (int k = 0; k < nb; ++k) ds[h * nb + k] &= keep;
+          vz[h] &= keep;
+          vs[h] &= keep;
         }
       }
       uint32_t large = 0;
 #pragma unroll
-      for (int k = 0; k < 2 * nb; ++k) {
-        ds[k] = mul2(ds[k], f2);
-        large |= ds[k];
-      }
-      bool move = (large & 0x40004000u) != 0;  // a scaled step of 2 or more
+      for (int k = 0; k < 2 * nb; ++k) large |= ds[k];
+      bool move = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + kLazy;
-      if (__any_sync(0xffffffffu, move)) {
-        uint32_t vd[2 * nb], top = 0;
-        load_words(tp + 18 * D + 8 * nb * c, vd);
+      if (__any_sync(0xffffffffu, move || (large & 0x40004000u))) {  // or a step of 2 or more
+        uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < 2 * nb; ++k) {
-          vd[k] &= keep[k / nb];
-          top = max(top, max(vd[k] & 0xffffu, vd[k] >> 16));
-        }
+        for (int k = 0; k < 2 * nb; ++k) top = max(top, max(ds[k] & 0xffffu, ds[k] >> 16));
         top = __reduce_max_sync(0xffffffffu, top);
-        float fo = 1.0f;
-        const float d = half_bits_to_float((uint16_t)top);
-        if (d > 0.0f && ldexpf(d, F) >= 2.0f) {
-          const int F2 = max(-15, min(15, -2 - ilogbf(d)));
-          fo = ldexpf(1.0f, F2 - F);
-          F = F2;
-          f2 = pow2_pair(F);
-#pragma unroll
-          for (int k = 0; k < 2 * nb; ++k) ds[k] = mul2(vd[k], f2);
-        }
+        const int E2 = max(E, (int)(top >> 10) - 15);  // its exponent
+        const float fo = pow2(E - E2);
+        E = E2;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float fr[2];
@@ -517,28 +564,21 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
             t = fmaxf(t, m[n][e]);
             fr[e] = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - t);
             m[n][e] = t;
-            ref[n][e] = t == -INFINITY ? 0.0f : t - kBoost;
+            ref[n][e] = t == -INFINITY ? 0.0f : t - kBoost + E;
+            fr[e] *= fo;
             l[n][e] *= fr[e];
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            oz[n][e] *= fr[e & 1] * (e >= 2 ? fo : 1.0f);
+            oz[n][e] *= fr[e & 1];
 #pragma unroll
-            for (int k = 0; k < 2 * nb; ++k) o[n][k][e] *= fr[e & 1] * fo;
+            for (int k = 0; k < 2 * nb; ++k) o[n][k][e] *= fr[e & 1];
           }
         }
       }
 
-      // ---- probabilities, turned into the B operand; their products with the midpoints (rows 0 to 7) and,
-      // where the codes are not centred, with the scaled steps (rows 8 to 15)
-      uint32_t vs[2] = {0u, 0u};
-      if constexpr (!kCentre) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t w = g < nb ? *reinterpret_cast<const uint32_t*>(tp + 18 * D + 8 * nb * c + 4 * (h * nb + g)) : 0u;
-          vs[h] = mul2(w & keep[h], f2);
-        }
-      }
+      // ---- probabilities, turned into the B operand; their products with the midpoints (rows 0 to 7) and the
+      // steps (rows 8 to 15)
       uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -575,19 +615,13 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
           for (int h = 0; h < 2; ++h) {
             const uint32_t d = ds[h * nb + b2];
             bh[n][h] = mul2(ph[n][h], d);
-            if constexpr (PS) bl[n][h] = fma2(pl[n][h], d, fma2(ph[n][h], d, bh[n][h] ^ 0x80008000u));
+            if constexpr (PS) bl[n][h] = fma2(pl[n][h], d, residue2(ph[n][h], d, bh[n][h]));
           }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
           uint32_t a0 = w0 & 0x000f000fu, a1 = w0 & 0x00f000f0u, a2 = w1 & 0x000f000fu, a3 = w1 & 0x00f000f0u;
-          if constexpr (kCentre) {
-            // (2 c - 15) 2^-24 and (16 c - 120) 2^-24: the low and the high nibbles less 7.5
-            a0 = fma2(a0, 0x40004000u, 0x800f800fu);
-            a1 = add2(a1, 0x80788078u);
-            a2 = fma2(a2, 0x40004000u, 0x800f800fu);
-            a3 = add2(a3, 0x80788078u);
-          }
+          if constexpr (kCentre) centre(a0, a2, a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bh[n][0], bh[n][1]);
@@ -601,7 +635,8 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
 
     // ---- the warp's result, in its ring: [row][D], in units of 2^(ref)
     float* res = reinterpret_cast<float*>(sm.ring[warp]);
-    const float u0 = ldexpf(1.0f, (kCentre ? 23 : 24) - F), u1 = ldexpf(1.0f, 20 - F), us = ldexpf(-7.5f, -F);
+    // low nibbles entered as c 2^-24, high ones as c 2^-20; centred, as c - 8 and 16 (c - 8)
+    constexpr float u0 = kCentre ? 1.0f : 0x1p24f, u1 = kCentre ? 0x1p-4f : 0x1p20f, us = kCentre ? 0.5f : -7.5f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -612,10 +647,10 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
         t += __shfl_xor_sync(0xffffffffu, t, 16);
         const int row = 8 * n + 2 * c + e;
         if (g == 0) {
-          sm.ref[warp][row] = m[n][e] - kBoost;
+          sm.ref[warp][row] = m[n][e] - kBoost + E;
           sm.sum[warp][row] = t;
         }
-        const float z0 = kCentre ? oz[n][e] : fmaf(us, oz[n][e + 2], oz[n][e]);
+        const float z0 = fmaf(us, oz[n][e + 2], oz[n][e]);
 #pragma unroll
         for (int b2 = 0; b2 < nb; ++b2) {
           const float z = __shfl_sync(0xffffffffu, z0, 4 * b2 + c);
@@ -630,16 +665,18 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
     }
     __syncthreads();
 
-    // A row's parts (ref, sum), k = 0 .. n - 1: the row's ref and sum, and the factor of each part.  A part
-    // without a finite score has ref -inf and sum 0 (or NaN, which must stay).
-    auto weigh = [&](int row, int n, auto part) {
+    // A row's parts k = 0 .. n - 1, in sm.ref and sm.sum: the row's ref and sum, and the factor of each part.
+    // A part without a finite score has ref -inf and sum 0 (or NaN, which must stay).
+    auto weigh = [&](int row, int n) {
       float top = -INFINITY, sum = 0.0f;
-      for (int k = 0; k < n; ++k) top = fmaxf(top, part(k).x);
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) top = fmaxf(top, sm.ref[k][row]);
+#pragma unroll 8
       for (int k = 0; k < n; ++k) {
-        const float2 rs = part(k);
-        const float f = rs.x == -INFINITY ? (rs.y == 0.0f ? 0.0f : 1.0f) : ex2(rs.x - top);
+        const float r = sm.ref[k][row], u = sm.sum[k][row];
+        const float f = r == -INFINITY ? (u == 0.0f ? 0.0f : 1.0f) : ex2(r - top);
         sm.factor[k][row] = f;
-        sum = fmaf(f, rs.y, sum);
+        sum = fmaf(f, u, sum);
       }
       sm.row_ref[row] = top;
       sm.row_sum[row] = sum;
@@ -654,21 +691,20 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
     };
 
     // ---- the CTA's result: to the outputs, or to a slot of the workspace
-    if (tid < n_rows) weigh(tid, kKv4Warps, [&](int k) { return make_float2(sm.ref[k][tid], sm.sum[k][tid]); });
+    if (tid < n_rows) weigh(tid, kWarps);
     __syncthreads();
-    // the CTA that has unit u: the largest i with total * i / n_ctas <= u
-    auto cta_of = [&](int64_t u) { return (int)(((u + 1) * n_ctas - 1) / total); };
-    const int first = cta_of(tiles0), last = cta_of(item1 - 1), parts = last - first + 1;
+    const int first = lo <= tiles0 ? cta : shares.cta_of(tiles0), last = hi >= item1 ? cta : shares.cta_of(item1 - 1);
+    const int parts = last - first + 1;
     // CTA i's part of this item: the second slot where CTA i has earlier items, else the first
     auto slot_of = [&](int i) {
-      return slots + (2 * (int64_t)i + (total * i / n_ctas < item0 ? 1 : 0)) * kv4_slot_floats(D);
+      return slots + (2 * (int64_t)i + (shares.begin(i) < item0 ? 1 : 0)) * kv4_slot_floats(D);
     };
     float* slot = parts > 1 ? slot_of(cta) : nullptr;
-    for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Threads) {
+    for (int idx = tid; idx < n_rows * (D / 4); idx += kThreads) {
       const int row = idx / (D / 4), d4 = idx - row * (D / 4);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float f = sm.factor[w][row];
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + row * D + 4 * d4);
         v.x = fmaf(f, x.x, v.x);
@@ -702,31 +738,47 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
       };
       // parts of CTAs from, from + step, ...: n of them, at most kJoin
       auto join = [&](int from, int step, int n, bool final) {
-        if (tid < n_rows)
-          weigh(tid, n, [&](int k) {
-            return __ldcg(reinterpret_cast<const float2*>(slot_of(from + k * step) + kRows * D + 2 * tid));
-          });
-        __syncthreads();
         const float* base = slot_of(from);
         const float* rest = slot_of(from + step);  // the others lie at equal distances: their first slots
         const int64_t stride = 2 * (int64_t)step * kv4_slot_floats(D);
-        for (int idx = tid; idx < n_rows * (D / 4); idx += kKv4Threads) {
-          const int row = idx / (D / 4), d4 = idx - row * (D / 4);
-          const int64_t off = row * D + 4 * d4;
-          float4 v = __ldcg(reinterpret_cast<const float4*>(base + off));
-          const float f0 = sm.factor[0][row];
-          v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
-#pragma unroll 8
-          for (int k = 1; k < n; ++k) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(rest + (k - 1) * stride + off));
-            const float f = sm.factor[k][row];
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
+        for (int idx = tid; idx < n * kRows; idx += kThreads) {
+          const int k = idx / kRows, row = idx % kRows;
+          if (row < n_rows) {
+            const float2 rs = __ldcg(reinterpret_cast<const float2*>((k ? rest + (k - 1) * stride : base) + kRows * D) + row);
+            sm.ref[k][row] = rs.x;
+            sm.sum[k][row] = rs.y;
           }
-          if (final) store_row(row, d4, v);
-          else *reinterpret_cast<float4*>(slot_of(from) + off) = v;
+        }
+        __syncthreads();
+        if (tid < n_rows) weigh(tid, n);
+        __syncthreads();
+        constexpr int kEach = (kRows * D / 4 + kThreads - 1) / kThreads;
+        float4 v[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const float* part = k ? rest + (k - 1) * stride : base;
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            const int idx = tid + e * kThreads;
+            if (idx < n_rows * (D / 4)) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(part) + idx);
+              const float f = sm.factor[k][idx / (D / 4)];
+              v[e].x = fmaf(f, x.x, v[e].x);
+              v[e].y = fmaf(f, x.y, v[e].y);
+              v[e].z = fmaf(f, x.z, v[e].z);
+              v[e].w = fmaf(f, x.w, v[e].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int idx = tid + e * kThreads;
+          if (idx < n_rows * (D / 4)) {
+            if (final) store_row(idx / (D / 4), idx % (D / 4), v[e]);
+            else reinterpret_cast<float4*>(slot_of(from))[idx] = v[e];
+          }
         }
         if (!final && tid < n_rows)
           *reinterpret_cast<float2*>(slot_of(from) + kRows * D + 2 * tid) =
@@ -749,8 +801,9 @@ __global__ void __launch_bounds__(kKv4Threads, (D <= 128 && NT == 1) || D == 64 
 
 template <int D, int NT, bool QS, bool PS, typename T>
 int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
-  auto kern = kv4_attention_kernel<D, NT, QS, PS, T>;
-  constexpr int kSmem = (int)sizeof(Smem<D, NT, QS>);
+  using S = Shape<D, NT, QS>;
+  auto kern = kv4_attention_kernel<S, PS, T>;
+  constexpr int kSmem = (int)sizeof(Smem<S>);
   static int per_device[64];  // CTAs of a full launch, by device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MMVQ_ERR_CUDA;
@@ -759,7 +812,7 @@ int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
     int sms = 0, per_sm = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kKv4Threads, kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, S::kThreads, kSmem) != cudaSuccess ||
         per_sm < 1)
       return MMVQ_ERR_CUDA;
     ctas = min(sms * per_sm, kKv4MaxCtas);
@@ -771,7 +824,7 @@ int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
                         (a.ld_table * (a.page_tokens / kKv4Tile) + kKv4ItemUnits);
   const int64_t most = (units + kKv4MinUnits - 1) / kKv4MinUnits;
   const int grid = (int)(most < ctas ? most : ctas);
-  return launch_pdl(kern, dim3(grid), dim3(kKv4Threads), kSmem, stream, a, p);
+  return launch_pdl(kern, dim3(grid), dim3(S::kThreads), kSmem, stream, a, p);
 }
 
 template <int D, bool QS, bool PS, typename T>

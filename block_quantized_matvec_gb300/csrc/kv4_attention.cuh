@@ -29,12 +29,10 @@ struct Kv4Attention {
   int page_shift;
 };
 
-constexpr int kKv4Warps = 8;          // warps of an attention CTA
-constexpr int kKv4Threads = 32 * kKv4Warps;
 constexpr int kKv4MaxRows = 16;       // rows of a block (NT = 2)
 constexpr int kKv4MaxCtas = 1024;     // of a launch
-constexpr int kKv4ItemUnits = 16;     // what an item costs besides its tiles
-constexpr int kKv4MinUnits = 24;      // of a CTA: below, fewer CTAs take part
+constexpr int kKv4ItemUnits = 24;     // what an item costs besides its tiles
+constexpr int kKv4MinUnits = 32;      // of a CTA: below, fewer CTAs take part
 
 // Workspace: join counters (two per CTA for the groups of a split item, one for
 // the groups' results), then two partial results per CTA.
