@@ -71,16 +71,16 @@ __device__ __forceinline__ bool kv4_place(const Kv4Batch& a, int r, int lane, in
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;
-    const bool starts = lane * step < n && __ldg(a.offsets + i) <= r;
+    const bool starts = lane * step < n && a.offsets[i] <= r;
     const uint32_t m = __ballot_sync(0xffffffffu, starts);
     const int last = m ? 31 - __clz(m) : 0;
     n = min(step, n - last * step);
     lo += last * step;
   }
   b = lo;
-  const int first = __ldg(a.offsets + b), end = __ldg(a.offsets + b + 1);
+  const int first = a.offsets[b], end = a.offsets[b + 1];
   if (r < first || r >= end) return false;
-  pos = __ldg(a.lens + b) - (end - r);
+  pos = a.lens[b] - (end - r);
   return true;
 }
 
@@ -90,7 +90,7 @@ __device__ __forceinline__ uint8_t* kv4_tile(const Kv4Batch& a, int tile_bytes, 
   const int per_page = a.page_tokens / kKv4Tile;
   const int pi = tile / per_page;
   if (pi >= a.ld_table) return nullptr;
-  const int64_t page = __ldg(a.page_table + (int64_t)b * a.ld_table + pi);
+  const int64_t page = a.page_table[(int64_t)b * a.ld_table + pi];
   if (page < 0 || page >= a.n_pages) return nullptr;
   return a.cache + (page * a.n_kv_heads * per_page + (tile - pi * per_page)) * tile_bytes;
 }

@@ -158,7 +158,7 @@ __device__ __forceinline__ void load_values(const T* src, bool vector, float (&q
     if (vector) {
 #pragma unroll
       for (int k = 0; k < N / kEach; ++k) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
+        const uint4 v = reinterpret_cast<const uint4*>(src)[k];
         const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) q[kEach * k + i] = kv4_load(e + i);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       const int tile = tile_of(next);
       const int pi = (int)(((uint64_t)(uint32_t)tile * p.page_mul) >> p.page_shift);
       next_at = tile - pi * per_page;
-      next_page = next < tile1 && pi < a.ld_table && (int64_t)tile * kKv4Tile < s.len ? __ldg(table + pi) : -1;
+      next_page = next < tile1 && pi < a.ld_table && (int64_t)tile * kKv4Tile < s.len ? table[pi] : -1;
     };
     auto fetch = [&](int stage) {
       const bool there = next_page >= 0 && next_page < a.n_pages;

@@ -54,10 +54,10 @@ struct Kv4Seq {
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Batch& a, const Kv4Attention& p, int rows_block,
                                           int b, int* error) {
   Kv4Seq s;
-  s.first = __ldg(a.offsets + b);
-  const int end = __ldg(a.offsets + b + 1);
+  s.first = a.offsets[b];
+  const int end = a.offsets[b + 1];
   s.n_new = end - s.first;
-  s.len = max(0, __ldg(a.lens + b));
+  s.len = max(0, a.lens[b]);
   if (s.n_new < 0 || s.n_new > kKv4MaxNew || s.first < 0 || end > a.n_tokens) {
     *error = s.n_new > kKv4MaxNew && s.first >= 0 && end <= a.n_tokens ? MMVQ_ERR_NCOLS
                                                                         : MMVQ_ERR_ROUTING;
