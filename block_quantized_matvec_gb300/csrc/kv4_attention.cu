@@ -4,7 +4,7 @@
 // S^T[tokens x rows] = K Q^T from m16n8k16 f16 products whose A operand is the
 // tile's codes: masked out of its word a code c stands, as the bits of an
 // fp16, for c * 2^-24 (low nibble of a byte) or c * 2^-20 (high nibble), so a
-// key costs no conversion; for fp32 queries it becomes c - 8 (centre() below).
+// key costs no conversion; for fp32 queries it becomes c - 8 (centred() below).
 // The rows of Q are scaled by a power of two each, and by 16 more where they
 // meet low nibbles.  Per block of 32 the sum is multiplied by the block's d in
 // fp32; sum(z sum(q)) and sum(d sum(q)) (the codes' offset) over the blocks
@@ -18,23 +18,12 @@
 // the products p d do too; bf16 keeps 11 bits of p d, finer than its own 8.
 // Every sum is fp32 (in the tensor core or outside).
 #include "kv4.cuh"
-#include "kv4_attention.cuh"
+#include "kv4_work.cuh"
 
 namespace mmvq {
 namespace {
 
 constexpr int kStages = 4;
-constexpr float kLazy = 2.0f;    // slack of the reference, log2 units
-constexpr int kJoin = 32;        // parts that are joined at a time: sqrt(kKv4MaxCtas)
-constexpr int kJoinAtOnce = 12;  // more are joined in two steps
-constexpr float kBoost = 12.0f;  // p is at most 2^(kLazy + kBoost) = 2^14, below fp16's largest
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -57,18 +46,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  return u32(__hmul2_rn(h2(a), h2(b)));
-}
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
-  return u32(__hfma2(h2(a), h2(b), h2(c)));
-}
-__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
-  return u32(__hadd2_rn(h2(a), h2(b)));
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -80,36 +57,26 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 2^e, -126 <= e <= 127, and the exponent of a positive normal x.
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }
-
-// a / b of unsigned numbers: most fit 32 bits, whose division is several times shorter.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
-// The division of `total` units among n CTAs: the first `more` have share + 1.
-struct Shares {
-  int64_t share, more;
-  __device__ __forceinline__ Shares(int64_t total, int n) : share(divide(total, n)), more(total - share * n) {}
-  __device__ __forceinline__ int64_t begin(int i) const { return i * share + min((int64_t)i, more); }
-  __device__ __forceinline__ int cta_of(int64_t unit) const {
-    const int64_t large = more * (share + 1);
-    return (int)(unit < large ? divide(unit, share + 1) : more + divide(unit - large, share));
-  }
-};
-
-// Codes masked out of a word, low nibbles in a0 and a1, high ones in a2 and a3, become c - 8 and 16 (c - 8):
-// set below 1024 as the mantissa's last bits, exactly, then 1024 and the centre are taken off.  The tensor core
+// The codes of two words, low nibbles in a0 and a1, high ones in a2 and a3: as they are, or as c - 8 and 16 (c - 8),
+// set below 1024 as the mantissa's last bits, exactly, from which 1024 and the centre are taken off.  The tensor core
 // aligns a subnormal by its nominal exponent and cuts off what lies far below it (sums then keep about 17 bits);
 // these are normal numbers.
-__device__ __forceinline__ void centre(uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
-  a0 = add2(a0 | 0x64006400u, 0xe408e408u);  // - 1032
-  a1 = add2(a1 | 0x64006400u, 0xe408e408u);
-  a2 = add2(a2 | 0x64006400u, 0xe480e480u);  // - 1152
-  a3 = add2(a3 | 0x64006400u, 0xe480e480u);
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {  // one instruction
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ void centred(uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1, uint32_t& a2,
+                                        uint32_t& a3) {
+  a0 = add2(and_or(w0, 0x000f000fu, 0x64006400u), 0xe408e408u);  // - 1032
+  a1 = add2(and_or(w1, 0x000f000fu, 0x64006400u), 0xe408e408u);
+  a2 = add2(and_or(w0, 0x00f000f0u, 0x64006400u), 0xe480e480u);  // - 1152
+  a3 = add2(and_or(w1, 0x00f000f0u, 0x64006400u), 0xe480e480u);
+}
+__device__ __forceinline__ void plain(uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1, uint32_t& a2,
+                                      uint32_t& a3) {
+  a0 = w0 & 0x000f000fu, a1 = w1 & 0x000f000fu;
+  a2 = w0 & 0x00f000f0u, a3 = w1 & 0x00f000f0u;
 }
 
 // a b - c, rounded once: what a product c = a b lost in rounding, exactly.
@@ -141,34 +108,10 @@ struct Smem {
   __half q_sum[S::kRows][S::kGroups][4][S::kOfGroup];  // sum(q) of a block, and its multiple for d, in two parts each
   float row_factor[S::kRows];
   int row_pos[S::kRows];
-  float ref[kJoin][S::kRows], sum[kJoin][S::kRows], factor[kJoin][S::kRows];  // of the warps, or of an item's parts
-  float row_ref[S::kRows], row_sum[S::kRows];
-  int64_t before[S::kThreads];      // units before each thread's sequences
-  int64_t warp_units[S::kWarps];
-  Kv4Seq seq[S::kThreads];          // where each thread has one sequence
-  int last;
+  Kv4JoinSmem<S::kRows> join;       // of the warps' results, then of an item's parts
+  Kv4Plan<S::kThreads, true> plan;
   static_assert(kRing >= S::kRows * S::D * 4, "a warp's results fit its ring");
 };
-
-// N values from src in fp32; `vector`: src is 16-byte aligned.
-template <int N, typename T>
-__device__ __forceinline__ void load_values(const T* src, bool vector, float (&q)[N]) {
-  constexpr int kEach = 16 / sizeof(T);
-  if constexpr (N % kEach == 0) {
-    if (vector) {
-#pragma unroll
-      for (int k = 0; k < N / kEach; ++k) {
-        const uint4 v = reinterpret_cast<const uint4*>(src)[k];
-        const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) q[kEach * k + i] = kv4_load(e + i);
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) q[i] = kv4_load(src + i);
-}
 
 // The query rows of a block into q, q_sum, row_factor and row_pos, by the first 8 warps.
 template <typename S, typename T>
@@ -185,7 +128,7 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   const int t = on ? r / group : 0;
   float q[kOwn], top = 0.0f;
   if (on) {
-    load_values(static_cast<const T*>(p.q) + (int64_t)(s.first + t) * p.ldq +
+    kv4_load_values(static_cast<const T*>(p.q) + (int64_t)(s.first + t) * p.ldq +
                     (int64_t)(head * group + r - t * group) * p.hq + sub * kOwn,
                 p.q_vector, q);
   } else {
@@ -198,7 +141,7 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   for (int o = 1; o < kPer; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   // largest |q| into [2^6, 2^7): 16 q, and 7.5 times a sum of 32, stay below fp16's largest
   const int e = top > 0.0f && top < INFINITY ? min(6 - exponent(top), 126) : 0;
-  const float f = pow2(e);
+  const float f = p.scale < 0.0f ? -pow2(e) : pow2(e);  // the factor of the scores is not negative
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) q[i] *= f;
 #pragma unroll
@@ -232,7 +175,8 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
     // a power of two in two steps: it can pass fp32's range where the product does not
     constexpr int kUnit = QS ? -4 : 20;
     const int f2 = kUnit - e;
-    sm.row_factor[row] = p.scale * 1.4426950408889634f * pow2(f2 / 2) * pow2(f2 - f2 / 2);
+    const float factor = fabsf(p.scale) * 1.4426950408889634f * pow2(f2 / 2) * pow2(f2 - f2 / 2);
+    sm.row_factor[row] = fminf(fmaxf(factor, 1e-37f), 1e37f);  // not 0: masked scores are -inf
     sm.row_pos[row] = on ? s.len - s.n_new + t : -1;
   }
 }
@@ -279,109 +223,75 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   // The next kernel may be launched now: whatever it is, it waits for this one's results
   grid_launch_dependents();
 
-  // ---- the batch's units, and this CTA's share of them
-  const int chunk = (a.n_seqs + kThreads - 1) / kThreads;
-  int error = 0;
-  int64_t mine = 0;
-  for (int b = tid * chunk; b < min(a.n_seqs, (tid + 1) * chunk); ++b) {
-    const Kv4Seq s = kv4_seq(a, p, kRows, b, &error);
-    if (chunk == 1) sm.seq[tid] = s;
-    mine += (int64_t)a.n_kv_heads * s.blocks * s.item_units();
-  }
-  if (error && blockIdx.x == 0) kv4_set_status(a.status, error);
-  int64_t up_to = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, up_to, o);
-    if (lane >= o) up_to += x;
-  }
-  if (lane == 31) sm.warp_units[warp] = up_to;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) up_to += sm.warp_units[w];
-    total += sm.warp_units[w];
-  }
-  sm.before[tid] = up_to - mine;
-  __syncthreads();
-  const int n_ctas = (int)min((int64_t)gridDim.x, (total + kKv4MinUnits - 1) / kKv4MinUnits);
-  const int cta = blockIdx.x;
+  const int64_t total = kv4_plan(a, p, kRows, sm.plan, tid);
+  const int n_ctas = kv4_ctas(total), cta = blockIdx.x;
   if (cta >= n_ctas) return;
   const Shares shares(total, n_ctas);
-  const int64_t lo = shares.begin(cta), hi = shares.begin(cta + 1);
-  const int group = p.n_heads / a.n_kv_heads;
   const int per_page = a.page_tokens / kKv4Tile;
-  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kKv4CounterBytes);
-  uint32_t* counters = static_cast<uint32_t*>(p.workspace);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]) + lane * 16;
 
-  for (int64_t unit = lo; unit < hi;) {
-    // ---- the item of this unit: its sequence by a search over the threads' sums
-    int th = 0;
-#pragma unroll
-    for (int o = 256; o > 0; o >>= 1)
-      if (th + o < kThreads && sm.before[th + o] <= unit) th += o;
-    int b = th * chunk;
-    int64_t at = sm.before[th];
-    Kv4Seq s = chunk == 1 ? sm.seq[th] : kv4_seq(a, p, kRows, b, &error);
-    for (;;) {
-      const int64_t units = (int64_t)a.n_kv_heads * s.blocks * s.item_units();
-      if (at + units > unit) break;
-      at += units;
-      s = kv4_seq(a, p, kRows, ++b, &error);
-    }
-    const int item = (int)divide(unit - at, s.item_units());
-    const int64_t item0 = at + (int64_t)item * s.item_units(), item1 = item0 + s.item_units();
-    // its units from kKv4ItemUnits on are its tiles
-    const int64_t tiles0 = item0 + kKv4ItemUnits;
-    const int tile0 = (int)max(unit - tiles0, (int64_t)0), tile1 = (int)(min(hi, item1) - tiles0);
-    unit = min(hi, item1);
-    if (tile1 <= tile0) continue;
-    const int head = item / s.blocks, row0 = (item - head * s.blocks) * kRows;
-    const int n_rows = min(kRows, s.n_new * group - row0);
+  for (int64_t unit = shares.begin(cta); unit < shares.begin(cta + 1);) {
+    Kv4Item it;
+    if (!kv4_next(a, p, kRows, sm.plan, shares, cta, unit, it)) continue;
+    const Kv4Seq& s = it.s;
+    const int tile0 = it.tile0, tile1 = it.tile1, n_rows = it.n_rows;
 
     __syncthreads();  // the item before is done with the shared memory
 
-    // ---- tiles tile0 + warp, + kWarps, ... through the warp's ring; the page of the next is looked up
-    // a tile ahead, and the last bits of `present` say which of the fetched tiles are there
-    const uint8_t* head_base = a.cache + (int64_t)head * per_page * kv4_tile_bytes(D);
+    // ---- the warp's share of the tiles, one after the other through its ring; the page after a tile's is looked
+    // up with it, and the last bits of `present` say which of the fetched tiles are there
+    const int begin = tile0 + (tile1 - tile0) * warp / kWarps, end = tile0 + (tile1 - tile0) * (warp + 1) / kWarps;
+    const uint8_t* head_base = a.cache + (int64_t)it.head * per_page * kv4_tile_bytes(D) + lane * 16;
     const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kv4_tile_bytes(D);
-    const int32_t* table = a.page_table + (int64_t)b * a.ld_table;
+    const int32_t* table = a.page_table + (int64_t)it.b * a.ld_table;
     const int pos_lo = s.len - s.n_new;  // of the sequence's rows
     auto tile_of = [&](int i) { return i + (i >= s.sink_tiles ? s.skip : 0); };
+    const int gap = s.skip > 0 ? s.sink_tiles : -1;  // the tile before which some are skipped
     uint32_t present = 0;
-    int next = tile0 + warp, next_page = -1, next_at = 0;
-    auto look_up = [&]() {
+    int next = begin, pi = 0, in_page = 0, page_after = -1;
+    bool there = false;
+    const uint8_t* src = head_base;
+    auto page_at = [&](int i) { return i < a.ld_table && s.len > 0 ? table[i] : -1; };
+    auto enter = [&](int page) {  // page pi of the table
+      there = page >= 0 && page < a.n_pages;
+      src = head_base + page * page_bytes + in_page * kv4_tile_bytes(D);
+      page_after = page_at(pi + 1);
+    };
+    auto find = [&]() {  // where tile `next` lies
       const int tile = tile_of(next);
-      const int pi = (int)(((uint64_t)(uint32_t)tile * p.page_mul) >> p.page_shift);
-      next_at = tile - pi * per_page;
-      next_page = next < tile1 && pi < a.ld_table && (int64_t)tile * kKv4Tile < s.len ? table[pi] : -1;
+      pi = (int)(((uint64_t)(uint32_t)tile * p.page_mul) >> p.page_shift);
+      in_page = tile - pi * per_page;
+      enter(page_at(pi));
     };
     auto fetch = [&](int stage) {
-      const bool there = next_page >= 0 && next_page < a.n_pages;
-      present = present << 1 | (there ? 1u : 0u);
-      if (there) {
-        const uint8_t* src = head_base + next_page * page_bytes + next_at * kv4_tile_bytes(D);
+      const bool on = next < end && there;
+      present = present << 1 | (on ? 1u : 0u);
+      if (on) {
         const uint32_t dst = ring + stage * kBytes;
 #pragma unroll
         for (int k = 0; k < (kBytes + 511) / 512; ++k)
-          if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes)
-            cp_async16(dst + k * 512 + lane * 16, src + k * 512 + lane * 16);
+          if ((k + 1) * 512 <= kBytes || k * 512 + lane * 16 < kBytes) cp_async16(dst + k * 512, src + k * 512);
       }
       cp_async_commit();
-      next += kWarps;
-      look_up();
+      if (++next == gap) {
+        find();
+      } else if (++in_page == per_page) {
+        in_page = 0;
+        ++pi;
+        enter(page_after);
+      } else {
+        src += kv4_tile_bytes(D);
+      }
     };
-    look_up();
+    if (begin < end) find();
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(k);
 
-    load_queries<S, T>(a, p, sm, s, head, row0, tid);
+    load_queries<S, T>(a, p, sm, s, it.head, it.row0, tid);
     __syncthreads();
 
     // ---- what a lane keeps of the queries: columns 2c, 2c + 1 of each row tile
-    float fac[NT][2];
+    float fac[NT][2], slack[NT][2];
     int pos[NT][2];
     uint32_t qz[NT][kGroups][2];  // B operands of the products with midpoints and steps
 #pragma unroll
@@ -389,6 +299,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         fac[n][e] = sm.row_factor[8 * n + 2 * c + e];
+        slack[n][e] = kKv4Lazy / fac[n][e];
         pos[n][e] = sm.row_pos[8 * n + 2 * c + e];
       }
       // k positions: of 4 blocks, both parts of sum(q), then both of -7.5 sum(q); of 2, all four at once
@@ -399,7 +310,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         qz[n][k][1] = nb == 2 ? 0u : qs[4 + c];
       }
     }
-    float o[NT][2 * nb][4], oz[NT][4], m[NT][2], ref[NT][2], l[NT][2];
+    float o[NT][2 * nb][4], oz[NT][4], bar[NT][2], ref[NT][2], l[NT][2];  // bar: a score above it moves ref
     int E = 0;  // p is smaller by 2^E where steps reach 2^(E + 1): p d stays in fp16's range
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -409,21 +320,21 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) oz[n][e] = 0.0f;
-      m[n][0] = m[n][1] = -INFINITY;
+      bar[n][0] = bar[n][1] = -INFINITY;
       ref[n][0] = ref[n][1] = 0.0f;
       l[n][0] = l[n][1] = 0.0f;
     }
 
     int stage = 0;
-    for (int i = tile0 + warp; i < tile1; i += kWarps) {
+    for (int i = begin; i < end; ++i) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      const bool there = present >> (kStages - 2) & 1;
+      const bool on = present >> (kStages - 2) & 1;
       fetch((stage + kStages - 1) % kStages);
       const uint8_t* tp = sm.ring[warp] + stage * kBytes;
       stage = (stage + 1) % kStages;
       const int key0 = tile_of(i) * kKv4Tile;
-      if (!there) {
+      if (!on) {
         if (lane == 0 && key0 < s.len) kv4_set_status(a.status, MMVQ_ERR_ROUTING);
         continue;
       }
@@ -468,9 +379,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = kw[b2] >> (8 * hh), w1 = kw[nb + b2] >> (8 * hh);
-          ka[hh][0] = w0 & 0x000f000fu, ka[hh][1] = w1 & 0x000f000fu;
-          ka[hh][2] = w0 & 0x00f000f0u, ka[hh][3] = w1 & 0x00f000f0u;
-          if constexpr (QS) centre(ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
+          if constexpr (QS) centred(w0, w1, ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
+          else plain(w0, w1, ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -503,10 +413,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         vs[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at) : 0u;
         vz[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at + D) : 0u;
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] *= fac[n][e & 1];
 
       // ---- masks: a tile that every row sees in full needs none
       const bool all = key0 + kKv4Tile - 1 <= pos_lo &&
@@ -543,14 +449,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + kLazy;
+        for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > bar[n][e];
       if (__any_sync(0xffffffffu, move || (large & 0x40004000u))) {  // or a step of 2 or more
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < 2 * nb; ++k) top = max(top, max(ds[k] & 0xffffu, ds[k] >> 16));
         top = __reduce_max_sync(0xffffffffu, top);
         const int E2 = max(E, (int)(top >> 10) - 15);  // its exponent
-        const float fo = pow2(E - E2);
+        const int E1 = E;
         E = E2;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -561,11 +467,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            t = fmaxf(t, m[n][e]);
-            fr[e] = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - t);
-            m[n][e] = t;
-            ref[n][e] = t == -INFINITY ? 0.0f : t - kBoost + E;
-            fr[e] *= fo;
+            // ref = (largest score) * fac - kKv4Boost + E, from none (bar -inf, ref 0) or the last one on
+            const bool none = bar[n][e] == -INFINITY, some = t > -INFINITY;
+            float r = t * fac[n][e] - kKv4Boost;
+            if (!none) r = fmaxf(r, ref[n][e] - E1);
+            if (none && !some) r = -E;
+            r += E;
+            fr[e] = none ? 0.0f : ex2(ref[n][e] - r);
+            ref[n][e] = r;
+            bar[n][e] = fmaxf(bar[n][e], t + slack[n][e]);
             l[n][e] *= fr[e];
           }
 #pragma unroll
@@ -584,7 +494,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       for (int n = 0; n < NT; ++n) {
         float pr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2(x[n][e] - ref[n][e & 1]);
+        for (int e = 0; e < 4; ++e) pr[e] = ex2(fmaf(x[n][e], fac[n][e & 1], -ref[n][e & 1]));
         l[n][0] += pr[0] + pr[2];
         l[n][1] += pr[1] + pr[3];
 #pragma unroll
@@ -620,8 +530,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
-          uint32_t a0 = w0 & 0x000f000fu, a1 = w0 & 0x00f000f0u, a2 = w1 & 0x000f000fu, a3 = w1 & 0x00f000f0u;
-          if constexpr (kCentre) centre(a0, a2, a1, a3);
+          uint32_t a0, a1, a2, a3;
+          if constexpr (kCentre) centred(w0, w1, a0, a2, a1, a3);
+          else plain(w0, w1, a0, a2, a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bh[n][0], bh[n][1]);
@@ -647,8 +558,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         t += __shfl_xor_sync(0xffffffffu, t, 16);
         const int row = 8 * n + 2 * c + e;
         if (g == 0) {
-          sm.ref[warp][row] = m[n][e] - kBoost + E;
-          sm.sum[warp][row] = t;
+          sm.join.ref[warp][row] = bar[n][e] == -INFINITY ? -INFINITY : ref[n][e];
+          sm.join.sum[warp][row] = t;
         }
         const float z0 = fmaf(us, oz[n][e + 2], oz[n][e]);
 #pragma unroll
@@ -665,137 +576,32 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     }
     __syncthreads();
 
-    // A row's parts k = 0 .. n - 1, in sm.ref and sm.sum: the row's ref and sum, and the factor of each part.
-    // A part without a finite score has ref -inf and sum 0 (or NaN, which must stay).
-    auto weigh = [&](int row, int n) {
-      float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) top = fmaxf(top, sm.ref[k][row]);
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        const float r = sm.ref[k][row], u = sm.sum[k][row];
-        const float f = r == -INFINITY ? (u == 0.0f ? 0.0f : 1.0f) : ex2(r - top);
-        sm.factor[k][row] = f;
-        sum = fmaf(f, u, sum);
-      }
-      sm.row_ref[row] = top;
-      sm.row_sum[row] = sum;
-    };
-    auto store_row = [&](int row, int d4, float4 v) {
-      const int r = row0 + row, t = r / group;
-      const int64_t out = (int64_t)(s.first + t) * p.n_heads + head * group + (r - t * group);
-      const float sum = sm.row_sum[row], inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-      kv4_store4(static_cast<T*>(p.y) + out * D + 4 * d4, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-      if (p.lse && d4 == 0)
-        p.lse[out] = sum == 0.0f ? -INFINITY : (sm.row_ref[row] + log2f(sum)) * 0.6931471805599453f;
-    };
-
     // ---- the CTA's result: to the outputs, or to a slot of the workspace
-    if (tid < n_rows) weigh(tid, kWarps);
+    if (tid < n_rows) sm.join.weigh(tid, kWarps);
     __syncthreads();
-    const int first = lo <= tiles0 ? cta : shares.cta_of(tiles0), last = hi >= item1 ? cta : shares.cta_of(item1 - 1);
-    const int parts = last - first + 1;
-    // CTA i's part of this item: the second slot where CTA i has earlier items, else the first
-    auto slot_of = [&](int i) {
-      return slots + (2 * (int64_t)i + (shares.begin(i) < item0 ? 1 : 0)) * kv4_slot_floats(D);
-    };
-    float* slot = parts > 1 ? slot_of(cta) : nullptr;
+    float* slot = it.last > it.first ? kv4_slot<kRows, D>(p, shares, it, cta) : nullptr;
     for (int idx = tid; idx < n_rows * (D / 4); idx += kThreads) {
       const int row = idx / (D / 4), d4 = idx - row * (D / 4);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = sm.factor[w][row];
+        const float f = sm.join.factor[w][row];
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + row * D + 4 * d4);
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
         v.z = fmaf(f, x.z, v.z);
         v.w = fmaf(f, x.w, v.w);
       }
-      if (parts == 1) {
-        store_row(row, d4, v);
+      if (!slot) {
+        kv4_store_row<T>(a, p, it, D, row, d4, v, sm.join.row_ref[row], sm.join.row_sum[row]);
       } else {
         *reinterpret_cast<float4*>(slot + row * D + 4 * d4) = v;
         if (d4 == 0)
-          *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(sm.row_ref[row], sm.row_sum[row]);
+          *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) =
+              make_float2(sm.join.row_ref[row], sm.join.row_sum[row]);
       }
     }
-
-    // ---- joining the parts of a split item: in groups by the last CTA of a group to arrive, then the
-    // groups by the last group's; always added in the order of the CTAs
-    if (parts > 1) {
-      auto arrive = [&](uint32_t* counter, int n) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const bool is_last = atomicAdd(counter, 1u) == (uint32_t)n - 1u;
-          if (is_last) *counter = 0u;
-          sm.last = is_last;
-        }
-        __syncthreads();
-        __threadfence();
-        return sm.last != 0;
-      };
-      // parts of CTAs from, from + step, ...: n of them, at most kJoin
-      auto join = [&](int from, int step, int n, bool final) {
-        const float* base = slot_of(from);
-        const float* rest = slot_of(from + step);  // the others lie at equal distances: their first slots
-        const int64_t stride = 2 * (int64_t)step * kv4_slot_floats(D);
-        for (int idx = tid; idx < n * kRows; idx += kThreads) {
-          const int k = idx / kRows, row = idx % kRows;
-          if (row < n_rows) {
-            const float2 rs = __ldcg(reinterpret_cast<const float2*>((k ? rest + (k - 1) * stride : base) + kRows * D) + row);
-            sm.ref[k][row] = rs.x;
-            sm.sum[k][row] = rs.y;
-          }
-        }
-        __syncthreads();
-        if (tid < n_rows) weigh(tid, n);
-        __syncthreads();
-        constexpr int kEach = (kRows * D / 4 + kThreads - 1) / kThreads;
-        float4 v[kEach];
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-          const float* part = k ? rest + (k - 1) * stride : base;
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            const int idx = tid + e * kThreads;
-            if (idx < n_rows * (D / 4)) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(part) + idx);
-              const float f = sm.factor[k][idx / (D / 4)];
-              v[e].x = fmaf(f, x.x, v[e].x);
-              v[e].y = fmaf(f, x.y, v[e].y);
-              v[e].z = fmaf(f, x.z, v[e].z);
-              v[e].w = fmaf(f, x.w, v[e].w);
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-          const int idx = tid + e * kThreads;
-          if (idx < n_rows * (D / 4)) {
-            if (final) store_row(idx / (D / 4), idx % (D / 4), v[e]);
-            else reinterpret_cast<float4*>(slot_of(from))[idx] = v[e];
-          }
-        }
-        if (!final && tid < n_rows)
-          *reinterpret_cast<float2*>(slot_of(from) + kRows * D + 2 * tid) =
-              make_float2(sm.row_ref[tid], sm.row_sum[tid]);
-      };
-      int per = parts;
-      if (parts > kJoinAtOnce) {
-        per = 1;
-        while (per * per < parts) ++per;
-      }
-      const int grp = (cta - first) / per, from = first + grp * per, n = min(per, last + 1 - from);
-      const int n_groups = (parts + per - 1) / per;
-      if (arrive(counters + 2 * from + (grp == 0 ? 1 : 0), n)) {
-        join(from, 1, n, n_groups == 1);
-        if (n_groups > 1 && arrive(counters + 2 * kKv4MaxCtas + first, n_groups)) join(first, per, n_groups, true);
-      }
-    }
+    if (slot) kv4_join<kThreads, kRows, D, T>(a, p, shares, it, cta, sm.join, tid);
   }
 }
 
@@ -859,7 +665,7 @@ int launch_kv4_attention(const Kv4Batch& a, const Kv4Attention& args, int D, int
 }
 
 int64_t kv4_attention_workspace_bytes(int D) {
-  return kKv4CounterBytes + 2 * kKv4MaxCtas * kv4_slot_floats(D) * 4;
+  return kKv4CounterBytes + 2 * kKv4MaxCtas * kv4_slot_floats(kKv4MaxRows, D) * 4;
 }
 
 }  // namespace mmvq

@@ -29,15 +29,15 @@ struct Kv4Attention {
   int page_shift;
 };
 
-constexpr int kKv4MaxRows = 16;       // rows of a block (NT = 2)
 constexpr int kKv4MaxCtas = 1024;     // of a launch
-constexpr int kKv4ItemUnits = 24;     // what an item costs besides its tiles
-constexpr int kKv4MinUnits = 32;      // of a CTA: below, fewer CTAs take part
+constexpr int kKv4ItemUnits = 32;     // what an item costs besides its tiles
+constexpr int kKv4MinUnits = 24;      // of a CTA: below, fewer CTAs take part
 
 // Workspace: join counters (two per CTA for the groups of a split item, one for
 // the groups' results), then two partial results per CTA.
+constexpr int kKv4MaxRows = 16;       // rows of a block (NT = 2)
 constexpr int kKv4CounterBytes = kKv4MaxCtas * 3 * 4;
-__host__ __device__ constexpr int64_t kv4_slot_floats(int D) { return (int64_t)kKv4MaxRows * (D + 2); }
+__host__ __device__ constexpr int64_t kv4_slot_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
 
 // What a sequence asks for.
 struct Kv4Seq {
