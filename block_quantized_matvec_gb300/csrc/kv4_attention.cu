@@ -32,6 +32,15 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from zero.
+__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
       "{%0,%1,%2,%3};"
@@ -91,10 +100,10 @@ struct Shape {
   static constexpr bool QS = QS_;
   static constexpr int nb = D / 32, kGroups = nb > 4 ? nb / 4 : 1, kOfGroup = nb / kGroups;  // blocks
   static constexpr int kRows = 8 * NT;
-  // two CTAs of 8 warps and 128 registers a thread; one of 12 and 168 or of 8 and 255 where the accumulators
+  // four CTAs of 4 warps and 128 registers a thread; one of 12 and 168 or of 8 and 255 where the accumulators
   // (4 registers per 16 values and row tile) need them
-  static constexpr int kWarps = D == 128 && NT == 2 ? 12 : 8;
-  static constexpr int kCtas = D * NT <= 128 ? 2 : 1;
+  static constexpr int kWarps = D * NT <= 128 ? 4 : D == 128 ? 12 : 8;
+  static constexpr int kCtas = D * NT <= 128 ? 4 : 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kBytes = kv4_tile_bytes(D);
 };
@@ -113,14 +122,15 @@ struct Smem {
   static_assert(kRing >= S::kRows * S::D * 4, "a warp's results fit its ring");
 };
 
-// The query rows of a block into q, q_sum, row_factor and row_pos, by the first 8 warps.
+// The query rows of a block into q, q_sum, row_factor and row_pos, by 8 warps at most.
 template <typename S, typename T>
 __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attention& p, Smem<S>& sm,
                                              const Kv4Seq& s, int head, int row0, int tid) {
   constexpr int D = S::D, NT = S::NT;
   constexpr bool QS = S::QS;
-  constexpr int kPer = 32 / NT, kOwn = D / kPer;  // threads a row, values a thread
-  if (tid >= 256) return;
+  constexpr int kUsed = S::kThreads < 256 ? S::kThreads : 256;
+  constexpr int kPer = kUsed / S::kRows, kOwn = D / kPer;  // threads a row, values a thread
+  if (tid >= kUsed) return;
   const int row = tid / kPer, sub = tid % kPer;
   const int group = p.n_heads / a.n_kv_heads;
   const int r = row0 + row;
@@ -139,8 +149,9 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   for (int i = 0; i < kOwn; ++i) top = fmaxf(top, fabsf(q[i]));
 #pragma unroll
   for (int o = 1; o < kPer; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // largest |q| into [2^6, 2^7): 16 q, and 7.5 times a sum of 32, stay below fp16's largest
-  const int e = top > 0.0f && top < INFINITY ? min(6 - exponent(top), 126) : 0;
+  // largest |q| into [2^6, 2^7), or [2^4, 2^5) in two parts: 16 q and 7.5 times, or 16 times, a sum of 32 stay
+  // below fp16's largest
+  const int e = top > 0.0f && top < INFINITY ? min((QS ? 4 : 6) - exponent(top), 126) : 0;
   const float f = p.scale < 0.0f ? -pow2(e) : pow2(e);  // the factor of the scores is not negative
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) q[i] *= f;
@@ -164,6 +175,7 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
   if (sub % kBlk == 0) {
     const int b = sub / kBlk;
     constexpr float kOff = QS ? 0.5f : -7.5f;  // the codes enter less 8, or as they are
+    if (QS) sum *= 16.0f;  // as the products do
     const __half hi = __float2half_rn(sum), mid = __float2half_rn(kOff * sum);
     auto& out = sm.q_sum[row][b / S::kOfGroup];
     out[0][b % S::kOfGroup] = hi;
@@ -358,23 +370,24 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int h = 0; h < 2; ++h) {
           const uint8_t* at = tp + kv4_key_scale(D, g + 8 * h, 4 * k);
           az[h] = *reinterpret_cast<const uint32_t*>(at + (nb == 2 ? (c < 2 ? D : 0) : D + 4 * (c & 1)));
-          ad[h] = nb == 2 ? 0u : (c & 1) ? kd[h][nb == 2 ? 0 : 2 * k + 1] : kd[h][2 * k];
+          ad[h] = nb == 2 ? 0u : *reinterpret_cast<const uint32_t*>(at + 4 * (c & 1));
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (nb == 2) mma8(x[n], az[0], az[1], qz[n][k][0]);
+          else if (k == 0) mma16_first(x[n], az[0], az[1], ad[0], ad[1], qz[n][k][0], qz[n][k][1]);
           else mma16(x[n], az[0], az[1], ad[0], ad[1], qz[n][k][0], qz[n][k][1]);
         }
       }
+      if constexpr (!QS) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] *= QS ? 0x1p+4f : 0x1p-20f;
+          for (int e = 0; e < 4; ++e) x[n][e] *= 0x1p-20f;
+      }
 #pragma unroll
       for (int b2 = 0; b2 < nb; ++b2) {
         float acc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
         uint32_t ka[2][4];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -387,11 +400,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           const uint8_t* qp = sm.q + (size_t)((b2 * (QS ? 2 : 1) * NT + n) * 32 + lane) * 16;
           if constexpr (QS) {
             const uint4 q = *reinterpret_cast<const uint4*>(qp + NT * 32 * 16);
-            mma16(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
+            mma16_first(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
             mma16(acc[n], ka[1][0], ka[1][1], ka[1][2], ka[1][3], q.z, q.w);
           }
           const uint4 q = *reinterpret_cast<const uint4*>(qp);
-          mma16(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
+          if constexpr (QS) mma16(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
+          else mma16_first(acc[n], ka[0][0], ka[0][1], ka[0][2], ka[0][3], q.x, q.y);
           mma16(acc[n], ka[1][0], ka[1][1], ka[1][2], ka[1][3], q.z, q.w);
         }
         const float d0 = half_of(kd[0][b2 / 2], b2 & 1), d1 = half_of(kd[1][b2 / 2], b2 & 1);
@@ -442,18 +456,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           vs[h] &= keep;
         }
       }
-      uint32_t large = 0;
-#pragma unroll
-      for (int k = 0; k < 2 * nb; ++k) large |= ds[k];
       bool move = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > bar[n][e];
-      if (__any_sync(0xffffffffu, move || (large & 0x40004000u))) {  // or a step of 2 or more
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 2 * nb; ++k) top = max(top, max(ds[k] & 0xffffu, ds[k] >> 16));
+      if (__any_sync(0xffffffffu, move || ((vs[0] | vs[1]) & 0x40004000u))) {  // or a step of 2 or more
+        uint32_t top = max(max(vs[0] & 0xffffu, vs[0] >> 16), max(vs[1] & 0xffffu, vs[1] >> 16));
         top = __reduce_max_sync(0xffffffffu, top);
         const int E2 = max(E, (int)(top >> 10) - 15);  // its exponent
         const int E1 = E;
