@@ -64,24 +64,32 @@ __device__ __forceinline__ void kv4_set_status(int32_t* status, int code) {
   if (status) *status = code;
 }
 
-// Row r's sequence (by a search over the offsets, 32 at a time, by all lanes of
-// the warp) and its position; false where r lies in no sequence.
-__device__ __forceinline__ bool kv4_place(const Kv4Batch& a, int r, int lane, int& b, int& pos) {
+// A sequence: its number, rows first .. end - 1, and length.
+struct Kv4Place {
+  int b, first, end, len;
+};
+
+// Row r's sequence, by a search over the offsets, 32 at a time, by all lanes of the warp; false where r lies in none.
+// The last step's lanes hold the sequence's numbers already.
+__device__ __forceinline__ bool kv4_place(const Kv4Batch& a, int r, int lane, Kv4Place& s) {
   int lo = 0, n = a.n_seqs;  // the sequence lies in [lo, lo + n)
-  while (n > 1) {
+  while (n > 32) {
     const int step = (n + 31) / 32;
-    const int i = lo + lane * step;
-    const bool starts = lane * step < n && a.offsets[i] <= r;
+    const bool starts = lane * step < n && a.offsets[lo + lane * step] <= r;
     const uint32_t m = __ballot_sync(0xffffffffu, starts);
     const int last = m ? 31 - __clz(m) : 0;
     n = min(step, n - last * step);
     lo += last * step;
   }
-  b = lo;
-  const int first = a.offsets[b], end = a.offsets[b + 1];
-  if (r < first || r >= end) return false;
-  pos = a.lens[b] - (end - r);
-  return true;
+  const int i = lo + min(lane, n - 1);
+  const int first = a.offsets[i], end = a.offsets[i + 1], len = a.lens[i];
+  const uint32_t m = __ballot_sync(0xffffffffu, lane < n && first <= r);
+  const int at = m ? 31 - __clz(m) : 0;
+  s.b = lo + at;
+  s.first = __shfl_sync(0xffffffffu, first, at);
+  s.end = __shfl_sync(0xffffffffu, end, at);
+  s.len = __shfl_sync(0xffffffffu, len, at);
+  return r >= s.first && r < s.end;
 }
 
 // The tile of position pos of sequence b (head 0), or NULL where the table

@@ -45,6 +45,14 @@ __device__ __forceinline__ void load_run(const T* src, bool vector, float (&x)[N
   }
 }
 
+// Eight consecutive values of a 2-byte type as they lie in memory.
+template <typename T>
+__device__ __forceinline__ uint4 load_raw(const T* src, bool vector) {
+  if (vector) return __ldcs(reinterpret_cast<const uint4*>(src));
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(src);
+  return make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -64,14 +72,18 @@ __device__ __forceinline__ float divide15(float x) {
 }
 
 // W blocks of 32 values, N of each in every one of 32 / N neighbouring lanes: the codes of this lane's values (value i
-// of block w in bits 4 i of codes[w]), and the blocks' d (low half) and z as fp16.
+// of block w in bits 4 i of codes[w]), and d (low half) and z as fp16 of block (this lane's place in the blocks) % W,
+// whose numbers this lane works out for all of them.
 //
 // Beyond fp16's range (and for NaN) the values are clamped first (NaN to 0); odd: whether one was not finite.
 //
 // The quotient (x - z) / d is correctly rounded without a division each: Markstein's correction of x * r by
 // its exact remainder, r the correctly rounded reciprocal of d.
 template <int W, int N>
-__device__ __forceinline__ void quantize_blocks(float (&x)[W][N], uint32_t (&codes)[W], uint32_t (&dz)[W], bool& odd) {
+__device__ __forceinline__ void quantize_blocks(float (&x)[W][N], uint32_t (&codes)[W], uint32_t& dz, bool& odd) {
+  constexpr int kLanes = 32 / N;
+  static_assert(W <= kLanes, "a lane for each block");
+  const int lane = threadIdx.x & 31, own = lane % W, from = lane & ~(kLanes - 1);
   float hi[W], lo[W];
   auto extremes = [&]() {
 #pragma unroll
@@ -80,7 +92,7 @@ __device__ __forceinline__ void quantize_blocks(float (&x)[W][N], uint32_t (&cod
 #pragma unroll
       for (int i = 1; i < N; ++i) hi[w] = max_nan(hi[w], x[w][i]), lo[w] = min_nan(lo[w], x[w][i]);
 #pragma unroll
-      for (int o = 1; o < 32 / N; o <<= 1) {
+      for (int o = 1; o < kLanes; o <<= 1) {
         hi[w] = max_nan(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], o));
         lo[w] = min_nan(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], o));
       }
@@ -101,22 +113,27 @@ __device__ __forceinline__ void quantize_blocks(float (&x)[W][N], uint32_t (&cod
       }
     extremes();
   }
-  bool outside = false;
+  float top_own = hi[0], low_own = lo[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w)
+    if (own == w) top_own = hi[w], low_own = lo[w];
+  const __half dh = __float2half_rn(divide15(__fsub_rn(top_own, low_own)));
+  const __half zh = __float2half_rn(__fmul_rn(__fadd_rn(top_own, low_own), 0.5f));
+  dz = (uint32_t)__half_as_ushort(dh) | (uint32_t)__half_as_ushort(zh) << 16;
+  const float d_own = __half2float(dh), z_own = __half2float(zh);
+  const float r_own = d_own > 0.0f ? __frcp_rn(d_own) : 0.0f;  // without a step every quotient, and code, is 0
+  auto quotient = [](float v, float d, float z, float r) {
+    const float e = __fsub_rn(v, z), q = __fmul_rn(e, r);
+    return fmaf(fmaf(-d, q, e), r, q);
+  };
+  // a z that was rounded by much against d: codes beyond 0 and 15
+  const bool outside = !(quotient(top_own, d_own, z_own, r_own) < 8.0f && quotient(low_own, d_own, z_own, r_own) >= -8.0f);
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    const __half dh = __float2half_rn(divide15(__fsub_rn(hi[w], lo[w])));
-    const __half zh = __float2half_rn(__fmul_rn(__fadd_rn(hi[w], lo[w]), 0.5f));
-    dz[w] = (uint32_t)__half_as_ushort(dh) | (uint32_t)__half_as_ushort(zh) << 16;
-    const float d = __half2float(dh), z = __half2float(zh);
-    const float r = d > 0.0f ? __frcp_rn(d) : 0.0f;  // without a step every quotient is 0: set to 0 below
-    auto quotient = [&](float v) {
-      const float e = __fsub_rn(v, z), q = __fmul_rn(e, r);
-      return fmaf(fmaf(-d, q, e), r, q);
-    };
-    // a z that was rounded by much against d: codes beyond 0 and 15
-    outside |= !(quotient(hi[w]) < 8.0f && quotient(lo[w]) >= -8.0f);
+    const float d = __shfl_sync(0xffffffffu, d_own, from + w), z = __shfl_sync(0xffffffffu, z_own, from + w);
+    const float r = __shfl_sync(0xffffffffu, r_own, from + w), mid = r > 0.0f ? 7.5f : 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[w][i] = __fadd_rn(quotient(x[w][i]), d > 0.0f ? 7.5f : 0.0f);
+    for (int i = 0; i < N; ++i) x[w][i] = __fadd_rn(quotient(x[w][i], d, z, r), mid);
   }
   if (__any_sync(0xffffffffu, outside)) {
 #pragma unroll
@@ -126,10 +143,15 @@ __device__ __forceinline__ void quantize_blocks(float (&x)[W][N], uint32_t (&cod
   }
 #pragma unroll
   for (int w = 0; w < W; ++w) {
+    // 1.5 * 2^23 added, the bits are that number's plus the value rounded to even: the former's share is taken off
     codes[w] = 0;
+    uint32_t share = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)  // 1.5 * 2^23 added: the sum's last bits are the number rounded to even
-      codes[w] |= (__float_as_uint(__fadd_rn(x[w][i], 12582912.0f)) & 15u) << (4 * i);
+    for (int i = 0; i < N; ++i) {
+      codes[w] += __float_as_uint(__fadd_rn(x[w][i], 12582912.0f)) << (4 * i);
+      share += 0x4b400000u << (4 * i);
+    }
+    codes[w] -= share;
   }
 }
 
@@ -154,29 +176,25 @@ __device__ __forceinline__ uint8_t* segment_tile(const Kv4Batch& a, const Segmen
 template <typename F, typename B>
 __device__ __forceinline__ void for_segments(const Kv4Batch& a, int r, int chunk, int lane, F f, B before) {
   const int r0 = r, end = (int)min((int64_t)a.n_tokens, (int64_t)r + chunk);
-  int b = 0, pos = 0, first = 0, last = r;  // the sequence of row r, its rows: none yet
+  Kv4Place q = {0, 0, r, 0};  // the sequence of row r: none yet
 #pragma unroll 1
   while (r < end) {
-    if (r >= last) {
-      if (!kv4_place(a, r, lane, b, pos)) {
-        last = ++r;
-        continue;
-      }
-      first = a.offsets[b];
-      last = min(a.n_tokens, a.offsets[b + 1]);
+    if (r >= q.end && !kv4_place(a, r, lane, q)) {
+      q.end = ++r;
+      continue;
     }
+    const int pos = q.len - (q.end - r);
     int n = 1;
     if (pos < 0) {
       before(r);
     } else {
-      Segment s = {b, pos / kKv4Tile, pos % kKv4Tile, 0, 0};
-      n = chunk == 1 ? 1 : min(kKv4Tile - s.t0, last - r);
+      Segment s = {q.b, pos / kKv4Tile, pos % kKv4Tile, 0, 0};
+      n = chunk == 1 ? 1 : min(kKv4Tile - s.t0, min(a.n_tokens, q.end) - r);
       s.t1 = s.t0 + n;
       s.row0 = (int64_t)r - s.t0;
-      if (chunk == 1 || max(first, r - s.t0) >= r0) f(s);  // else it began in an earlier chunk
+      if (chunk == 1 || max(q.first, r - s.t0) >= r0) f(s);  // else it began in an earlier chunk
     }
     r += n;
-    pos += n;
   }
 }
 
@@ -199,9 +217,11 @@ __global__ void __launch_bounds__(256) kv4_append_rows_kernel(Kv4Batch a, Kv4Src
     const int q = 4 * i + (lane >> 3);
     load_run((q < nb ? k : v) + 32 * (q % nb) + 4 * g, src.vector, x[i]);
   }
-  int b, pos;
-  if (!kv4_place(a, (int)r, lane, b, pos) || pos < 0) return;
-  uint8_t* tile = kv4_tile(a, kv4_tile_bytes(D), b, pos / kKv4Tile);
+  Kv4Place q;
+  if (!kv4_place(a, (int)r, lane, q)) return;
+  const int pos = q.len - (q.end - (int)r);
+  if (pos < 0) return;
+  uint8_t* tile = kv4_tile(a, kv4_tile_bytes(D), q.b, pos / kKv4Tile);
   if (!tile) {
     if (lane == 0) kv4_set_status(a.status, MMVQ_ERR_ROUTING);
     return;
@@ -209,7 +229,7 @@ __global__ void __launch_bounds__(256) kv4_append_rows_kernel(Kv4Batch a, Kv4Src
   tile += head * kv4_head_stride(a, kv4_tile_bytes(D));
   const int t = pos % kKv4Tile;
   bool odd = false;
-  uint32_t codes[kTurns], dz[kTurns];
+  uint32_t codes[kTurns], dz;
   quantize_blocks(x, codes, dz, odd);
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
@@ -218,10 +238,12 @@ __global__ void __launch_bounds__(256) kv4_append_rows_kernel(Kv4Batch a, Kv4Src
     const int at = key ? kv4_word(j, 4 * (t & 7) + (g >> 1)) + 2 * (g & 1)
                        : 8 * D + kv4_word(j, 4 * g + ((t & 7) >> 1)) + 2 * (t & 1);
     *reinterpret_cast<uint16_t*>(tile + at) = (uint16_t)codes[i];
-    if (g < 2) {
-      const int sc = key ? kv4_key_scale(D, t, blk) : kv4_value_scale(D, t, blk);
-      *reinterpret_cast<uint16_t*>(tile + sc + g * D) = (uint16_t)(dz[i] >> (16 * g));
-    }
+  }
+  if (g < kTurns) {
+    const int q = 4 * g + (lane >> 3), blk = q % nb;
+    const int sc = q < nb ? kv4_key_scale(D, t, blk) : kv4_value_scale(D, t, blk);
+    *reinterpret_cast<uint16_t*>(tile + sc) = (uint16_t)dz;
+    *reinterpret_cast<uint16_t*>(tile + sc + D) = (uint16_t)(dz >> 16);
   }
   if (odd) kv4_set_status(a.status, MMVQ_ERR_VALUE);
 }
@@ -229,7 +251,7 @@ __global__ void __launch_bounds__(256) kv4_append_rows_kernel(Kv4Batch a, Kv4Src
 // A chunk of one head a warp, either its keys or its values, and of heads of 256 one half of the blocks; half a
 // tile's tokens at a time.  The rows are requested before the page is looked up.
 template <int D, typename T>
-__global__ void __launch_bounds__(256, 4) kv4_append_kernel(Kv4Batch a, Kv4Src src, int chunk) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 4) kv4_append_kernel(Kv4Batch a, Kv4Src src, int chunk) {
   constexpr int nb = D / 32, kN = nb < 4 ? nb : 4, kGroups = nb / kN;  // blocks of a warp
   grid_dependency_wait();
   grid_launch_dependents();
@@ -246,16 +268,34 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(Kv4Batch a, Kv4Src s
   bool odd = false;
   for_segments(a, r0, chunk, lane, [&](const Segment& s) {
     uint8_t* tile = nullptr;
+    // this lane: values 8 c .. + 7 of every block of tokens g and 8 + g; of 2-byte types the second half's are
+    // requested with the first's (fp32 would need twice the registers for it)
+    constexpr bool kBoth = sizeof(T) == 2;
+    uint4 ahead[kN];
+    auto on_of = [&](int h) { return 8 * h + g >= s.t0 && 8 * h + g < s.t1; };
+    auto row_of = [&](int h) { return base + (s.row0 + 8 * h + g) * ld; };
+    if constexpr (kBoth) {
+#pragma unroll
+      for (int w = 0; w < kN; ++w) {
+        ahead[w] = make_uint4(0u, 0u, 0u, 0u);
+        if (on_of(1)) ahead[w] = load_raw(row_of(1) + 32 * w, src.vector);
+      }
+    }
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
-      // this lane: values 8 c .. + 7 of every block of token 8 h + g
       const int t = 8 * h + g;
-      const bool on = t >= s.t0 && t < s.t1;
+      const bool on = on_of(h);
       float x[kN][8];
 #pragma unroll
       for (int w = 0; w < kN; ++w) {
-        if (on) {
-          load_run(base + (s.row0 + t) * ld + 32 * w, src.vector, x[w]);
+        if constexpr (kBoth) {
+          uint4 v = ahead[w];
+          if (h == 0) v = on ? load_raw(row_of(0) + 32 * w, src.vector) : make_uint4(0u, 0u, 0u, 0u);
+          const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[w][i] = kv4_load(e + i);
+        } else if (on) {
+          load_run(row_of(h) + 32 * w, src.vector, x[w]);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[w][i] = 0.0f;
@@ -266,58 +306,58 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(Kv4Batch a, Kv4Src s
         if (!tile) return;
         tile += head * kv4_head_stride(a, kv4_tile_bytes(D));
       }
-      uint32_t words[kN], dz[kN];
+      uint32_t words[kN], dz;
       quantize_blocks(x, words, dz, odd);
+      if (on && c < kN) {
+        const int sc = keys ? kv4_key_scale(D, t, b0 + c) : kv4_value_scale(D, t, b0 + c);
+        *reinterpret_cast<uint16_t*>(tile + sc) = (uint16_t)dz;
+        *reinterpret_cast<uint16_t*>(tile + sc + D) = (uint16_t)(dz >> 16);
+      }
       if (keys) {
         if (on) {
           uint8_t* at = tile + kv4_word(nb * h + b0, lane);
-          uint8_t* sc = tile + kv4_key_scale(D, t, b0) + c * D;  // lanes 0 and 1 of a token store its d, its z
-          uint32_t two[2];
-#pragma unroll
-          for (int w = 0; w < kN; w += 2) two[w / 2] = __byte_perm(dz[w], dz[w + 1], c ? 0x7632 : 0x5410);
-          if constexpr (kN == 4) {
-            *reinterpret_cast<uint4*>(at) = make_uint4(words[0], words[1], words[2], words[3]);
-            if (c < 2) *reinterpret_cast<uint2*>(sc) = make_uint2(two[0], two[1]);
-          } else {
-            *reinterpret_cast<uint2*>(at) = make_uint2(words[0], words[1]);
-            if (c < 2) *reinterpret_cast<uint32_t*>(sc) = two[0];
-          }
+          if constexpr (kN == 4) *reinterpret_cast<uint4*>(at) = make_uint4(words[0], words[1], words[2], words[3]);
+          else *reinterpret_cast<uint2*>(at) = make_uint2(words[0], words[1]);
         }
       } else {
         // the layout's word of this lane: values 4 g .. + 3 of tokens 2 c and 2 c + 1 of the half, which lanes
-        // (2 c, g / 2) and (2 c + 1, g / 2) hold, in the half word g % 2; tokens 2 c, 2 c + 1: their d and z too
+        // (2 c, g / 2) and (2 c + 1, g / 2) hold, in the half word g % 2
         const int from = 8 * c + (g >> 1), u = 8 * h + 2 * c;
         const bool on0 = u >= s.t0 && u < s.t1, on1 = u + 1 >= s.t0 && u + 1 < s.t1;
-        uint32_t two[kN];
 #pragma unroll
         for (int w = 0; w < kN; ++w) {
           const uint32_t w0 = __shfl_sync(0xffffffffu, words[w], from), w1 = __shfl_sync(0xffffffffu, words[w], from + 4);
-          const uint32_t s0 = __shfl_sync(0xffffffffu, dz[w], from), s1 = __shfl_sync(0xffffffffu, dz[w], from + 4);
           words[w] = __byte_perm(w0, w1, g & 1 ? 0x7632 : 0x5410);
-          two[w] = __byte_perm(s0, s1, g & 1 ? 0x7632 : 0x5410);  // g = 0: both d; g = 1: both z
         }
         uint8_t* at = tile + 8 * D + kv4_word(nb * h + b0, lane);
-        uint8_t* sc = tile + kv4_value_scale(D, u, b0) + (g & 1) * D;
         if (on0 && on1) {
-          if constexpr (kN == 4) {
-            *reinterpret_cast<uint4*>(at) = make_uint4(words[0], words[1], words[2], words[3]);
-            if (g < 2) *reinterpret_cast<uint4*>(sc) = make_uint4(two[0], two[1], two[2], two[3]);
-          } else {
-            *reinterpret_cast<uint2*>(at) = make_uint2(words[0], words[1]);
-            if (g < 2) *reinterpret_cast<uint2*>(sc) = make_uint2(two[0], two[1]);
-          }
+          if constexpr (kN == 4) *reinterpret_cast<uint4*>(at) = make_uint4(words[0], words[1], words[2], words[3]);
+          else *reinterpret_cast<uint2*>(at) = make_uint2(words[0], words[1]);
         } else if (on0 || on1) {
           const int e = on1 ? 1 : 0;
 #pragma unroll
-          for (int w = 0; w < kN; ++w) {
+          for (int w = 0; w < kN; ++w)
             *reinterpret_cast<uint16_t*>(at + 4 * w + 2 * e) = (uint16_t)(words[w] >> (16 * e));
-            if (g < 2) *reinterpret_cast<uint16_t*>(sc + 4 * w + 2 * e) = (uint16_t)(two[w] >> (16 * e));
-          }
         }
       }
     }
   }, [](int) {});
   if (odd) kv4_set_status(a.status, MMVQ_ERR_VALUE);
+}
+
+// N 32-bit words at p, aligned to their size (to 16 bytes at most).
+template <int N>
+__device__ __forceinline__ void load_words_global(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    static_assert(N == 1, "one, two or four");
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // Eight or four values from their codes to p.
@@ -339,23 +379,27 @@ __device__ __forceinline__ void store_codes8(T* p, uint32_t codes, float d, floa
   }
 }
 
+// A chunk of one head a warp, of heads of 256 one half of the blocks.
 template <int D, typename T>
-__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Batch a, T* __restrict__ k_out, T* __restrict__ v_out,
-                                                       int chunk) {
-  constexpr int nb = D / 32;
+__global__ void __launch_bounds__(256, 3) kv4_read_kernel(Kv4Batch a, T* __restrict__ k_out, T* __restrict__ v_out,
+                                                          int chunk) {
+  constexpr int nb = D / 32, kN = nb < 4 ? nb : 4, kGroups = nb / kN;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r0 = (int)(item / a.n_kv_heads) * chunk, head = (int)(item % a.n_kv_heads);
-  if (item / a.n_kv_heads * chunk >= a.n_tokens) return;
+  const int b0 = (int)(item % kGroups) * kN;
+  const int64_t unit = item / kGroups;
+  const int head = (int)(unit % a.n_kv_heads);
+  if (unit / a.n_kv_heads * chunk >= a.n_tokens) return;
+  const int r0 = (int)(unit / a.n_kv_heads) * chunk;
   const int64_t ld = (int64_t)a.n_kv_heads * D;
-  T* k = k_out + head * D;
-  T* v = v_out + head * D;
+  T* k = k_out + head * D + 32 * b0;
+  T* v = v_out + head * D + 32 * b0;
   auto zero_row = [&](int64_t r) {
-    for (int i = lane; i < D / 4; i += 32) {
-      kv4_store4(k + r * ld + 4 * i, 0.0f, 0.0f, 0.0f, 0.0f);
-      kv4_store4(v + r * ld + 4 * i, 0.0f, 0.0f, 0.0f, 0.0f);
+    if (lane < 8 * kN) {
+      kv4_store4(k + r * ld + 4 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
+      kv4_store4(v + r * ld + 4 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
     }
   };
   for_segments(a, r0, chunk, lane, [&](const Segment& s) {
@@ -365,47 +409,43 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Batch a, T* __restrict
       return;
     }
     tile += head * kv4_head_stride(a, kv4_tile_bytes(D));
-    // the tile's words of this lane's tokens, all requested before the first is used
-    uint4 kw[nb / 2], vw[nb / 2];
-    bool kon[2], von[2][2];
+    auto on = [&](int t) { return t >= s.t0 && t < s.t1; };
+    // the words of this lane's tokens and their steps and midpoints, all requested before the first is used
+    uint32_t kw[2][kN], kd[2][kN / 2], kz[2][kN / 2], vw[2][kN], vd[2][kN], vz[2][kN];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      kon[h] = 8 * h + g >= s.t0 && 8 * h + g < s.t1;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) von[h][e] = 8 * h + 2 * c + e >= s.t0 && 8 * h + 2 * c + e < s.t1;
-    }
-#pragma unroll
-    for (int q = 0; q < nb / 2; ++q) {
-      const int h0 = 4 * q / nb, h1 = (4 * q + 3) / nb;
-      kw[q] = vw[q] = make_uint4(0, 0, 0, 0);
-      if (kon[h0] || kon[h1]) kw[q] = *reinterpret_cast<const uint4*>(tile + 512 * q + 16 * lane);
-      if (von[h0][0] || von[h0][1] || von[h1][0] || von[h1][1])
-        vw[q] = *reinterpret_cast<const uint4*>(tile + 8 * D + 512 * q + 16 * lane);
-    }
-#pragma unroll
-    for (int j = 0; j < 2 * nb; ++j) {
-      const int h = j / nb, b = j % nb, t = 8 * h + g;
-      const uint32_t w = j % 4 == 0 ? kw[j / 4].x : j % 4 == 1 ? kw[j / 4].y : j % 4 == 2 ? kw[j / 4].z : kw[j / 4].w;
-      if (kon[h]) {
-        const uint16_t* sc = reinterpret_cast<const uint16_t*>(tile + kv4_key_scale(D, t, b));
-        store_codes8(k + (s.row0 + t) * ld + 32 * b + 8 * c, w, half_bits_to_float(sc[0]),
-                     half_bits_to_float(sc[D / 2]));
+      if (on(8 * h + g)) {
+        const uint8_t* sc = tile + kv4_key_scale(D, 8 * h + g, b0);
+        load_words_global(tile + kv4_word(nb * h + b0, lane), kw[h]);
+        load_words_global(sc, kd[h]);
+        load_words_global(sc + D, kz[h]);
+      }
+      if (on(8 * h + 2 * c) || on(8 * h + 2 * c + 1)) {
+        const uint8_t* sc = tile + kv4_value_scale(D, 8 * h + 2 * c, b0);
+        load_words_global(tile + 8 * D + kv4_word(nb * h + b0, lane), vw[h]);
+        load_words_global(sc, vd[h]);
+        load_words_global(sc + D, vz[h]);
       }
     }
+    auto half_at = [](uint32_t pair, int i) { return half_bits_to_float((uint16_t)(pair >> (16 * i))); };
 #pragma unroll
-    for (int j = 0; j < 2 * nb; ++j) {
-      const int h = j / nb, b = j % nb, t = 8 * h + 2 * c;
-      const uint32_t w = j % 4 == 0 ? vw[j / 4].x : j % 4 == 1 ? vw[j / 4].y : j % 4 == 2 ? vw[j / 4].z : vw[j / 4].w;
-      if (von[h][0] || von[h][1]) {
-        const uint32_t* sc = reinterpret_cast<const uint32_t*>(tile + kv4_value_scale(D, t, b));
-        const uint32_t d = sc[0], z = sc[D / 4];
+    for (int h = 0; h < 2; ++h)
+      if (on(8 * h + g)) {
+        T* row = k + (s.row0 + 8 * h + g) * ld + 8 * c;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (von[h][e])
-            store_codes(v + (s.row0 + t + e) * ld + 32 * b + 4 * g, w >> (16 * e),
-                        half_bits_to_float((uint16_t)(d >> (16 * e))), half_bits_to_float((uint16_t)(z >> (16 * e))));
+        for (int w = 0; w < kN; ++w)
+          store_codes8(row + 32 * w, kw[h][w], half_at(kd[h][w / 2], w & 1), half_at(kz[h][w / 2], w & 1));
       }
-    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (on(8 * h + 2 * c + e)) {
+          T* row = v + (s.row0 + 8 * h + 2 * c + e) * ld + 4 * g;
+#pragma unroll
+          for (int w = 0; w < kN; ++w)
+            store_codes(row + 32 * w, vw[h][w] >> (16 * e), half_at(vd[h][w], e), half_at(vz[h][w], e));
+        }
   }, zero_row);
 }
 
@@ -443,7 +483,7 @@ int read_typed(const Kv4Batch& a, int D, void* k, void* v, cudaStream_t stream) 
   T* vo = static_cast<T*>(v);
   if (D == 64) return launch_chunks(kv4_read_kernel<64, T>, a, 1, stream, ko, vo);
   if (D == 128) return launch_chunks(kv4_read_kernel<128, T>, a, 1, stream, ko, vo);
-  return launch_chunks(kv4_read_kernel<256, T>, a, 1, stream, ko, vo);
+  return launch_chunks(kv4_read_kernel<256, T>, a, 2, stream, ko, vo);
 }
 
 }  // namespace
