@@ -303,16 +303,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     __syncthreads();
 
     // ---- what a lane keeps of the queries: columns 2c, 2c + 1 of each row tile
-    float fac[NT][2], slack[NT][2];
-    int pos[NT][2];
+    float fac[NT][2];
     uint32_t qz[NT][kGroups][2];  // B operands of the products with midpoints and steps
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         fac[n][e] = sm.row_factor[8 * n + 2 * c + e];
-        slack[n][e] = kKv4Lazy / fac[n][e];
-        pos[n][e] = sm.row_pos[8 * n + 2 * c + e];
       }
       // k positions: of 4 blocks, both parts of sum(q), then both of -7.5 sum(q); of 2, all four at once
 #pragma unroll
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = key0 + g + 8 * (e >> 1), q = pos[n][e & 1];
+            const int key = key0 + g + 8 * (e >> 1), q = sm.row_pos[8 * n + 2 * c + (e & 1)];
             const bool see = key <= q && (p.window == 0 || key > q - p.window || key < p.sinks);
             if (!see) x[n][e] = -INFINITY;
           }
@@ -484,7 +481,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             r += E;
             fr[e] = none ? 0.0f : ex2(ref[n][e] - r);
             ref[n][e] = r;
-            bar[n][e] = fmaxf(bar[n][e], t + slack[n][e]);
+            bar[n][e] = fmaxf(bar[n][e], t + kKv4Lazy / fac[n][e]);
             l[n][e] *= fr[e];
           }
 #pragma unroll

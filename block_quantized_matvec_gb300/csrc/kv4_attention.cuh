@@ -31,7 +31,7 @@ struct Kv4Attention {
 
 constexpr int kKv4MaxCtas = 1024;     // of a launch
 constexpr int kKv4ItemUnits = 32;     // what an item costs besides its tiles
-constexpr int kKv4MinUnits = 24;      // of a CTA: below, fewer CTAs take part
+constexpr int kKv4MinUnits = 16;      // of a CTA: below, fewer CTAs take part
 
 // Workspace: join counters (two per CTA for the groups of a split item, one for
 // the groups' results), then two partial results per CTA.

@@ -549,7 +549,7 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tenso
     shape = (n_tokens, where[3], where[4])
     if out is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         for t in out:
@@ -560,12 +560,22 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tenso
     return k, v
 
 
+_workspace_bytes = {}  # by head_dim: a constant of the library
+
+
+def kv4_attention_workspace_bytes(head_dim: int) -> int:
+    n = _workspace_bytes.get(head_dim)
+    if n is None:
+        n = lib().mmvq_kv4_attention_workspace_bytes(head_dim)
+        if n < 0:
+            raise MMVQError(ERR_SHAPE, "mmvq_kv4_attention_workspace_bytes")
+        _workspace_bytes[head_dim] = n
+    return n
+
+
 def kv4_attention_workspace(head_dim: int, device) -> torch.Tensor:
     """A zeroed workspace for kv4_attention (one per concurrently running call)."""
-    n = lib().mmvq_kv4_attention_workspace_bytes(head_dim)
-    if n < 0:
-        raise MMVQError(ERR_SHAPE, "mmvq_kv4_attention_workspace_bytes")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.zeros(kv4_attention_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
 
 
 def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
@@ -583,18 +593,18 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     dim = where[4]
     dtype, n, heads, ldq, hq = _kv4_rows(q, 0, dim, "q")
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor of q's shape and type")
     if lse is None and with_lse:
-        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((n, heads), dtype=torch.float32)
     elif lse is not None and (lse.shape != (n, heads) or lse.dtype != torch.float32 or
                               not lse.is_cuda or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous CUDA float32 tensor [tokens, heads]")
     if workspace is None:
         workspace = kv4_attention_workspace(dim, q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous() or \
-            workspace.nbytes < lib().mmvq_kv4_attention_workspace_bytes(dim):
+            workspace.nbytes < kv4_attention_workspace_bytes(dim):
         raise ValueError("workspace is too small: kv4_attention_workspace(head_dim, device)")
     _check(lib().mmvq_kv4_attention(dtype, q.data_ptr(), ldq, hq, heads,
                                     dim ** -0.5 if scale is None else scale, window, sinks,
