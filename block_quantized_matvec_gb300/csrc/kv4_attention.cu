@@ -105,6 +105,7 @@ struct Shape {
   static constexpr int kWarps = D * NT <= 128 ? 4 : D == 128 ? 12 : 8;
   static constexpr int kCtas = D * NT <= 128 ? 4 : 1;
   static constexpr int kThreads = 32 * kWarps;
+  static_assert(kCtas <= kKv4MaxCtasSm && kCtas * kRows <= kv4_rows_sm(D), "the workspace");
   static constexpr int kBytes = kv4_tile_bytes(D);
 };
 
@@ -627,7 +628,7 @@ int launch(const Kv4Batch& a, const Kv4Attention& p, cudaStream_t stream) {
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, S::kThreads, kSmem) != cudaSuccess ||
         per_sm < 1)
       return MMVQ_ERR_CUDA;
-    ctas = min(sms * per_sm, kKv4MaxCtas);
+    ctas = min(sms, kKv4MaxSms) * min(per_sm, S::kCtas);
     __atomic_store_n(&per_device[dev], ctas, __ATOMIC_RELEASE);
   }
   // no more CTAs than the longest sequences that the table can hold would use
@@ -671,7 +672,7 @@ int launch_kv4_attention(const Kv4Batch& a, const Kv4Attention& args, int D, int
 }
 
 int64_t kv4_attention_workspace_bytes(int D) {
-  return kKv4CounterBytes + 2 * kKv4MaxCtas * kv4_slot_floats(kKv4MaxRows, D) * 4;
+  return kKv4CounterBytes + 2 * kKv4MaxSms * kv4_slot_floats(kv4_rows_sm(D), D) * 4;
 }
 
 }  // namespace mmvq

@@ -29,14 +29,16 @@ struct Kv4Attention {
   int page_shift;
 };
 
-constexpr int kKv4MaxCtas = 1024;     // of a launch
+constexpr int kKv4MaxSms = 160, kKv4MaxCtasSm = 4;  // of a launch
+constexpr int kKv4MaxCtas = kKv4MaxSms * kKv4MaxCtasSm;
 constexpr int kKv4ItemUnits = 32;     // what an item costs besides its tiles
 constexpr int kKv4MinUnits = 16;      // of a CTA: below, fewer CTAs take part
 
 // Workspace: join counters (two per CTA for the groups of a split item, one for
-// the groups' results), then two partial results per CTA.
-constexpr int kKv4MaxRows = 16;       // rows of a block (NT = 2)
+// the groups' results), then two partial results per CTA.  An SM's CTAs have at
+// most 4096 / D rows between them.
 constexpr int kKv4CounterBytes = kKv4MaxCtas * 3 * 4;
+__host__ __device__ constexpr int kv4_rows_sm(int D) { return 4096 / D; }
 __host__ __device__ constexpr int64_t kv4_slot_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
 
 // What a sequence asks for.

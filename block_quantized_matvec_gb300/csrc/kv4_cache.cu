@@ -14,6 +14,8 @@
 namespace mmvq {
 namespace {
 
+constexpr int kCtaWarps = 2;  // of the kernels that take tiles
+
 struct Kv4Src {
   const void* k;
   const void* v;
@@ -251,12 +253,12 @@ __global__ void __launch_bounds__(256) kv4_append_rows_kernel(Kv4Batch a, Kv4Src
 // A chunk of one head a warp, either its keys or its values, and of heads of 256 one half of the blocks; half a
 // tile's tokens at a time.  The rows are requested before the page is looked up.
 template <int D, typename T>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 4) kv4_append_kernel(Kv4Batch a, Kv4Src src, int chunk) {
+__global__ void __launch_bounds__(32 * kCtaWarps, (sizeof(T) == 2 ? 24 : 32) / kCtaWarps) kv4_append_kernel(Kv4Batch a, Kv4Src src, int chunk) {
   constexpr int nb = D / 32, kN = nb < 4 ? nb : 4, kGroups = nb / kN;  // blocks of a warp
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t item = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
   const int part = (int)(item % (2 * kGroups)), b0 = part % kGroups * kN;
   const bool keys = part < kGroups;
   const int64_t unit = item / (2 * kGroups);
@@ -381,13 +383,13 @@ __device__ __forceinline__ void store_codes8(T* p, uint32_t codes, float d, floa
 
 // A chunk of one head a warp, of heads of 256 one half of the blocks.
 template <int D, typename T>
-__global__ void __launch_bounds__(256, 3) kv4_read_kernel(Kv4Batch a, T* __restrict__ k_out, T* __restrict__ v_out,
+__global__ void __launch_bounds__(32 * kCtaWarps, 24 / kCtaWarps) kv4_read_kernel(Kv4Batch a, T* __restrict__ k_out, T* __restrict__ v_out,
                                                           int chunk) {
   constexpr int nb = D / 32, kN = nb < 4 ? nb : 4, kGroups = nb / kN;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t item = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
   const int b0 = (int)(item % kGroups) * kN;
   const int64_t unit = item / kGroups;
   const int head = (int)(unit % a.n_kv_heads);
@@ -458,8 +460,9 @@ template <typename K, typename... Args>
 int launch_chunks(K kern, const Kv4Batch& a, int parts, cudaStream_t stream, Args... args) {
   const int chunk = chunk_of(a);
   const int64_t items = ((int64_t)a.n_tokens + chunk - 1) / chunk * a.n_kv_heads * parts;
-  if ((items + 7) / 8 > 0x7fffffffLL) return MMVQ_ERR_SHAPE;
-  return launch_pdl(kern, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, stream, a, args..., chunk);
+  const int64_t ctas = (items + kCtaWarps - 1) / kCtaWarps;
+  if (ctas > 0x7fffffffLL) return MMVQ_ERR_SHAPE;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(32 * kCtaWarps), 0, stream, a, args..., chunk);
 }
 
 template <int D, typename T>

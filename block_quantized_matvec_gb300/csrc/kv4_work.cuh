@@ -7,7 +7,7 @@ namespace mmvq {
 
 constexpr float kKv4Lazy = 2.0f;    // slack of the softmax reference, log2 units
 constexpr float kKv4Boost = 12.0f;  // p is at most 2^(kKv4Lazy + kKv4Boost) = 2^14, below fp16's largest
-constexpr int kKv4Join = 32;        // parts that are joined at a time: sqrt(kKv4MaxCtas)
+constexpr int kKv4Join = 32;        // parts that are joined at a time: at least sqrt(kKv4MaxCtas)
 constexpr int kKv4JoinAtOnce = 24;  // more are joined in two steps
 
 __device__ __forceinline__ float ex2(float x) {

@@ -469,10 +469,16 @@ MMVQ_API int mmvq_kv4_read(int dtype, void* k, void* v, const void* cache, int64
  * y ([n_tokens][n_heads][head_dim] of dtype, contiguous) = sum softmax(scale *
  * q.k) v over the seen tokens, zeros where there are none; lse (may be NULL):
  * fp32 [n_tokens][n_heads], log(sum(exp(scale * q.k))), -inf where there are
- * none.  Scores, the softmax and the sums are fp32; for fp32 q the products
- * keep about 22 bits of q and of the probabilities.
- * Arithmetic on masked places never reaches y: what lies in the cache past a
- * sequence's length may hold anything.
+ * none.  Scores, the softmax and the sums are fp32; fp32 q and, for fp32 and
+ * fp16, the weighted probabilities enter the products with about 22 bits.
+ * Results do not depend on the run: parts of a sequence are added in a fixed
+ * order.  Masked places never reach y or lse: what lies in the cache past a
+ * sequence's length may hold anything.  A NaN or infinite query gives NaN in
+ * its own row only.
+ * Lengths are read on the device: one captured graph serves a growing batch.
+ * The next kernel on the stream may be launched before this one ends and must
+ * wait for it (every kernel of this library does, but y is not a stable input
+ * in MMVQ_FLAG_XQ_STABLE's sense for the call right after).
  * workspace: mmvq_kv4_attention_workspace_bytes(head_dim) bytes, 256-byte
  * aligned, zeroed once before the first call and left ready by every call;
  * calls that may run at the same time need separate ones.

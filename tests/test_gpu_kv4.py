@@ -389,3 +389,55 @@ def test_offsets_past_32_bits():
     assert np.array_equal(host(cache[pages - bt.n_pages:]), expected_cache(bt, k.double().numpy(), v.double().numpy()))
     del cache
     torch.cuda.empty_cache()
+
+
+def test_graph_replay_with_new_tokens_and_lengths():
+    """A captured step (append, attention) replayed after the lengths, inputs and queries changed on the device."""
+    D, kv, heads = 128, 2, 8
+    bt = _kv4.Batch(D, kv, 32, [400, 90], [1, 1], seed=24)
+    bt.fill_random()
+    w = where(bt)
+    k, v, q = (torch.zeros(2, h, D, device="cuda") for h in (kv, kv, heads))
+    y, ws = torch.empty(2, heads, D, device="cuda"), mmvq.kv4_attention_workspace(D, "cuda")
+
+    def step():
+        mmvq.kv4_append(k, v, *w)
+        mmvq.kv4_attention(q, *w, out=y, workspace=ws)
+    for length in ([400, 90], [37, 90]):
+        w[3].copy_(torch.tensor(length, dtype=torch.int32))
+        step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.synchronize()
+    for length in ([5, 90], [400, 1], [333, 47], [16, 17]):
+        for t in (k, v, q):
+            t.copy_(torch.from_numpy(bt.rng.normal(size=tuple(t.shape))))
+        w[3].copy_(torch.tensor(length, dtype=torch.int32))
+        before = host(w[0]).copy()
+        graph.replay()
+        bt.cache, bt.lens = before, length
+        bt.cache = expected_cache(bt, k.double().cpu().numpy(), v.double().cpu().numpy())
+        assert np.array_equal(host(w[0]), bt.cache)
+        want, _, a, s = _kv4.attention(bt, q.double().cpu().numpy(), D ** -0.5)
+        assert (np.abs(host(y) - want) <= bound("f32", want, a, s)).all()
+
+
+def test_one_workspace_for_calls_of_every_shape():
+    """Split and whole items, few rows and many, one after the other in one workspace: the bits of a fresh one."""
+    ws = mmvq.kv4_attention_workspace(64, "cuda")
+    calls = []
+    for i, (kv, group, lens, news) in enumerate([(1, 2, [4000], [1]), (2, 8, [30, 2000, 5], [2, 1, 1]), (1, 16, [900], [8]), (3, 1, [16] * 40, [1] * 40)]):
+        bt = _kv4.Batch(64, kv, 16, lens, news, seed=30 + i)
+        bt.fill_random()
+        q = torch.from_numpy(bt.rng.normal(size=(bt.n, kv * group, 64))).float().cuda()
+        calls.append((q, where(bt)))
+    fresh = [host(mmvq.kv4_attention(q, *w)).copy() for q, w in calls]
+    for _ in range(2):
+        outs = [mmvq.kv4_attention(q, *w, workspace=ws) for q, w in calls]   # nothing waits in between
+        for got, want in zip(outs, fresh):
+            assert np.array_equal(host(got).view(np.uint32), want.view(np.uint32))
+    assert not host(ws[:7680]).any()   # the join counters are left at zero
