@@ -17,6 +17,28 @@
 // Precision.  fp32 q enters as two fp16 parts (22 bits), and for fp32 and fp16
 // the products p d do too; bf16 keeps 11 bits of p d, finer than its own 8.
 // Every sum is fp32 (in the tensor core or outside).
+//
+// Why warp-level products.  Each 32-block of a key has its own factor on the
+// sum, and each block of a value its own on the probability, so a product
+// reaches over 32 values only, and the accumulators are needed in registers
+// between them.  (Decoded to fp16 for tcgen05 instead, keys keep 11 bits: with
+// 96 rows of bf16 that took 124 us against 144 here, but put the log-sum-exp
+// 2e-4 off; two parts of each key do not fit shared memory next to 128 rows of Q.)
+//
+// What bounds it, measured on GB300 (6768 GB/s copied):
+//  - one row tile, D = 128 (64 bf16 sequences of 128 .. 8192 tokens, 32 / 8
+//    heads, 337 MB): 77 us, 4.4 TB/s.  The instructions: 61% of the issue slots,
+//    48% of the ALU pipe (masking codes out of words), tensor pipe 22%.
+//    Four CTAs of 4 warps an SM at 128 registers: 77 us; two of 8: 80; one of 12
+//    with 168 registers: 114.
+//  - two row tiles, D = 256: the latency of 8 warps an SM at 255 registers (128 of
+//    them accumulators).  131071 fp32 tokens, 24 / 2 heads, 84 MB: 52 us, of which
+//    28 tiles and 10 joining 76 parts a head; tensor pipe 34%, issue 36%.  8 x 8
+//    query tokens over 16389, bf16: 144 us, tensor pipe 34%, issue 44%.  Splitting
+//    the values between two warps (175), 32 rows a warp (159) and two CTAs of 4
+//    warps (142; but 59 instead of 52 on the former) were no better.
+//  - short batches: about 10 us for 77 tokens: work division 1, first tile and
+//    queries 3, a tile 3 (its code is fetched for the first time), results 3.
 #include "kv4.cuh"
 #include "kv4_work.cuh"
 

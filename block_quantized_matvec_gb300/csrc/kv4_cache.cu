@@ -7,8 +7,18 @@
 // values of two tokens, are put together from those by 2 shuffles (both
 // tokens present: 16-byte stores, one: 2-byte ones).  Whole tiles move as
 // 512-byte rows of the layout on the cache's side and 64- or 128-byte runs on
-// the plain side, nothing is staged in shared memory.  With fewer rows a warp takes one row, so that a
-// decode step's rows spread over the GPU.
+// the plain side, nothing is staged in shared memory.  With fewer rows a warp
+// takes one row, so that a decode step's rows spread over the GPU.
+//
+// Measured on GB300 (6768 GB/s copied).  Append of 24575 fp32 tokens, 2 heads of
+// 256 (116 MB): 23.4 us, 5.0 TB/s; of 24 bf16 prompts of 50 .. 1201 tokens behind 37
+// cached ones, 8 heads of 128 (71 MB): 38.5 us, 1.8 TB/s.  Both are bound by
+// instructions and the latency of a warp's few loads (60 to 66% of the issue
+// slots; about 20 instructions a value).  CTAs of 2 warps: a warp that finds
+// nothing to do, or two segments, holds up no others (8 warps: 24.5 and 43 us).
+// Read of 65536 bf16 tokens, 8 heads of 128 (352 MB): 55 us, 6.4 TB/s, DRAM: 20
+// warps an SM with all of a tile's words in flight (24: 56 us, 32: 63, 40: 75).
+// One row a warp: 4 us for one token, launch and three loads in a row.
 #include "kv4.cuh"
 
 namespace mmvq {
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(256) kv4_append_rows_kernel(Kv4Batch a, Kv4Src
 // A chunk of one head a warp, either its keys or its values, and of heads of 256 one half of the blocks; half a
 // tile's tokens at a time.  The rows are requested before the page is looked up.
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kCtaWarps, (sizeof(T) == 2 ? 24 : 32) / kCtaWarps) kv4_append_kernel(Kv4Batch a, Kv4Src src, int chunk) {
+__global__ void __launch_bounds__(32 * kCtaWarps, (sizeof(T) == 2 ? 20 : 32) / kCtaWarps) kv4_append_kernel(Kv4Batch a, Kv4Src src, int chunk) {
   constexpr int nb = D / 32, kN = nb < 4 ? nb : 4, kGroups = nb / kN;  // blocks of a warp
   grid_dependency_wait();
   grid_launch_dependents();
@@ -383,7 +393,7 @@ __device__ __forceinline__ void store_codes8(T* p, uint32_t codes, float d, floa
 
 // A chunk of one head a warp, of heads of 256 one half of the blocks.
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kCtaWarps, 24 / kCtaWarps) kv4_read_kernel(Kv4Batch a, T* __restrict__ k_out, T* __restrict__ v_out,
+__global__ void __launch_bounds__(32 * kCtaWarps, 20 / kCtaWarps) kv4_read_kernel(Kv4Batch a, T* __restrict__ k_out, T* __restrict__ v_out,
                                                           int chunk) {
   constexpr int nb = D / 32, kN = nb < 4 ? nb : 4, kGroups = nb / kN;
   grid_dependency_wait();

@@ -168,7 +168,8 @@ def test_append_then_read_is_the_quantised_value():
 # the magnitudes, eight blocks added in fp32 (2^-24 each), the scale: below 2^-19 of s = scale *
 # sum |q| (|z| + 15 d).  A probability is then off by 2^-19 s (twice: once in the sum, once in the
 # weight) and 2^-20 for exp2 and its fp32 argument; weighted sums of the values by as much of a =
-# sum p (|z| + d |c - 7.5|), plus 2^-20 for their accumulation.  Types whose probabilities are kept to
+# sum p (|z| + d |c - 7.5|), plus 2^-20 for their accumulation.  (For fp16 and bf16 queries the codes enter as
+# subnormals, whose sums drop 2^-18 of the largest product instead of 2^-23 of the magnitudes: inside the same bound.)  Types whose probabilities are kept to
 # 11 bits (bf16) add 2^-12 for each of two roundings; the output is rounded once.
 
 def bound(dtype, y, a, s):
