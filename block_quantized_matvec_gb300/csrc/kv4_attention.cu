@@ -4,7 +4,8 @@
 // S^T[tokens x rows] = K Q^T from m16n8k16 f16 products whose A operand is the
 // tile's codes: masked out of its word a code c stands, as the bits of an
 // fp16, for c * 2^-24 (low nibble of a byte) or c * 2^-20 (high nibble), so a
-// key costs no conversion; for fp32 queries it becomes c - 8 (centred() below).
+// key costs no conversion; for fp32 queries, and in values, it becomes c - 8
+// (centred() below).
 // The rows of Q are scaled by a power of two each, and by 16 more where they
 // meet low nibbles.  Per block of 32 the sum is multiplied by the block's d in
 // fp32; sum(z sum(q)) and sum(d sum(q)) (the codes' offset) over the blocks
@@ -12,7 +13,7 @@
 // p = 2^(s - m + 12) use a reference m that is only moved when a score exceeds
 // it by 2 (in log2 units): the result does not depend on m, and most tiles skip
 // the maximum across lanes and the rescaling.  O^T[values x rows] += V^T P':
-// A = the codes, B = p d per block of 32; sum(p z) and sum(p d) one more product.
+// A = c - 8, B = p d per block of 32; sum(p z) and sum(p d) one more product.
 //
 // Precision.  fp32 q enters as two fp16 parts (22 bits), and for fp32 and fp16
 // the products p d do too; bf16 keeps 11 bits of p d, finer than its own 8.
@@ -46,6 +47,7 @@ namespace mmvq {
 namespace {
 
 constexpr int kStages = 4;
+
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -247,10 +249,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   constexpr int D = S::D, NT = S::NT, nb = S::nb, kRows = S::kRows, kBytes = S::kBytes;
   constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kGroups = S::kGroups;
   constexpr bool QS = S::QS;
-  // Value codes less 8 before the product, and 0.5 sum(p d) after it, or -7.5 sum(p d) after it: a rounding of
-  // p d counts with c - 8 or with c.  With p d in two parts and an fp16 output the latter is far below the
-  // output's rounding.
-  constexpr bool kCentre = QS || !PS;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<S>& sm = *reinterpret_cast<Smem<S>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -560,8 +558,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
           uint32_t a0, a1, a2, a3;
-          if constexpr (kCentre) centred(w0, w1, a0, a2, a1, a3);
-          else plain(w0, w1, a0, a2, a1, a3);
+          // c - 8 here and 0.5 sum(p d) at the end.  Codes as they are, with -7.5 sum(p d), cost less (32 fp16
+          // windows of 4096 tokens: 47.2 us, 48.7 with c - 8), but where the probabilities are even the two sums
+          // cancel: over 131072 tokens at D = 256 the error is then 2.5 times the fp16 output's own rounding, and
+          // 1.01 times with c - 8.
+          centred(w0, w1, a0, a2, a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma16(o[n][2 * b2 + hh], a0, a1, a2, a3, bh[n][0], bh[n][1]);
@@ -575,8 +576,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 
     // ---- the warp's result, in its ring: [row][D], in units of 2^(ref)
     float* res = reinterpret_cast<float*>(sm.ring[warp]);
-    // low nibbles entered as c 2^-24, high ones as c 2^-20; centred, as c - 8 and 16 (c - 8)
-    constexpr float u0 = kCentre ? 1.0f : 0x1p24f, u1 = kCentre ? 0x1p-4f : 0x1p20f, us = kCentre ? 0.5f : -7.5f;
+    // low nibbles entered as c - 8, high ones as 16 (c - 8)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -590,15 +590,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           sm.join.ref[warp][row] = bar[n][e] == -INFINITY ? -INFINITY : ref[n][e];
           sm.join.sum[warp][row] = t;
         }
-        const float z0 = fmaf(us, oz[n][e + 2], oz[n][e]);
+        const float z0 = fmaf(0.5f, oz[n][e + 2], oz[n][e]);
 #pragma unroll
         for (int b2 = 0; b2 < nb; ++b2) {
           const float z = __shfl_sync(0xffffffffu, z0, 4 * b2 + c);
           float4 v;
-          v.x = fmaf(o[n][2 * b2][e], u0, z);
-          v.y = fmaf(o[n][2 * b2][e + 2], u1, z);
-          v.z = fmaf(o[n][2 * b2 + 1][e], u0, z);
-          v.w = fmaf(o[n][2 * b2 + 1][e + 2], u1, z);
+          v.x = o[n][2 * b2][e] + z;
+          v.y = fmaf(o[n][2 * b2][e + 2], 0x1p-4f, z);
+          v.z = o[n][2 * b2 + 1][e] + z;
+          v.w = fmaf(o[n][2 * b2 + 1][e + 2], 0x1p-4f, z);
           *reinterpret_cast<float4*>(res + row * D + 32 * b2 + 4 * g) = v;
         }
       }

@@ -307,6 +307,21 @@ def test_attention_long_and_uneven(D, kv, group, lens, news):
     check_attention(bt, kv * group, "bf16", window=1500, sinks=5)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_even_probabilities_over_many_tokens_cost_no_more_than_the_outputs_rounding(dtype):
+    """Values of both signs under nearly equal probabilities cancel to 1/256 of themselves.  What the kernel
+    adds to the output's own rounding stays below three quarters of that (1.25 squared is 1 + 0.75 squared).
+    Four sequences share the pages, so that a warp adds up a dozen tiles."""
+    bt = _kv4.Batch(256, 1, 256, [65536], [1], seed=19)
+    bt.fill_random()
+    q = torch.from_numpy(bt.rng.normal(size=(1, 12, 256)) * 0.05).to(TYPES[dtype])
+    want = _kv4.attention(bt, q.double().numpy(), 1 / 16)[0]
+    w = (dev(bt.cache), dev(np.repeat(bt.table, 4, 0)), dev(np.arange(5, dtype=np.int32)), dev(np.full(4, 65536, np.int32)))
+    got = host(mmvq.kv4_attention(q.cuda().expand(4, -1, -1), *w).double())
+    rounding = np.linalg.norm(torch.from_numpy(want).to(TYPES[dtype]).double().numpy() - want)
+    assert max(np.linalg.norm(row - want[0]) for row in got) <= 1.25 * rounding
+
+
 def test_attention_of_a_large_batch():
     """More sequences than one search step, lengths of every residue."""
     n = 300
