@@ -131,6 +131,15 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _made(stream, make, *args, **kw):
+    """A tensor that a call makes itself, on the stream that the call runs on: its zeroing and its
+    memory's earlier uses come before the kernel, and its memory is used again only after it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _dev(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -548,8 +557,8 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tenso
         raise ValueError("dtype must be float32, float16 or bfloat16")
     shape = (n_tokens, where[3], where[4])
     if out is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty_like(k)
+        k = _made(stream, torch.empty, shape, dtype=dtype, device=cache.device)
+        v = _made(stream, torch.empty_like, k)
     else:
         k, v = out
         for t in out:
@@ -588,21 +597,22 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     kv4_append) over the cache -> y [n, heads, head_dim], or (y, lse [n, heads] fp32) with
     with_lse or lse.  A query sees the tokens up to its own position; with window > 0 only the
     last `window` of them and the first `sinks` of the sequence.  scale defaults to
-    head_dim**-0.5; workspace: kv4_attention_workspace.  (mmvq_kv4_attention)"""
+    head_dim**-0.5; workspace: kv4_attention_workspace, zeroed before this call on its stream
+    (a temporary one otherwise).  (mmvq_kv4_attention)"""
     where = _kv4_where(cache, page_table, offsets, lens)
     dim = where[4]
     dtype, n, heads, ldq, hq = _kv4_rows(q, 0, dim, "q")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor of q's shape and type")
     if lse is None and with_lse:
-        lse = q.new_empty((n, heads), dtype=torch.float32)
+        lse = _made(stream, q.new_empty, (n, heads), dtype=torch.float32)
     elif lse is not None and (lse.shape != (n, heads) or lse.dtype != torch.float32 or
                               not lse.is_cuda or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous CUDA float32 tensor [tokens, heads]")
     if workspace is None:
-        workspace = kv4_attention_workspace(dim, q.device)
+        workspace = _made(stream, kv4_attention_workspace, dim, q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous() or \
             workspace.nbytes < kv4_attention_workspace_bytes(dim):
         raise ValueError("workspace is too small: kv4_attention_workspace(head_dim, device)")

@@ -1,0 +1,72 @@
+"""The binding of the 4-bit cache's calls on the CPU: on which stream a call's own tensors are made,
+and the tensors it refuses."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+from block_quantized_matvec_gb300 import mmvq
+
+
+class Tensor(torch.Tensor):
+    """A CPU tensor that says it is on the GPU."""
+    is_cuda = True
+
+
+def tensor(shape, dtype):
+    return torch.zeros(shape, dtype=dtype).as_subclass(Tensor)
+
+
+def batch():
+    """A cache of one page of 16 tokens, and one sequence in it."""
+    return (tensor((1, 1, 1, 20 * 64), torch.uint8), tensor((1, 1), torch.int32), tensor((2,), torch.int32),
+            tensor((1,), torch.int32))
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The stream that is current at each allocation and at each launch, the launch's last argument too."""
+    seen, current = [], [None]
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def watched(name):
+        make = getattr(torch, name)
+
+        def f(*args, **kw):
+            seen.append((name, current[-1]))
+            return make(*args, **kw)
+        return f
+    for name in ("empty", "empty_like", "zeros"):
+        monkeypatch.setattr(torch, name, watched(name))
+    new_empty = torch.Tensor.new_empty
+    monkeypatch.setattr(torch.Tensor, "new_empty", lambda t, *a, **kw: seen.append(("new_empty", current[-1])) or new_empty(t, *a, **kw))
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+
+    def launch(*args):
+        seen.append(("launch", args[-1]))
+        return mmvq.OK
+    fake = types.SimpleNamespace(mmvq_kv4_append=launch, mmvq_kv4_read=launch, mmvq_kv4_attention=launch,
+                                 mmvq_kv4_attention_workspace_bytes=lambda dim: 1024)
+    monkeypatch.setattr(mmvq, "lib", lambda: fake)
+    monkeypatch.setattr(mmvq, "_workspace_bytes", {})
+    return seen
+
+
+def test_a_calls_own_tensors_are_made_on_its_stream(calls):
+    """Made on another stream, they would be zeroed after the kernel began, or belong to that stream's pool while
+    the kernel uses them."""
+    side = types.SimpleNamespace(cuda_stream=77)
+    q, where = tensor((1, 2, 64), torch.float32), batch()
+    calls.clear()
+    mmvq.kv4_attention(q, *where, with_lse=True, stream=side)
+    assert {name for name, _ in calls} == {"empty_like", "new_empty", "zeros", "launch"}
+    assert calls[-1] == ("launch", 77) and all(s is side for _, s in calls[:-1])
+    calls.clear()
+    mmvq.kv4_read(*where, 1, stream=side)
+    assert calls[-1] == ("launch", 77) and len(calls) == 3 and all(s is side for _, s in calls[:2])
