@@ -159,7 +159,7 @@ def quantize_q8_1(x: torch.Tensor, K: int | None = None, out: torch.Tensor | Non
     ncols, ldx = x2.shape
     K = ldx if K is None else K
     if out is None:
-        out = torch.empty((ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=x.device)
+        out = _made(stream, torch.empty, (ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=x.device)
     _check(lib().mmvq_quantize_q8_1(_ptr(x2), K, ncols, ldx, _ptr(out), _stream(stream)),
            "mmvq_quantize_q8_1")
     return out
@@ -173,7 +173,7 @@ def gemv(type_: int, W: torch.Tensor, rows: int, K: int, xq: torch.Tensor, ncols
     _dev(W, "W")
     _dev(xq, "xq")
     if out is None:
-        out = torch.empty((ncols, rows), dtype=torch.float32, device=W.device)
+        out = _made(stream, torch.empty, (ncols, rows), dtype=torch.float32, device=W.device)
     if flags:
         _check(lib().mmvq_gemv_ex(type_, _ptr(W), rows, K, _ptr(xq), ncols, _ptr(out), flags,
                                   _stream(stream)), "mmvq_gemv_ex")
@@ -195,9 +195,9 @@ def gemv_f32(type_: int, W: torch.Tensor, rows: int, K: int, x: torch.Tensor, nc
         raise ValueError("x must be a CUDA float32 tensor with unit column stride")
     ncols = x.shape[0] if ncols is None else ncols
     if xq is None:
-        xq = torch.empty((ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=x.device)
+        xq = _made(stream, torch.empty, (ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=x.device)
     if out is None:
-        out = torch.empty((ncols, rows), dtype=torch.float32, device=x.device)
+        out = _made(stream, torch.empty, (ncols, rows), dtype=torch.float32, device=x.device)
     _check(lib().mmvq_gemv_f32(type_, _ptr(W), rows, K, _ptr(x), x.stride(0), ncols, _ptr(xq),
                                _ptr(out), flags, _stream(stream)), "mmvq_gemv_f32")
     return out, xq
@@ -215,8 +215,8 @@ def debug_block_sums(type_: int, W: torch.Tensor, rows: int, K: int, xq: torch.T
     """(sumi [ncols, rows, K/32] int32, y [ncols, rows]) from the gemv kernel itself."""
     _dev(W, "W")
     _dev(xq, "xq")
-    sumi = torch.empty((ncols, rows, K // 32), dtype=torch.int32, device=W.device)
-    y = torch.empty((ncols, rows), dtype=torch.float32, device=W.device)
+    sumi = _made(stream, torch.empty, (ncols, rows, K // 32), dtype=torch.int32, device=W.device)
+    y = _made(stream, torch.empty, (ncols, rows), dtype=torch.float32, device=W.device)
     if flags:
         _check(lib().mmvq_debug_block_sums_ex(type_, _ptr(W), rows, K, _ptr(xq), ncols,
                                               _ptr(sumi), _ptr(y), flags, _stream(stream)),
@@ -236,7 +236,7 @@ def grouped(type_: int, W_experts: torch.Tensor, n_experts: int, rows: int, K: i
                  (xq, "xq")):
         _dev(t, n)
     if out is None:
-        out = torch.empty((max(n_positions, 1), rows), dtype=torch.float32, device=xq.device)
+        out = _made(stream, torch.empty, (max(n_positions, 1), rows), dtype=torch.float32, device=xq.device)
     _check(lib().mmvq_grouped(type_, _ptr(W_experts), n_experts, rows, K, _ptr(expert_ids),
                               _ptr(offsets), expert_ids.numel(), _ptr(act_index), _ptr(xq),
                               n_xq_cols, _ptr(out), _ptr(status), _stream(stream)), "mmvq_grouped")
@@ -255,12 +255,12 @@ def quantize_route_groups(x: torch.Tensor, topk: torch.Tensor, n_experts: int,
     T, k = topk.shape
     dev = x.device
     if xq is None:
-        xq = torch.empty((ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=dev)
-    eids = torch.empty(n_experts, dtype=torch.int32, device=dev)
-    offs = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
-    act = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
-    slot = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
-    status = torch.zeros(1, dtype=torch.int32, device=dev)
+        xq = _made(stream, torch.empty, (ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=dev)
+    eids = _made(stream, torch.empty, n_experts, dtype=torch.int32, device=dev)
+    offs = _made(stream, torch.empty, n_experts + 1, dtype=torch.int32, device=dev)
+    act = _made(stream, torch.empty, max(T * k, 1), dtype=torch.int32, device=dev)
+    slot = _made(stream, torch.empty, max(T * k, 1), dtype=torch.int32, device=dev)
+    status = _made(stream, torch.zeros, 1, dtype=torch.int32, device=dev)
     _check(lib().mmvq_quantize_route_groups(_ptr(x), K, ncols, K, _ptr(xq),
                                             _ptr(topk) if T else None, T, k, n_experts,
                                             _ptr(eids), _ptr(offs), _ptr(act), _ptr(slot),
@@ -292,24 +292,24 @@ def expert_ffn(type_: int, W_gate_up: torch.Tensor, W_down: torch.Tensor, n_expe
     n = T * k
     dev = x.device
     if gu is None:
-        gu = torch.empty((n, 2 * F), dtype=torch.float32, device=dev)
+        gu = _made(stream, torch.empty, (n, 2 * F), dtype=torch.float32, device=dev)
     if hq is None:
-        hq = torch.empty((n, F // 32, Q8_1_BYTES), dtype=torch.uint8, device=dev)
+        hq = _made(stream, torch.empty, (n, F // 32, Q8_1_BYTES), dtype=torch.uint8, device=dev)
     if y is None:
-        y = torch.empty((n, H), dtype=torch.float32, device=dev)
+        y = _made(stream, torch.empty, (n, H), dtype=torch.float32, device=dev)
     out = {"gu": gu, "hq": hq, "y": y}
     if lists:
-        out.update(expert_ids=torch.empty(n_experts, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
-                   act_index=torch.empty(max(n, 1), dtype=torch.int32, device=dev),
-                   slot_of=torch.empty(max(n, 1), dtype=torch.int32, device=dev))
+        out.update(expert_ids=_made(stream, torch.empty, n_experts, dtype=torch.int32, device=dev),
+                   offsets=_made(stream, torch.empty, n_experts + 1, dtype=torch.int32, device=dev),
+                   act_index=_made(stream, torch.empty, max(n, 1), dtype=torch.int32, device=dev),
+                   slot_of=_made(stream, torch.empty, max(n, 1), dtype=torch.int32, device=dev))
     if xq is None:
-        xq = torch.empty((T, H // 32, Q8_1_BYTES), dtype=torch.uint8, device=dev)
+        xq = _made(stream, torch.empty, (T, H // 32, Q8_1_BYTES), dtype=torch.uint8, device=dev)
     out["xq"] = xq
     if status is not None:
         out["status"] = status
     if sync is None:
-        sync = expert_ffn_workspace(dev)
+        sync = _made(stream, expert_ffn_workspace, dev)
     _check(lib().mmvq_expert_ffn(type_, _ptr(W_gate_up), _ptr(W_down), n_experts, H, F, _ptr(x),
                                  x.stride(0), T, _ptr(topk), k, _ptr(gu), _ptr(hq), _ptr(y),
                                  _ptr(out.get("expert_ids")), _ptr(out.get("offsets")),
@@ -335,13 +335,13 @@ def expert_ffn_noalloc(type_: int, W_gate_up: torch.Tensor, W_down: torch.Tensor
     n = T * k
     dev = x.device
     if y is None:
-        y = torch.empty((n, H), dtype=torch.float32, device=dev)
+        y = _made(stream, torch.empty, (n, H), dtype=torch.float32, device=dev)
     out = {"y": y}
     if lists:
-        out.update(expert_ids=torch.empty(n_experts, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
-                   act_index=torch.empty(max(n, 1), dtype=torch.int32, device=dev),
-                   slot_of=torch.empty(max(n, 1), dtype=torch.int32, device=dev))
+        out.update(expert_ids=_made(stream, torch.empty, n_experts, dtype=torch.int32, device=dev),
+                   offsets=_made(stream, torch.empty, n_experts + 1, dtype=torch.int32, device=dev),
+                   act_index=_made(stream, torch.empty, max(n, 1), dtype=torch.int32, device=dev),
+                   slot_of=_made(stream, torch.empty, max(n, 1), dtype=torch.int32, device=dev))
     if status is not None:
         out["status"] = status
     _check(lib().mmvq_expert_ffn_noalloc(type_, _ptr(W_gate_up), _ptr(W_down), n_experts, H, F,
@@ -374,11 +374,11 @@ def route_groups(topk: torch.Tensor, n_experts: int, stream=None):
     _dev(topk, "topk")
     T, k = topk.shape
     dev = topk.device
-    eids = torch.empty(n_experts, dtype=torch.int32, device=dev)
-    offs = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
-    act = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
-    slot = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
-    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    eids = _made(stream, torch.empty, n_experts, dtype=torch.int32, device=dev)
+    offs = _made(stream, torch.empty, n_experts + 1, dtype=torch.int32, device=dev)
+    act = _made(stream, torch.empty, max(T * k, 1), dtype=torch.int32, device=dev)
+    slot = _made(stream, torch.empty, max(T * k, 1), dtype=torch.int32, device=dev)
+    status = _made(stream, torch.zeros, 1, dtype=torch.int32, device=dev)
     _check(lib().mmvq_route_groups(_ptr(topk) if T else None, T, k, n_experts, _ptr(eids),
                                    _ptr(offs), _ptr(act), _ptr(slot), _ptr(status),
                                    _stream(stream)), "mmvq_route_groups")
@@ -391,7 +391,7 @@ def silu_mul_quantize_q8_1(gu: torch.Tensor, F: int, out: torch.Tensor | None = 
     _dev(gu, "gu")
     n = gu.shape[0]
     if out is None:
-        out = torch.empty((n, F // 32, Q8_1_BYTES), dtype=torch.uint8, device=gu.device)
+        out = _made(stream, torch.empty, (n, F // 32, Q8_1_BYTES), dtype=torch.uint8, device=gu.device)
     _check(lib().mmvq_silu_mul_quantize_q8_1(_ptr(gu), F, n, _ptr(out), _ptr(h_out),
                                              _stream(stream)), "mmvq_silu_mul_quantize_q8_1")
     return out
@@ -429,7 +429,7 @@ def rmsnorm_quantize_q8_1(x: torch.Tensor, w: torch.Tensor, eps: float,
             not w.is_contiguous() or w.numel() != K:
         raise ValueError("x [ncols, K] with unit inner stride and w [K], both float32")
     if out is None:
-        out = torch.empty((ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=x.device)
+        out = _made(stream, torch.empty, (ncols, K // 32, Q8_1_BYTES), dtype=torch.uint8, device=x.device)
     _check(lib().mmvq_rmsnorm_quantize_q8_1(_ptr(x), _ptr(w), eps, K, ncols, x.stride(0),
                                             _ptr(out), _ptr(y_out), _stream(stream)),
            "mmvq_rmsnorm_quantize_q8_1")
@@ -454,7 +454,7 @@ def repack_planar(W_gguf: torch.Tensor, rows: int, K: int, out: torch.Tensor | N
     """GGUF Q6_K (or Q4_K) bytes -> planar tiles (uint8, planar_bytes(rows, K, type_))."""
     _dev(W_gguf, "W_gguf")
     if out is None:
-        out = torch.empty(planar_bytes(rows, K, type_), dtype=torch.uint8, device=W_gguf.device)
+        out = _made(stream, torch.empty, planar_bytes(rows, K, type_), dtype=torch.uint8, device=W_gguf.device)
     _check(lib().mmvq_repack_planar(type_, _ptr(W_gguf), rows, K, _ptr(out), _stream(stream)),
            "mmvq_repack_planar")
     return out
@@ -467,8 +467,8 @@ def gather_planar_rows(W_planar: torch.Tensor, rows: int, K: int, row_ids: torch
     _dev(row_ids, "row_ids")
     n = row_ids.numel()
     if out is None:
-        out = torch.empty(planar_bytes(n, K), dtype=torch.uint8, device=W_planar.device)
-    status = torch.zeros(1, dtype=torch.int32, device=W_planar.device)
+        out = _made(stream, torch.empty, planar_bytes(n, K), dtype=torch.uint8, device=W_planar.device)
+    status = _made(stream, torch.zeros, 1, dtype=torch.int32, device=W_planar.device)
     _check(lib().mmvq_gather_planar_rows(_ptr(W_planar), rows, K, _ptr(row_ids), n, _ptr(out),
                                          _ptr(status), _stream(stream)), "mmvq_gather_planar_rows")
     return out, status

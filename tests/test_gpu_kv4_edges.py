@@ -19,7 +19,7 @@ def test_defaults_on_another_stream():
     bt.fill_random()
     q = torch.from_numpy(bt.rng.normal(size=(2, 8, 128))).float()
     want, _, a, s = _kv4.attention(bt, q.double().numpy(), 128 ** -0.5)
-    w, qc = where(bt), q.cuda()
+    w, qc, all_of_0 = where(bt), q.cuda(), dev(np.array([0, 5000, 5000], np.int32))
     (k, *_), (v, *_) = bt.sequence(0)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -28,7 +28,7 @@ def test_defaults_on_another_stream():
         del dirty
         torch.cuda._sleep(2_000_000)          # about a millisecond of the current stream
         y = mmvq.kv4_attention(qc, *w, stream=side)
-        kr, vr = mmvq.kv4_read(*w[:2], dev(np.array([0, 5000, 5000], np.int32)), w[3], 5000, stream=side)
+        kr, vr = mmvq.kv4_read(*w[:2], all_of_0, w[3], 5000, stream=side)
         dirty = torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
         side.synchronize()
         assert (np.abs(host(y) - want) <= bound("f32", want, a, s)).all()

@@ -1,5 +1,5 @@
-"""The binding of the 4-bit cache's calls on the CPU: on which stream a call's own tensors are made,
-and the tensors it refuses."""
+"""The binding on the CPU: on which stream a call's own tensors are made, and the tensors that the 4-bit
+cache's calls refuse."""
 import contextlib
 import types
 
@@ -51,7 +51,9 @@ def calls(monkeypatch):
     def launch(*args):
         seen.append(("launch", args[-1]))
         return mmvq.OK
-    fake = types.SimpleNamespace(mmvq_kv4_append=launch, mmvq_kv4_read=launch, mmvq_kv4_attention=launch,
+    fake = types.SimpleNamespace(mmvq_quantize_q8_1=launch, mmvq_gemv=launch, mmvq_route_groups=launch,
+                                 mmvq_expert_ffn=launch, mmvq_kv4_append=launch, mmvq_kv4_read=launch,
+                                 mmvq_kv4_attention=launch,
                                  mmvq_kv4_attention_workspace_bytes=lambda dim: 1024)
     monkeypatch.setattr(mmvq, "lib", lambda: fake)
     monkeypatch.setattr(mmvq, "_workspace_bytes", {})
@@ -70,3 +72,16 @@ def test_a_calls_own_tensors_are_made_on_its_stream(calls):
     calls.clear()
     mmvq.kv4_read(*where, 1, stream=side)
     assert calls[-1] == ("launch", 77) and len(calls) == 3 and all(s is side for _, s in calls[:2])
+
+
+def test_so_are_the_products_and_the_expert_layers(calls):
+    """The expert layer's barrier word and the routing's status are zeroed by the call."""
+    side = types.SimpleNamespace(cuda_stream=77)
+    x, topk, W = tensor((2, 256), torch.float32), tensor((2, 4), torch.int32), tensor((64,), torch.uint8)
+    for call in (lambda: mmvq.quantize_q8_1(x, stream=side),
+                 lambda: mmvq.gemv(mmvq.TYPE_Q4_K_PLANAR, W, 16, 256, W, 2, stream=side),
+                 lambda: mmvq.route_groups(topk, 8, stream=side),
+                 lambda: mmvq.expert_ffn(mmvq.TYPE_Q4_K_PLANAR, W, W, 8, 256, 256, x, topk, stream=side)):
+        calls.clear()
+        call()
+        assert len(calls) > 1 and calls[-1] == ("launch", 77) and all(s is side for _, s in calls[:-1])
