@@ -214,7 +214,7 @@ __device__ __forceinline__ void load_queries(const Kv4Batch& a, const Kv4Attenti
     const int f2 = kUnit - e;
     const float factor = fabsf(p.scale) * 1.4426950408889634f * pow2(f2 / 2) * pow2(f2 - f2 / 2);
     sm.row_factor[row] = fminf(fmaxf(factor, 1e-37f), 1e37f);  // not 0: masked scores are -inf
-    sm.row_pos[row] = on ? s.len - s.n_new + t : -1;
+    sm.row_pos[row] = on ? max(-1, s.len - s.n_new + t) : -1;  // less a window of up to 2^31 - 1: in range
   }
 }
 
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     const uint8_t* head_base = a.cache + (int64_t)it.head * per_page * kv4_tile_bytes(D) + lane * 16;
     const int64_t page_bytes = (int64_t)a.n_kv_heads * per_page * kv4_tile_bytes(D);
     const int32_t* table = a.page_table + (int64_t)it.b * a.ld_table;
-    const int pos_lo = s.len - s.n_new;  // of the sequence's rows
+    const int pos_lo = max(0, s.len - s.n_new);  // of the sequence's rows that see anything
     auto tile_of = [&](int i) { return i + (i >= s.sink_tiles ? s.skip : 0); };
     const int gap = s.skip > 0 ? s.sink_tiles : -1;  // the tile before which some are skipped
     uint32_t present = 0;

@@ -7,7 +7,7 @@ import torch
 from block_quantized_matvec_gb300 import mmvq
 from tests import _kv4
 from tests._gpu import dev, host
-from tests.test_gpu_kv4 import bound, where
+from tests.test_gpu_kv4 import bound, check_attention, where
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,12 @@ def test_defaults_on_another_stream():
         assert (np.abs(host(y) - want) <= bound("f32", want, a, s)).all()
         assert np.array_equal(host(kr), k.astype(np.float32)) and np.array_equal(host(vr), v.astype(np.float32))
         del dirty
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 6, 1 << 30])
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_windows_up_to_the_largest_number(window, sinks):
+    """As good as none, also where a sequence has more rows than tokens, whose first position is negative."""
+    bt = _kv4.Batch(64, 2, 16, [3, 0, 20, 5], [5, 2, 8, 8], seed=41)
+    bt.fill_random()
+    check_attention(bt, 4, "f32", window=window, sinks=sinks)
