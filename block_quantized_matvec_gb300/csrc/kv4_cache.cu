@@ -138,8 +138,10 @@ __device__ __forceinline__ void quantize_blocks(float (&x)[W][N], uint32_t (&cod
     const float e = __fsub_rn(v, z), q = __fmul_rn(e, r);
     return fmaf(fmaf(-d, q, e), r, q);
   };
-  // a z that was rounded by much against d: codes beyond 0 and 15
-  const bool outside = !(quotient(top_own, d_own, z_own, r_own) < 8.0f && quotient(low_own, d_own, z_own, r_own) >= -8.0f);
+  // a z or d that was rounded by much against d: codes beyond 0 and 15.  The rounded sum decides: 7.5 and the largest
+  // number below 8 are 15.5, which rounds to 16.
+  const bool outside = !(__fadd_rn(quotient(top_own, d_own, z_own, r_own), 7.5f) < 15.5f &&
+                         quotient(low_own, d_own, z_own, r_own) >= -8.0f);
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     const float d = __shfl_sync(0xffffffffu, d_own, from + w), z = __shfl_sync(0xffffffffu, z_own, from + w);

@@ -7,7 +7,7 @@ import torch
 from block_quantized_matvec_gb300 import mmvq
 from tests import _kv4
 from tests._gpu import dev, host
-from tests.test_gpu_kv4 import bound, check_attention, where
+from tests.test_gpu_kv4 import bound, check_attention, expected_cache, where
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,25 @@ def test_windows_up_to_the_largest_number(window, sinks):
     bt = _kv4.Batch(64, 2, 16, [3, 0, 20, 5], [5, 2, 8, 8], seed=41)
     bt.fill_random()
     check_attention(bt, 4, "f32", window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("rows", [5, 40])   # the kernel for few rows a sequence, and the one for tiles
+def test_append_next_to_the_border_of_the_last_code(rows):
+    """Steps so small that fp16 rounds them by much: the quotient of a block's largest (or smallest) value lies next
+    to 8, where adding 7.5 rounds to 15.5.  At every place of a block, among zeros and among values like it."""
+    D = 64
+    bt = _kv4.Batch(D, 2, 16, [rows], [rows], seed=42)
+    k = np.zeros((rows, 2, D), np.float32)
+    v = bt.rng.uniform(-4, 4, (rows, 2, D)).astype(np.float32) * np.float32(2.0 ** -24)
+    below = np.nextafter(np.float32(8), np.float32(0))
+    for r in range(rows):
+        for h in range(2):
+            for b in range(2):
+                at = (7 * r + 5 * h + 3 * b + np.array([0, 9])) % 32 + 32 * b
+                step = np.float32((1 + r % 5) * 2.0 ** -24)
+                for x in (k, v):
+                    x[r, h, at[0]], x[r, h, at[1]] = below * step, -below * step
+    assert (_kv4.quantise(k.astype(np.float64))[0] == 15).any()
+    w = where(bt)
+    mmvq.kv4_append(dev(k), dev(v), *w)
+    assert np.array_equal(host(w[0]), expected_cache(bt, k.astype(np.float64), v.astype(np.float64)))
