@@ -45,7 +45,7 @@ __host__ __device__ constexpr int64_t kv4_slot_floats(int rows, int D) { return 
 struct Kv4Seq {
   int first;   // its first row
   int n_new;   // rows (0: nothing to do)
-  int len;     // cached tokens
+  int len;     // cached tokens (some may lie past the page table)
   int sink_tiles, skip, tiles;  // tile i of `tiles` is i + (i >= sink_tiles ? skip : 0)
   int blocks;  // row blocks
   __device__ __forceinline__ int item_units() const { return tiles + kKv4ItemUnits; }
@@ -65,7 +65,13 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Batch& a, const Kv4Attention&
                                                                         : MMVQ_ERR_ROUTING;
     s.n_new = 0;
   }
-  const int end_tile = (int)(((int64_t)s.len + kKv4Tile - 1) / kKv4Tile);
+  // tiles past the page table are no work: a length that is wrong by much would otherwise be hours of it
+  const int64_t in_table = a.ld_table * (a.page_tokens / kKv4Tile);
+  int end_tile = (int)(((int64_t)s.len + kKv4Tile - 1) / kKv4Tile);
+  if (end_tile > in_table) {
+    end_tile = (int)in_table;
+    if (s.n_new > 0) *error = MMVQ_ERR_ROUTING;
+  }
   s.sink_tiles = s.skip = 0;
   if (p.window > 0) {
     const int64_t from = max((int64_t)0, (int64_t)s.len - s.n_new - p.window + 1);

@@ -65,3 +65,34 @@ def test_append_next_to_the_border_of_the_last_code(rows):
     w = where(bt)
     mmvq.kv4_append(dev(k), dev(v), *w)
     assert np.array_equal(host(w[0]), expected_cache(bt, k.astype(np.float64), v.astype(np.float64)))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 20), (2 ** 31 - 1, 0)])
+def test_attention_of_lengths_far_past_the_table(window, sinks):
+    """Only the table's tokens are looked at, however long the sequence says it is; the others are as if masked."""
+    bt = _kv4.Batch(64, 2, 16, [96, 40, 64], [2, 1, 8], seed=43, table_spare=0)   # 6 pages a row of the table
+    bt.fill_random()
+    q = torch.from_numpy(bt.rng.normal(size=(bt.n, 16, 64))).float()
+    lens = np.array([2 ** 31 - 1, 40, 2 ** 31 - 9], np.int32)
+    table = bt.table.copy()
+    table[1, 3:], table[2, 4:] = 0, bt.n_pages                                     # sequence 2: two pages that are not there
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, lse = mmvq.kv4_attention(q.cuda(), dev(bt.cache), dev(table), dev(bt.offsets), dev(lens), window=window,
+                                sinks=sinks, status=status, with_lse=True)
+    y, lse = host(y).astype(np.float64), host(lse)
+    assert int(host(status)[0]) == mmvq.ERR_ROUTING
+    far = window == 100                     # the window lies past the table: the sinks alone are seen
+    for b, rows in ((0, range(0, 2)), (2, range(3, 11))):
+        (k, kz, kd, _), (v, vz, vd, vc) = bt.sequence(b)
+        n = 20 if far else bt.lens[b]
+        for r in rows:
+            x = np.einsum("hgd,nhd->hgn", q[r].double().numpy().reshape(2, 8, 64), k[:n]) / 8
+            p = np.exp(x - x.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            want, a = (np.einsum("hgn,nhd->hgd", p, w[:n]).reshape(16, 64) for w in (v, vz + vd * vc))
+            s = np.einsum("hgd,nhd->hgn", np.abs(q[r].double().numpy().reshape(2, 8, 64)), kz[:n] + 15 * kd[:n]).max(-1).reshape(16) / 8
+            assert (np.abs(y[r] - want) <= bound("f32", want, a, s)).all()
+    bt.lens, bt.news, bt.offsets = [40], [1], np.array([0, 1], np.int32)
+    bt.table = bt.table[1:2]
+    want, _, a, s = _kv4.attention(bt, q[2:3].double().numpy(), 0.125, window, sinks)
+    assert (np.abs(y[2:3] - want) <= bound("f32", want, a, s)).all()
