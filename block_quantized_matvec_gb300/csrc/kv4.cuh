@@ -82,7 +82,7 @@ __device__ __forceinline__ bool kv4_place(const Kv4Batch& a, int r, int lane, Kv
     lo += last * step;
   }
   const int i = lo + min(lane, n - 1);
-  const int first = a.offsets[i], end = a.offsets[i + 1], len = a.lens[i];
+  const int first = a.offsets[i], end = a.offsets[i + 1], len = max(0, a.lens[i]);  // positions stay in range
   const uint32_t m = __ballot_sync(0xffffffffu, lane < n && first <= r);
   const int at = m ? 31 - __clz(m) : 0;
   s.b = lo + at;

@@ -96,3 +96,23 @@ def test_attention_of_lengths_far_past_the_table(window, sinks):
     bt.table = bt.table[1:2]
     want, _, a, s = _kv4.attention(bt, q[2:3].double().numpy(), 0.125, window, sinks)
     assert (np.abs(y[2:3] - want) <= bound("f32", want, a, s)).all()
+
+
+@pytest.mark.parametrize("rows", [4, 40])
+def test_negative_lengths_hold_nothing(rows):
+    """Down to the least number: no row is written, reads as anything but zeros, or counts as an error."""
+    bt = _kv4.Batch(64, 2, 16, [rows, rows], [rows, rows], seed=44)
+    bt.fill_random()
+    w = (*where(bt)[:3], dev(np.array([-2 ** 31, rows], np.int32)))
+    k, v = (dev(bt.rng.normal(size=(bt.n, 2, 64)).astype(np.float32)) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kr, vr = mmvq.kv4_read(*w, bt.n, status=status)
+    assert not host(kr)[:rows].any() and not host(vr)[:rows].any() and host(kr)[rows:].any(-1).all()
+    assert int(host(status)[0]) == 0
+    mmvq.kv4_append(k, v, *w, status=status)
+    bt.lens = [-2 ** 31, rows]
+    assert np.array_equal(host(w[0]), expected_cache(bt, host(k).astype(np.float64), host(v).astype(np.float64)))
+    y, lse = mmvq.kv4_attention(dev(bt.rng.normal(size=(2, 4, 64)).astype(np.float32)), *w[:2], dev(np.array([0, 1, 2], np.int32)), w[3],
+                                with_lse=True, status=status)
+    assert not host(y)[0].any() and np.isneginf(host(lse)[0]).all() and np.isfinite(host(lse)[1]).all()
+    assert int(host(status)[0]) == 0
