@@ -497,36 +497,44 @@ def kv4_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int,
                        dtype=torch.uint8, device=device)
 
 
-def _kv4_where(cache, page_table, offsets, lens):
-    """Checks the tensors of a batch: the cache's and the batch's arguments of the C calls."""
+def _kv4_where(cache, page_table, offsets, lens, status):
+    """Checks the tensors of a batch: its device's number, and the cache's and the batch's arguments of
+    the C calls."""
     n_pages, n_kv, tiles, tile_bytes = cache.shape
     n_seqs, ld = page_table.shape
-    if cache.dtype is not torch.uint8 or not cache.is_cuda or not cache.is_contiguous() or \
-            tile_bytes % 20:
+    dev = cache.get_device()  # -1: the host's
+    if cache.dtype is not torch.uint8 or dev < 0 or not cache.is_contiguous() or tile_bytes % 20:
         raise ValueError("cache must be a contiguous CUDA uint8 tensor [pages, kv heads, "
                          "page_tokens/16, 20*head_dim] (kv4_cache)")
     i32 = torch.int32
-    if page_table.dtype is not i32 or not page_table.is_cuda or not page_table.is_contiguous():
-        raise ValueError("page_table must be a contiguous CUDA int32 tensor")
-    if offsets.dtype is not i32 or not offsets.is_cuda or not offsets.is_contiguous() or \
+    if page_table.dtype is not i32 or page_table.get_device() != dev or \
+            not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 tensor on the cache's device")
+    if offsets.dtype is not i32 or offsets.get_device() != dev or not offsets.is_contiguous() or \
             offsets.numel() != n_seqs + 1:
-        raise ValueError(f"offsets must be a contiguous CUDA int32 tensor of {n_seqs + 1} values")
-    if lens.dtype is not i32 or not lens.is_cuda or not lens.is_contiguous() or \
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {n_seqs + 1} values on the "
+                         "cache's device")
+    if lens.dtype is not i32 or lens.get_device() != dev or not lens.is_contiguous() or \
             lens.numel() != n_seqs:
-        raise ValueError(f"lens must be a contiguous CUDA int32 tensor of {n_seqs} values")
-    return (cache.data_ptr(), n_pages, tiles * KV4_TILE, n_kv, tile_bytes // 20,
-            page_table.data_ptr(), ld, offsets.data_ptr(), lens.data_ptr(), n_seqs)
+        raise ValueError(f"lens must be a contiguous int32 tensor of {n_seqs} values on the cache's "
+                         "device")
+    if status is not None and (status.dtype is not i32 or status.get_device() != dev or
+                               status.numel() < 1):
+        raise ValueError("status must be an int32 tensor on the cache's device")
+    return dev, (cache.data_ptr(), n_pages, tiles * KV4_TILE, n_kv, tile_bytes // 20,
+                 page_table.data_ptr(), ld, offsets.data_ptr(), lens.data_ptr(), n_seqs)
 
 
-def _kv4_rows(t, heads, dim, name):
+def _kv4_rows(t, heads, dim, dev, name):
     """A [n, heads, dim] tensor with unit inner stride: its type's number, tokens, and the token and
     head strides."""
     n, h, d = t.shape
     ld, hs, one = t.stride()
     dtype = _DTYPES.get(t.dtype)
-    if dtype is None or not t.is_cuda or (heads and h != heads) or d != dim or (one != 1 and n):
-        raise ValueError(f"{name} must be a CUDA float32, float16 or bfloat16 tensor "
-                         f"[tokens, {heads or 'heads'}, {dim}] with unit inner stride")
+    if dtype is None or t.get_device() != dev or (heads and h != heads) or d != dim or \
+            (one != 1 and n):
+        raise ValueError(f"{name} must be a float32, float16 or bfloat16 tensor [tokens, "
+                         f"{heads or 'heads'}, {dim}] with unit inner stride on the cache's device")
     return dtype, n, h, ld, hs
 
 
@@ -536,9 +544,9 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table
     """Quantises keys and values [n, kv heads, head_dim] into the cache: rows
     offsets[b]..offsets[b+1]-1 are the last tokens of sequence b, whose length with them is
     lens[b]; position p of it lies in page page_table[b, p // page_tokens].  (mmvq_kv4_append)"""
-    where = _kv4_where(cache, page_table, offsets, lens)
-    dtype, n, _, ldk, hk = _kv4_rows(k, where[3], where[4], "k")
-    dtype_v, n_v, _, ldv, hv = _kv4_rows(v, where[3], where[4], "v")
+    dev, where = _kv4_where(cache, page_table, offsets, lens, status)
+    dtype, n, _, ldk, hk = _kv4_rows(k, where[3], where[4], dev, "k")
+    dtype_v, n_v, _, ldv, hv = _kv4_rows(v, where[3], where[4], dev, "v")
     if n_v != n or dtype_v != dtype:
         raise ValueError("k and v must have the same tokens and type")
     _check(lib().mmvq_kv4_append(dtype, k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv, *where, n,
@@ -551,7 +559,7 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tenso
              status: torch.Tensor | None = None, stream=None):
     """(k, v), each [n_tokens, kv heads, head_dim] of dtype: the cached values of the last
     offsets[b+1]-offsets[b] of the first lens[b] tokens of each sequence b.  (mmvq_kv4_read)"""
-    where = _kv4_where(cache, page_table, offsets, lens)
+    dev, where = _kv4_where(cache, page_table, offsets, lens, status)
     number = _DTYPES.get(dtype)
     if number is None:
         raise ValueError("dtype must be float32, float16 or bfloat16")
@@ -562,8 +570,10 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, offsets: torch.Tenso
     else:
         k, v = out
         for t in out:
-            if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"out must be two contiguous CUDA tensors {list(shape)} of {dtype}")
+            if t.shape != shape or t.dtype != dtype or t.get_device() != dev or \
+                    not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous tensors {list(shape)} of {dtype} on the "
+                                 "cache's device")
     _check(lib().mmvq_kv4_read(number, k.data_ptr(), v.data_ptr(), *where, n_tokens,
                                _ptr(status), _stream(stream)), "mmvq_kv4_read")
     return k, v
@@ -599,23 +609,25 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     last `window` of them and the first `sinks` of the sequence.  scale defaults to
     head_dim**-0.5; workspace: kv4_attention_workspace, zeroed before this call on its stream
     (a temporary one otherwise).  (mmvq_kv4_attention)"""
-    where = _kv4_where(cache, page_table, offsets, lens)
+    dev, where = _kv4_where(cache, page_table, offsets, lens, status)
     dim = where[4]
-    dtype, n, heads, ldq, hq = _kv4_rows(q, 0, dim, "q")
+    dtype, n, heads, ldq, hq = _kv4_rows(q, 0, dim, dev, "q")
     if out is None:
         out = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or not out.is_contiguous():
-        raise ValueError("out must be a contiguous CUDA tensor of q's shape and type")
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != dev or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and type on its device")
     if lse is None and with_lse:
         lse = _made(stream, q.new_empty, (n, heads), dtype=torch.float32)
     elif lse is not None and (lse.shape != (n, heads) or lse.dtype != torch.float32 or
-                              not lse.is_cuda or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous CUDA float32 tensor [tokens, heads]")
+                              lse.get_device() != dev or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [tokens, heads] on q's device")
     if workspace is None:
         workspace = _made(stream, kv4_attention_workspace, dim, q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or \
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or \
             workspace.nbytes < kv4_attention_workspace_bytes(dim):
-        raise ValueError("workspace is too small: kv4_attention_workspace(head_dim, device)")
+        raise ValueError("workspace is too small or on another device: "
+                         "kv4_attention_workspace(head_dim, device)")
     _check(lib().mmvq_kv4_attention(dtype, q.data_ptr(), ldq, hq, heads,
                                     dim ** -0.5 if scale is None else scale, window, sinks,
                                     out.data_ptr(), _ptr(lse), *where, n, workspace.data_ptr(),

@@ -10,8 +10,17 @@ from block_quantized_matvec_gb300 import mmvq
 
 
 class Tensor(torch.Tensor):
-    """A CPU tensor that says it is on the GPU."""
+    """A CPU tensor that says it is on a GPU."""
     is_cuda = True
+    number = 0
+
+    def get_device(self):
+        return self.number
+
+
+class Elsewhere(Tensor):
+    """One that says it is on another."""
+    number = 1
 
 
 def tensor(shape, dtype):
@@ -57,6 +66,7 @@ def calls(monkeypatch):
                                  mmvq_kv4_attention_workspace_bytes=lambda dim: 1024)
     monkeypatch.setattr(mmvq, "lib", lambda: fake)
     monkeypatch.setattr(mmvq, "_workspace_bytes", {})
+    monkeypatch.setattr(mmvq, "_stream", lambda s: s and s.cuda_stream)
     return seen
 
 
@@ -85,3 +95,38 @@ def test_so_are_the_products_and_the_expert_layers(calls):
         calls.clear()
         call()
         assert len(calls) > 1 and calls[-1] == ("launch", 77) and all(s is side for _, s in calls[:-1])
+
+
+def test_status_and_tensors_of_other_places_are_refused(calls):
+    """Their addresses go to the kernels as they are."""
+    where, q, k = batch(), tensor((1, 2, 64), torch.float32), tensor((1, 1, 64), torch.float32)
+    workspace = tensor((1024,), torch.uint8)
+    each = (lambda w, q, k, workspace, **kw: mmvq.kv4_append(k, k, *w, **kw),
+            lambda w, q, k, workspace, **kw: mmvq.kv4_read(*w, 1, **kw),
+            lambda w, q, k, workspace, **kw: mmvq.kv4_attention(q, *w, workspace=workspace, **kw))
+    plain = lambda t: t.as_subclass(torch.Tensor)  # noqa: E731
+    for call in each:
+        call(where, q, k, workspace, status=tensor((1,), torch.int32))
+    calls.clear()
+    for call in each:
+        for status in (torch.zeros(1, dtype=torch.int32), tensor((1,), torch.int64), tensor((0,), torch.int32),
+                       tensor((1,), torch.int32).as_subclass(Elsewhere)):
+            with pytest.raises(ValueError):
+                call(where, q, k, workspace, status=status)
+        for to in (plain, lambda t: t.as_subclass(Elsewhere)):
+            for i in range(4):
+                with pytest.raises(ValueError):
+                    call((*where[:i], to(where[i]), *where[i + 1:]), q, k, workspace)
+    for to in (plain, lambda t: t.as_subclass(Elsewhere)):
+        for args in ((q, to(k), workspace), (to(q), k, workspace), (q, k, to(workspace))):
+            for call in (each[0], each[2]):
+                if (call is each[0]) == (args[1] is not k):
+                    with pytest.raises(ValueError):
+                        call(where, *args)
+        with pytest.raises(ValueError):
+            mmvq.kv4_read(*where, 1, out=(k, to(k)))
+        with pytest.raises(ValueError):
+            mmvq.kv4_attention(q, *where, workspace=workspace, out=to(q.clone()))
+        with pytest.raises(ValueError):
+            mmvq.kv4_attention(q, *where, workspace=workspace, lse=to(tensor((1, 2), torch.float32)))
+    assert not [name for name, _ in calls if name == "launch"]
