@@ -143,7 +143,7 @@ struct Smem {
   float row_factor[S::kRows];
   int row_pos[S::kRows];
   Kv4JoinSmem<S::kRows> join;       // of the warps' results, then of an item's parts
-  Kv4Plan<S::kThreads, true> plan;
+  Kv4Plan<S::kThreads> plan;
   static_assert(kRing >= S::kRows * S::D * 4, "a warp's results fit its ring");
 };
 

@@ -72,26 +72,25 @@ __device__ __forceinline__ void kv4_load_values(const T* src, bool vector, float
   for (int i = 0; i < N; ++i) q[i] = kv4_load(src + i);
 }
 
-// The units of a batch before each thread's sequences, in shared memory; kKeep: the sequences too, where each
-// thread has one.
-template <int kThreads, bool kKeep>
+// The units of a batch before each thread's sequences, in shared memory, and where each thread has one, the sequences.
+template <int kThreads>
 struct Kv4Plan {
   int64_t before[kThreads];
   int64_t warp_units[kThreads / 32];
-  Kv4Seq seq[kKeep ? kThreads : 1];
+  Kv4Seq seq[kThreads];
 };
 
 // Fills the plan (by all threads of the CTA); the batch's units.
-template <int kThreads, bool kKeep>
+template <int kThreads>
 __device__ __forceinline__ int64_t kv4_plan(const Kv4Batch& a, const Kv4Attention& p, int rows_block,
-                                            Kv4Plan<kThreads, kKeep>& plan, int tid) {
+                                            Kv4Plan<kThreads>& plan, int tid) {
   const int lane = tid & 31, warp = tid >> 5;
   const int chunk = (a.n_seqs + kThreads - 1) / kThreads;
   int error = 0;
   int64_t mine = 0;
   for (int b = tid * chunk; b < min(a.n_seqs, (tid + 1) * chunk); ++b) {
     const Kv4Seq s = kv4_seq(a, p, rows_block, b, &error);
-    if (kKeep && chunk == 1) plan.seq[tid] = s;
+    if (chunk == 1) plan.seq[tid] = s;
     mine += (int64_t)a.n_kv_heads * s.blocks * s.item_units();
   }
   if (error && blockIdx.x == 0) kv4_set_status(a.status, error);
@@ -129,9 +128,9 @@ struct Kv4Item {
 };
 
 // The item of `unit`, which is moved past this CTA's part of it.  False where that part holds none of its tiles.
-template <int kThreads, bool kKeep>
+template <int kThreads>
 __device__ __forceinline__ bool kv4_next(const Kv4Batch& a, const Kv4Attention& p, int rows_block,
-                                         const Kv4Plan<kThreads, kKeep>& plan, const Shares& shares, int cta,
+                                         const Kv4Plan<kThreads>& plan, const Shares& shares, int cta,
                                          int64_t& unit, Kv4Item& it) {
   const int64_t lo = shares.begin(cta), hi = shares.begin(cta + 1);
   const int chunk = (a.n_seqs + kThreads - 1) / kThreads;
@@ -141,7 +140,7 @@ __device__ __forceinline__ bool kv4_next(const Kv4Batch& a, const Kv4Attention& 
     if (th + o < kThreads && plan.before[th + o] <= unit) th += o;
   it.b = th * chunk;
   int64_t at = plan.before[th];
-  it.s = kKeep && chunk == 1 ? plan.seq[kKeep ? th : 0] : kv4_seq(a, p, rows_block, it.b, &error);
+  it.s = chunk == 1 ? plan.seq[th] : kv4_seq(a, p, rows_block, it.b, &error);
   for (;;) {
     const int64_t units = (int64_t)a.n_kv_heads * it.s.blocks * it.s.item_units();
     if (at + units > unit) break;

@@ -116,3 +116,15 @@ def test_negative_lengths_hold_nothing(rows):
                                 with_lse=True, status=status)
     assert not host(y)[0].any() and np.isneginf(host(lse)[0]).all() and np.isfinite(host(lse)[1]).all()
     assert int(host(status)[0]) == 0
+
+
+@pytest.mark.parametrize("D,kv,group,dtype", [(128, 3, 2, "bf16"), (128, 2, 8, "f32"), (256, 2, 2, "f32"), (64, 2, 8, "f16")])
+def test_more_sequences_than_a_cta_has_threads(D, kv, group, dtype):
+    """400 and more, so that a thread takes several; empty ones between them, and a few long enough to be split."""
+    n = 400 if D == 256 else 1030
+    lens = [(7 * i) % 29 if i % 5 else 0 for i in range(n)]
+    lens[3], lens[n // 2], lens[n - 1] = 2500, 1111, 3000
+    news = [0 if i % 7 == 2 else 1 + i % 2 for i in range(n)]
+    bt = _kv4.Batch(D, kv, 32, lens, news, seed=45)
+    bt.fill_random()
+    check_attention(bt, kv * group, dtype)
