@@ -7,7 +7,7 @@ import torch
 from block_quantized_matvec_gb300 import mmvq
 from tests import _kv4
 from tests._gpu import dev, host
-from tests.test_gpu_kv4 import bound, check_attention, expected_cache, where
+from tests.test_gpu_kv4 import TYPES, bound, check_attention, expected_cache, where
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,36 @@ def test_more_sequences_than_a_cta_has_threads(D, kv, group, dtype):
     bt = _kv4.Batch(D, kv, 32, lens, news, seed=45)
     bt.fill_random()
     check_attention(bt, kv * group, dtype)
+
+
+def shared_rows(bt, q, rows):
+    """Attention of `rows` sequences that share bt's one sequence and its query: y in float64."""
+    w = (dev(bt.cache), dev(np.repeat(bt.table, rows, 0)), dev(np.arange(rows + 1, dtype=np.int32)), dev(np.full(rows, bt.lens[0], np.int32)))
+    return host(mmvq.kv4_attention(q.cuda().expand(rows, -1, -1), *w).double())
+
+
+@pytest.mark.parametrize("D,group", [(64, 4), (128, 12), (256, 6), (256, 12)])
+def test_long_sums_keep_their_precision(D, group):
+    """Enough sequences of 65536 tokens that a warp adds up a hundred tiles and more, under nearly even probabilities,
+    values with an offset: within the bound of a short sequence, whose chains of products are those of one tile."""
+    bt = _kv4.Batch(D, 1, 256, [65536], [1], seed=46)
+    bt.fill_random()
+    z = bt.cache.view(np.float16)[..., 9 * D + D // 2:]
+    z[:] = np.where(np.isfinite(z), np.abs(z) + np.float16(0.25), z)
+    q = torch.from_numpy(bt.rng.normal(size=(1, group, D)) * 0.01).float()
+    want, _, a, s = _kv4.attention(bt, q.double().numpy(), D ** -0.5)
+    got = shared_rows(bt, q, 64)
+    off = np.abs(got - want)
+    assert (off <= bound("f32", want, a, s)).all(), f"{(off / bound('f32', want, a, s)).max():.2f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_long_sums_that_cancel(dtype):
+    """Values of both signs under nearly even probabilities, a hundred tiles and more a warp: what the kernel adds
+    stays below three quarters of the output's own rounding."""
+    bt = _kv4.Batch(256, 1, 256, [65536], [1], seed=47)
+    bt.fill_random()
+    q = torch.from_numpy(bt.rng.normal(size=(1, 12, 256)) * 0.05).to(TYPES[dtype])
+    want = _kv4.attention(bt, q.double().numpy(), 1 / 16)[0]
+    rounding = np.linalg.norm(torch.from_numpy(want).to(TYPES[dtype]).double().numpy() - want)
+    assert max(np.linalg.norm(row - want[0]) for row in shared_rows(bt, q, 64)) <= 1.25 * rounding
