@@ -161,3 +161,29 @@ def test_long_sums_that_cancel(dtype):
     want = _kv4.attention(bt, q.double().numpy(), 1 / 16)[0]
     rounding = np.linalg.norm(torch.from_numpy(want).to(TYPES[dtype]).double().numpy() - want)
     assert max(np.linalg.norm(row - want[0]) for row in shared_rows(bt, q, 64)) <= 1.25 * rounding
+
+
+@pytest.mark.parametrize("n,longest", [(33, 90), (300, 2), (1100, 40)])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 128), ("f16", 256)])
+def test_append_and_read_of_many_sequences(n, longest, dtype, D):
+    """More than a warp has lanes, so that a row's sequence is found in two steps or three, empty ones between them;
+    with few rows each, and with tiles of them."""
+    news = [(5 * i) % (longest + 1) if i % 4 else 0 for i in range(n)]
+    lens = [t + (3 * i) % 19 for i, t in enumerate(news)]
+    bt = _kv4.Batch(D, 1, 16, lens, news, seed=48, fill=0)
+    x = torch.from_numpy(bt.rng.normal(size=(2, bt.n, 1, D))).to(TYPES[dtype])
+    w = where(bt)
+    mmvq.kv4_append(x[0].cuda(), x[1].cuda(), *w)
+    k, v = mmvq.kv4_read(*w, bt.n, dtype=TYPES[dtype])
+    for got, rows in ((k, x[0]), (v, x[1])):
+        want = _kv4.values(*_kv4.quantise(rows.double().numpy())).astype(np.float32)
+        assert torch.equal(got.cpu(), torch.from_numpy(want).to(TYPES[dtype]))
+
+
+@pytest.mark.parametrize("D,kv,group,dtype", [(128, 2, 5, "f16"), (64, 2, 4, "f16"), (64, 1, 16, "bf16"), (256, 2, 3, "f16"),
+                                              (256, 1, 12, "bf16"), (256, 1, 12, "f32")])
+@pytest.mark.parametrize("window,sinks", [(40, 4), (130, 0), (1000, 17)])
+def test_windows_of_every_head_size_and_type(D, kv, group, dtype, window, sinks):
+    bt = _kv4.Batch(D, kv, 32, [700, 40, 5, 0, 171, 64], [1, 2, 3, 1, 1, 8], seed=49)
+    bt.fill_random()
+    check_attention(bt, kv * group, dtype, window=window, sinks=sinks)
