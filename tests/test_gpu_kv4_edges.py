@@ -163,7 +163,7 @@ def test_long_sums_that_cancel(dtype):
     assert max(np.linalg.norm(row - want[0]) for row in shared_rows(bt, q, 64)) <= 1.25 * rounding
 
 
-@pytest.mark.parametrize("n,longest", [(33, 90), (300, 2), (1100, 40)])
+@pytest.mark.parametrize("n,longest", [(33, 90), (300, 2), (1100, 60), (1100, 3)])
 @pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 128), ("f16", 256)])
 def test_append_and_read_of_many_sequences(n, longest, dtype, D):
     """More than a warp has lanes, so that a row's sequence is found in two steps or three, empty ones between them;
