@@ -34,8 +34,8 @@
 //  - one row tile, D = 128 (64 bf16 sequences of 128 .. 8192 tokens, 32 / 8
 //    heads, 337 MB): 77 us, 4.4 TB/s.  The instructions: 61% of the issue slots,
 //    48% of the ALU pipe (masking codes out of words), tensor pipe 22%.
-//    Four CTAs of 4 warps an SM at 128 registers: 77 us; two of 8: 80; one of 12
-//    with 168 registers: 114.
+//    Three CTAs of 4 warps an SM at 168 registers: 77 us; four at 128: 81; one of
+//    12 at 168, which begins and ends its items alone: 114.
 //  - two row tiles, D = 256: the latency of 8 warps an SM at 255 registers (128 of
 //    them accumulators).  131071 fp32 tokens, 24 / 2 heads, 84 MB: 52 us, of which
 //    28 tiles and 10 joining 76 parts a head; tensor pipe 34%, issue 36%.  8 x 8
@@ -128,10 +128,12 @@ struct Shape {
   static constexpr bool QS = QS_;
   static constexpr int nb = D / 32, kGroups = nb > 4 ? nb / 4 : 1, kOfGroup = nb / kGroups;  // blocks
   static constexpr int kRows = 8 * NT;
-  // four CTAs of 4 warps and 128 registers a thread; one of 12 and 168 or of 8 and 255 where the accumulators
-  // (4 registers per 16 values and row tile) need them
+  // The accumulators, 4 registers per 16 values and row tile, and the ring, 80 D bytes a warp, decide.  32 accumulators
+  // at most: four CTAs of 4 warps and 128 registers a thread; of these D = 128, whose loads and masks spill at that
+  // (64 bf16 sequences 81 us), three and 168 (77).  64 of D = 128: one CTA of 12 warps and 168.  D = 256: 8 warps and
+  // 255, with 128 accumulators for want of registers, with 64 because the rings of 12 do not fit.
   static constexpr int kWarps = D * NT <= 128 ? 4 : D == 128 ? 12 : 8;
-  static constexpr int kCtas = D * NT <= 128 ? 4 : 1;
+  static constexpr int kCtas = D * NT <= 128 ? (D == 128 ? 3 : 4) : 1;
   static constexpr int kThreads = 32 * kWarps;
   static_assert(kCtas <= kKv4MaxCtasSm && kCtas * kRows <= kv4_rows_sm(D), "the workspace");
   static constexpr int kBytes = kv4_tile_bytes(D);
