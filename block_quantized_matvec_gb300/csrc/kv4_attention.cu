@@ -16,7 +16,13 @@
 // A = c - 8, B = p d per block of 32; sum(p z) and sum(p d) one more product.
 //
 // Precision.  fp32 q enters as two fp16 parts (22 bits), and for fp32 and fp16
-// the products p d do too; bf16 keeps 11 bits of p d, finer than its own 8.
+// the products p d do too.  bf16 keeps 11 bits of p and of p d, finer than its
+// own 8: outputs next to the middle of two bf16 numbers then round to the other
+// one (2e-4 off an fp32 form in 2-norm, while both are 1.7e-3 off 64 bits); two
+// parts cost 15 to 18% (64 sequences 83 -> 98 us).  For fp16 and bf16 the keys'
+// codes are subnormal, and a sum of 16 products keeps about 17 bits of the
+// largest: the log-sum-exp is 1e-7 to 6e-7 off, with c - 8 there too 3e-8 to
+// 1.5e-7 at 3 to 7% of the time.
 // Sums over tokens: a tile's products start from zero and are added in fp32, rounded to nearest.  The tensor core
 // cuts its sum off towards zero at every product, which is of no account within a tile, but where it keeps the sum
 // of all tiles is 1.3e-7 a tile that the sum falls short (fp32, 131072 tokens a sequence, one-signed midpoints:
@@ -27,23 +33,25 @@
 // sum, and each block of a value its own on the probability, so a product
 // reaches over 32 values only, and the accumulators are needed in registers
 // between them.  (Decoded to fp16 for tcgen05 instead, keys keep 11 bits: with
-// 96 rows of bf16 that took 124 us against 144 here, but put the log-sum-exp
-// 2e-4 off; two parts of each key do not fit shared memory next to 128 rows of Q.)
+// 96 rows of bf16 an attempt took 124 us against 144, with the log-sum-exp 2e-4
+// off, inside 2^-18 of the products' magnitudes.  Keys in two parts fit shared
+// memory next to 128 rows of Q in steps of 32 tokens; that has not been built.)
 //
 // What bounds it, measured on GB300 (6768 GB/s copied):
 //  - one row tile, D = 128 (64 bf16 sequences of 128 .. 8192 tokens, 32 / 8
 //    heads, 337 MB): 77 us, 4.4 TB/s.  The instructions: 61% of the issue slots,
-//    48% of the ALU pipe (masking codes out of words), tensor pipe 22%.
+//    43% of the ALU pipe (masking codes out of words), tensor pipe 22%.
 //    Three CTAs of 4 warps an SM at 168 registers: 77 us; four at 128: 81; one of
 //    12 at 168, which begins and ends its items alone: 114.
 //  - two row tiles, D = 256: the latency of 8 warps an SM at 255 registers (128 of
-//    them accumulators).  131071 fp32 tokens, 24 / 2 heads, 84 MB: 52 us, of which
-//    28 tiles and 10 joining 76 parts a head; tensor pipe 34%, issue 36%.  8 x 8
-//    query tokens over 16389, bf16: 144 us, tensor pipe 34%, issue 44%.  Splitting
-//    the values between two warps (175), 32 rows a warp (159) and two CTAs of 4
-//    warps (142; but 59 instead of 52 on the former) were no better.
-//  - short batches: about 10 us for 77 tokens: work division 1, first tile and
-//    queries 3, a tile 3 (its code is fetched for the first time), results 3.
+//    them accumulators).  131071 fp32 tokens, 24 / 2 heads, 84 MB: 55 us, of which
+//    about 31 tiles and 10 joining 76 parts a head; tensor pipe 32%, issue 38%.
+//    8 x 8 query tokens over 16389, bf16: 146 us, tensor pipe 33%, issue 51%.
+//    Without the additions (52 and 144 us), splitting the values between two warps
+//    (175 for the latter), 32 rows a warp (159) and two CTAs of 4 warps (142; but 59
+//    instead of 52 for the former) were no better.
+//  - short batches, 14 us for 77 tokens: work division, first tile and queries, the
+//    tile (its code is fetched for the first time) and results follow one another.
 #include "kv4.cuh"
 #include "kv4_work.cuh"
 
@@ -485,7 +493,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) move |= fmaxf(x[n][e], x[n][e + 2]) > bar[n][e];
-      if (__any_sync(0xffffffffu, move || ((vs[0] | vs[1]) & 0x40004000u))) {  // or a step of 2 or more
+      // or a step of 2 or more, also one that E covers: then every tile comes here (64 bf16 sequences 77 us, 81 with
+      // steps up to 2.8, 88 with steps up to 11)
+      if (__any_sync(0xffffffffu, move || ((vs[0] | vs[1]) & 0x40004000u))) {
         uint32_t top = max(max(vs[0] & 0xffffu, vs[0] >> 16), max(vs[1] & 0xffffu, vs[1] >> 16));
         top = __reduce_max_sync(0xffffffffu, top);
         const int E2 = max(E, (int)(top >> 10) - 15);  // its exponent
@@ -567,10 +577,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
           uint32_t a0, a1, a2, a3;
-          // c - 8 here and 0.5 sum(p d) at the end.  Codes as they are, with -7.5 sum(p d), cost less (32 fp16
-          // windows of 4096 tokens: 47.2 us, 48.7 with c - 8), but where the probabilities are even the two sums
-          // cancel: over 131072 tokens at D = 256 the error is then 2.5 times the fp16 output's own rounding, and
-          // 1.01 times with c - 8.
+          // c - 8 here and 0.5 sum(p d) at the end.  Codes as they are, with -7.5 sum(p d), cost 3% less for fp16, but
+          // where the probabilities are even the two sums cancel: over 131072 tokens at D = 256 the error was then 2.5
+          // times the fp16 output's own rounding, and 1.01 times with c - 8.  2 c - 15, which needs no sum(p d), takes
+          // a shift more a word: 64 bf16 sequences 82 us.
           centred(w0, w1, a0, a2, a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {

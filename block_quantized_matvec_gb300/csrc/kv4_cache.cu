@@ -11,14 +11,14 @@
 // takes one row, so that a decode step's rows spread over the GPU.
 //
 // Measured on GB300 (6768 GB/s copied).  Append of 24575 fp32 tokens, 2 heads of
-// 256 (116 MB): 23.4 us, 5.0 TB/s; of 24 bf16 prompts of 50 .. 1201 tokens behind 37
-// cached ones, 8 heads of 128 (71 MB): 38.5 us, 1.8 TB/s.  Both are bound by
-// instructions and the latency of a warp's few loads (60 to 66% of the issue
-// slots; about 20 instructions a value).  CTAs of 2 warps: a warp that finds
+// 256 (116 MB): 23.7 us, 4.9 TB/s; of 24 bf16 prompts of 50 .. 1201 tokens behind 37
+// cached ones, 8 heads of 128 (81 MB): 38.4 us, 2.1 TB/s.  Both are bound by
+// instructions and the latency of a warp's few loads (55 to 66% of the issue
+// slots; 21 and 24 instructions a value).  CTAs of 2 warps: a warp that finds
 // nothing to do, or two segments, holds up no others (8 warps: 24.5 and 43 us).
 // Read of 65536 bf16 tokens, 8 heads of 128 (352 MB): 55 us, 6.4 TB/s, DRAM: 20
 // warps an SM with all of a tile's words in flight (24: 56 us, 32: 63, 40: 75).
-// One row a warp: 4 us for one token, launch and three loads in a row.
+// One row a warp: 4.4 us for one token, launch and three loads in a row.
 #include "kv4.cuh"
 
 namespace mmvq {

@@ -1,8 +1,9 @@
 // The division of an attention batch's work among the CTAs, and the joining of
 // items that were split.  An item's fixed cost counts as 32 tiles and a CTA takes
-// 16 units at least: 64 sequences of 128 .. 8192 tokens took 102 us with 16 units an
-// item, 87 with 32 and 89 with 64 (then); joins of over 24 parts go in two steps of
-// about their square root, since one CTA reads them all.
+// 16 units at least: 64 bf16 sequences of 128 .. 8192 tokens take 80.4 us with 16
+// units an item, 76.3 with 24, 76.7 with 32 and 82.1 with 64; 32 fp16 windows of 4096
+// 50.8, 50.2, 50.7 and 54.9.  Joins of over 24 parts go in two steps of about their
+// square root, since one CTA reads them all.
 #pragma once
 #include "kv4_attention.cuh"
 

@@ -135,7 +135,8 @@ enum mmvq_status {
 /* Element types of the plain tensors of the key/value cache calls (GGUF's numbers). */
 enum mmvq_dtype { MMVQ_F32 = 0, MMVQ_F16 = 1, MMVQ_BF16 = 30 };
 
-/* Version of this ABI (major*10000 + minor*100 + patch). */
+/* Version of this ABI (major*10000 + minor*100 + patch).  Entry points and status codes that are
+ * only added leave it as it is; a caller that can do without one looks it up by name. */
 MMVQ_API int mmvq_version(void);
 
 /* Human-readable text for a status code (static storage). */
@@ -469,8 +470,14 @@ MMVQ_API int mmvq_kv4_read(int dtype, void* k, void* v, const void* cache, int64
  * y ([n_tokens][n_heads][head_dim] of dtype, contiguous) = sum softmax(scale *
  * q.k) v over the seen tokens, zeros where there are none; lse (may be NULL):
  * fp32 [n_tokens][n_heads], log(sum(exp(scale * q.k))), -inf where there are
- * none.  Scores, the softmax and the sums are fp32; fp32 q and, for fp32 and
- * fp16, the weighted probabilities enter the products with about 22 bits.
+ * none.  The softmax and the sums over tokens are fp32.  Scores are fp32 sums
+ * over blocks; fp32 q enters their products with about 22 bits, and for fp16
+ * and bf16 q a sum of 16 products keeps about 17 bits of the largest of them
+ * (lse: measured 2e-7 of itself for fp32, up to 7e-7 for fp16 and bf16; every
+ * type is tested to 2^-18 of scale * sum |q| (|z| + 15 d) of the key where that
+ * is largest, plus 2^-20 (1 + |lse|)).  The weighted probabilities enter the
+ * products with about 22 bits for fp32 and fp16, and with 11 for bf16, whose
+ * outputs can therefore round to the neighbour of what an fp32 form rounds to.
  * Results do not depend on the run: parts of a sequence are added in a fixed
  * order.  Masked places never reach y or lse: what lies in the cache past a
  * sequence's length may hold anything.  A NaN or infinite query gives NaN in
