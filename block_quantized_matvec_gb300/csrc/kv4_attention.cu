@@ -4,8 +4,8 @@
 // S^T[tokens x rows] = K Q^T from m16n8k16 f16 products whose A operand is the
 // tile's codes: masked out of its word a code c stands, as the bits of an
 // fp16, for c * 2^-24 (low nibble of a byte) or c * 2^-20 (high nibble), so a
-// key costs no conversion; for fp32 queries, and in values, it becomes c - 8
-// (centred() below).
+// key costs no conversion; for fp32 queries it becomes c - 8, in values c - 8 or
+// c - 7 (centred() below).
 // The rows of Q are scaled by a power of two each, and by 16 more where they
 // meet low nibbles.  Per block of 32 the sum is multiplied by the block's d in
 // fp32; sum(z sum(q)) and sum(d sum(q)) (the codes' offset) over the blocks
@@ -13,7 +13,8 @@
 // p = 2^(s - m + 12) use a reference m that is only moved when a score exceeds
 // it by 2 (in log2 units): the result does not depend on m, and most tiles skip
 // the maximum across lanes and the rescaling.  O^T[values x rows] += V^T P':
-// A = c - 8, B = p d per block of 32; sum(p z) and sum(p d) one more product.
+// A = c - 8 (even tokens) or c - 7 (odd), B = p d per block of 32; sum(p z) and
+// sum(+-p d) one more product.
 //
 // Precision.  fp32 q enters as two fp16 parts (22 bits), and for fp32 and fp16
 // the products p d do too.  bf16 keeps 11 bits of p and of p d, finer than its
@@ -26,8 +27,8 @@
 // Sums over tokens: a tile's products start from zero and are added in fp32, rounded to nearest.  The tensor core
 // cuts its sum off towards zero at every product, which is of no account within a tile, but where it keeps the sum
 // of all tiles is 1.3e-7 a tile that the sum falls short (fp32, 131072 tokens a sequence, one-signed midpoints:
-// 1.4e-5 off after 108 tiles of a warp, 1.5e-4 after 1700; with the additions 1.6e-7 after any number).  They cost
-// 3 to 6% of the time (64 bf16 sequences 77.5 -> 81 us).
+// 1.4e-5 off after 108 tiles of a warp, 1.5e-4 after 1700; with the additions 1.2e-7 and 2.3e-7).  They cost 2 to 5% of
+// the time (131071 fp32 tokens 53 -> 55 us).
 //
 // Why warp-level products.  Each 32-block of a key has its own factor on the
 // sum, and each block of a value its own on the probability, so a product
@@ -84,6 +85,17 @@ __device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(b0));
 }
 
+// c += a, rounded to nearest, two numbers an instruction.
+__device__ __forceinline__ void add4(float (&c)[4], const float (&a)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(c[e]), "+f"(c[e + 1])
+        : "f"(a[e]), "f"(a[e + 1]));
+  }
+}
+
 // Transposes an 8 x 8 matrix of fp16 held two of a row a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -102,21 +114,23 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The codes of two words, low nibbles in a0 and a1, high ones in a2 and a3: as they are, or as c - 8 and 16 (c - 8),
-// set below 1024 as the mantissa's last bits, exactly, from which 1024 and the centre are taken off.  The tensor core
-// aligns a subnormal by its nominal exponent and cuts off what lies far below it (sums then keep about 17 bits);
-// these are normal numbers.
+// The codes of two words, low nibbles in a0 and a1, high ones in a2 and a3: as they are, or less a centre of 8 (in the
+// halves' second one kOdd, 8 or 7) as c - 8 and 16 (c - 8), exactly: set below 1024 as the mantissa's last bits, from
+// which 1024 and the centre are taken off.  The tensor core aligns a subnormal by its nominal exponent and cuts off
+// what lies far below it (sums then keep about 17 bits); these are normal numbers.
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {  // one instruction
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+template <int kOdd>
 __device__ __forceinline__ void centred(uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1, uint32_t& a2,
                                         uint32_t& a3) {
-  a0 = add2(and_or(w0, 0x000f000fu, 0x64006400u), 0xe408e408u);  // - 1032
-  a1 = add2(and_or(w1, 0x000f000fu, 0x64006400u), 0xe408e408u);
-  a2 = add2(and_or(w0, 0x00f000f0u, 0x64006400u), 0xe480e480u);  // - 1152
-  a3 = add2(and_or(w1, 0x00f000f0u, 0x64006400u), 0xe480e480u);
+  constexpr uint32_t low = 0xe400e408u + (kOdd << 16), high = 0xe400e480u + (kOdd << 20);  // - 1032, - 1152
+  a0 = add2(and_or(w0, 0x000f000fu, 0x64006400u), low);
+  a1 = add2(and_or(w1, 0x000f000fu, 0x64006400u), low);
+  a2 = add2(and_or(w0, 0x00f000f0u, 0x64006400u), high);
+  a3 = add2(and_or(w1, 0x00f000f0u, 0x64006400u), high);
 }
 __device__ __forceinline__ void plain(uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1, uint32_t& a2,
                                       uint32_t& a3) {
@@ -424,7 +438,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = kw[b2] >> (8 * hh), w1 = kw[nb + b2] >> (8 * hh);
-          if constexpr (QS) centred(w0, w1, ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
+          if constexpr (QS) centred<8>(w0, w1, ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
           else plain(w0, w1, ka[hh][0], ka[hh][1], ka[hh][2], ka[hh][3]);
         }
 #pragma unroll
@@ -451,12 +465,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       }
 
       // ---- values: steps of the lane's token pairs (2c, 2c + 1) + 8 h, midpoints of block g
-      uint32_t ds[2 * nb], vz[2], vs[2] = {0u, 0u};  // and the steps of block g
+      constexpr uint32_t kOddSign = 0x80000000u;  // of the high half, the odd token
+      uint32_t ds[2 * nb], vz[2], vs[2] = {0u, 0u};  // and the steps of block g, less for the odd tokens
       load_words(tp + 18 * D + 8 * nb * c, ds);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint8_t* at = tp + 18 * D + 8 * nb * c + 4 * (h * nb + g);
-        vs[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+        vs[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at) ^ kOddSign : 0u;
         vz[h] = g < nb ? *reinterpret_cast<const uint32_t*>(at + D) : 0u;
       }
 
@@ -496,7 +511,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       // or a step of 2 or more, also one that E covers: then every tile comes here (64 bf16 sequences 77 us, 81 with
       // steps up to 2.8, 88 with steps up to 11)
       if (__any_sync(0xffffffffu, move || ((vs[0] | vs[1]) & 0x40004000u))) {
-        uint32_t top = max(max(vs[0] & 0xffffu, vs[0] >> 16), max(vs[1] & 0xffffu, vs[1] >> 16));
+        uint32_t top = max(max(vs[0] & 0x7fffu, vs[0] >> 16 & 0x7fffu), max(vs[1] & 0x7fffu, vs[1] >> 16 & 0x7fffu));
         top = __reduce_max_sync(0xffffffffu, top);
         const int E2 = max(E, (int)(top >> 10) - 15);  // its exponent
         const int E1 = E;
@@ -552,8 +567,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         float acc[4];
         mma16_first(acc, vz[0], vs[0], vz[1], vs[1], ph[n][0], ph[n][1]);
         if constexpr (PS) mma16(acc, vz[0], vs[0], vz[1], vs[1], pl[n][0], pl[n][1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) oz[n][e] += acc[e];
+        add4(oz[n], acc);
       }
       // ---- weighted values
       uint32_t vw[2 * nb];
@@ -577,18 +591,19 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t w0 = vw[b2] >> (8 * hh), w1 = vw[nb + b2] >> (8 * hh);
           uint32_t a0, a1, a2, a3;
-          // c - 8 here and 0.5 sum(p d) at the end.  Codes as they are, with -7.5 sum(p d), cost 3% less for fp16, but
-          // where the probabilities are even the two sums cancel: over 131072 tokens at D = 256 the error was then 2.5
-          // times the fp16 output's own rounding, and 1.01 times with c - 8.  2 c - 15, which needs no sum(p d), takes
-          // a shift more a word: 64 bf16 sequences 82 us.
-          centred(w0, w1, a0, a2, a1, a3);
+          // c - 8 for even tokens and c - 7 for odd ones here, and at the end half of sum(p d) over the even less that
+          // over the odd: neither sum drifts off with the tokens.  (c - 8 for all leaves a sum of half a step a token,
+          // whose rounding is what remains where values cancel: fp32, 131072 tokens and even probabilities, 8.7e-6 off
+          // after 1700 tiles of a warp, 6.2e-7 so.)  Codes as they are, with -7.5 sum(p d), cost 3% less for
+          // fp16, but put the output 2.5 of its own roundings off there.  2 c - 15, which needs no sum(p d), takes a
+          // shift more a word: 64 bf16 sequences 82 us.
+          centred<7>(w0, w1, a0, a2, a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float acc[4];
             mma16_first(acc, a0, a1, a2, a3, bh[n][0], bh[n][1]);
             if constexpr (PS) mma16(acc, a0, a1, a2, a3, bl[n][0], bl[n][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][2 * b2 + hh][e] += acc[e];
+            add4(o[n][2 * b2 + hh], acc);
           }
         }
       }
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 
     // ---- the warp's result, in its ring: [row][D], in units of 2^(ref)
     float* res = reinterpret_cast<float*>(sm.ring[warp]);
-    // low nibbles entered as c - 8, high ones as 16 (c - 8)
+    // low nibbles entered as c - 8 or c - 7, high ones as 16 times that
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll

@@ -163,6 +163,18 @@ def test_long_sums_that_cancel(dtype):
     assert max(np.linalg.norm(row - want[0]) for row in shared_rows(bt, q, 64)) <= 1.25 * rounding
 
 
+@pytest.mark.parametrize("D,group", [(64, 4), (128, 4), (256, 12)])
+def test_long_sums_that_cancel_carry_no_offset(D, group):
+    """The same in fp32, several hundred tiles a warp.  Sums that stay as small as their result: its 2-norm is off by
+    2^-22 for each of p, p d, the sums within tiles and sum(p), and by sqrt(1000) 2^-25 for the additions: below 2^-19."""
+    bt = _kv4.Batch(D, 1, 256, [65536], [1], seed=50)
+    bt.fill_random()
+    q = torch.from_numpy(bt.rng.normal(size=(1, group, D)) * 0.05).float()
+    want = _kv4.attention(bt, q.double().numpy(), D ** -0.5)[0]
+    off = max(np.linalg.norm(row - want[0]) for row in shared_rows(bt, q, 256)) / np.linalg.norm(want)
+    assert off <= 2.0 ** -19, f"{off:.2e}"
+
+
 @pytest.mark.parametrize("n,longest", [(33, 90), (300, 2), (1100, 60), (1100, 3)])
 @pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 128), ("f16", 256)])
 def test_append_and_read_of_many_sequences(n, longest, dtype, D):
