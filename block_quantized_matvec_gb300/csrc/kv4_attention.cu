@@ -40,14 +40,14 @@
 //
 // What bounds it, measured on GB300 (6768 GB/s copied):
 //  - one row tile, D = 128 (64 bf16 sequences of 128 .. 8192 tokens, 32 / 8
-//    heads, 337 MB): 77 us, 4.4 TB/s.  The instructions: 61% of the issue slots,
-//    43% of the ALU pipe (masking codes out of words), tensor pipe 22%.
+//    heads, 337 MB): 77 us, 4.4 TB/s.  The instructions: 59% of the issue slots,
+//    44% of the ALU pipe (masking codes out of words), tensor pipe 22%.
 //    Three CTAs of 4 warps an SM at 168 registers: 77 us; four at 128: 81; one of
 //    12 at 168, which begins and ends its items alone: 114.
 //  - two row tiles, D = 256: the latency of 8 warps an SM at 255 registers (128 of
 //    them accumulators).  131071 fp32 tokens, 24 / 2 heads, 84 MB: 55 us, of which
-//    about 31 tiles and 10 joining 76 parts a head; tensor pipe 32%, issue 38%.
-//    8 x 8 query tokens over 16389, bf16: 146 us, tensor pipe 33%, issue 51%.
+//    about 31 tiles and 10 joining 76 parts a head; tensor pipe 32%, issue 35%.
+//    8 x 8 query tokens over 16389, bf16: 147 us, tensor pipe 33%, issue 47%.
 //    Without the additions (52 and 144 us), splitting the values between two warps
 //    (175 for the latter), 32 rows a warp (159) and two CTAs of 4 warps (142; but 59
 //    instead of 52 for the former) were no better.
