@@ -7,6 +7,7 @@
 #include "ffn_args.cuh"
 #include "kv4.cuh"
 #include "kv4_attention.cuh"
+#include "layer.cuh"
 
 namespace mmvq {
 int launch_quantize_q8_1(const float* x, int K, int ncols, int64_t ldx, void* xq, cudaStream_t s);
@@ -72,7 +73,7 @@ const char* mmvq_strerror(int code) {
     case MMVQ_ERR_SCRATCH:
       return "the layer's intermediates exceed the fixed scratch of mmvq_expert_ffn_noalloc "
              "(MMVQ_NOALLOC_SCRATCH_BYTES)";
-    case MMVQ_ERR_VALUE: return "a non-finite key or value was clamped as it was written";
+    case MMVQ_ERR_VALUE: return "a non-finite input was clamped or left out";
   }
   return "unknown mmvq status";
 }
@@ -532,6 +533,160 @@ int mmvq_kv4_attention(int dtype, const void* q, int64_t ldq, int64_t hq, int n_
 int mmvq_read_device_fault(int* fault, mmvq_stream_t stream) {
   if (!fault) return MMVQ_ERR_NULL;
   return mmvq::read_device_fault(fault, (cudaStream_t)stream);
+}
+
+// ------------------------------------- the layer's steps between the products
+
+int mmvq_norm_rope(int dtype, const void* q, int64_t ldq, int64_t hq, int n_heads, const void* k,
+                   int64_t ldk, int64_t hk, int n_kv_heads, int head_dim, int n_tokens,
+                   const int32_t* positions, int64_t ld_positions, int n_axes,
+                   const int64_t* table, int rot_dim, const float* q_weight,
+                   const float* k_weight, float eps, unsigned int flags, void* yq, int64_t ldyq,
+                   int64_t hyq, void* yk, int64_t ldyk, int64_t hyk, int32_t* status,
+                   mmvq_stream_t stream) {
+  const int size = kv4_dtype_bytes(dtype);
+  if (!size) return MMVQ_ERR_TYPE;
+  if (!kv4_dim(head_dim) || n_tokens < 0 || n_heads < 1 || n_heads > 1024 || n_kv_heads < 0 ||
+      n_kv_heads > 1024 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 || n_axes < 1 ||
+      n_axes > mmvq::kRopeMaxAxes || ld_positions < 0)
+    return MMVQ_ERR_SHAPE;
+  if (ldq < 0 || hq < 0 || ldk < 0 || hk < 0 || ldyq < 0 || hyq < 0 || ldyk < 0 || hyk < 0)
+    return MMVQ_ERR_SHAPE;
+  if ((int64_t)n_tokens * (n_heads + n_kv_heads) >= (int64_t)1 << 32) return MMVQ_ERR_SHAPE;
+  if (flags & ~(MMVQ_ROPE_INTERLEAVED | MMVQ_ROPE_NO_NORM)) return MMVQ_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !(eps < INFINITY)) return MMVQ_ERR_SHAPE;
+  if (n_tokens == 0) return MMVQ_OK;
+  if (!q || !yq || !positions || !table || (n_kv_heads > 0 && (!k || !yk))) return MMVQ_ERR_NULL;
+  if (!aligned(q, size) || !aligned(yq, size) || !aligned(k, size) || !aligned(yk, size) ||
+      !aligned(positions, 4) || !aligned(table, 8) || !aligned(q_weight, 4) ||
+      !aligned(k_weight, 4) || !aligned(status, 4))
+    return MMVQ_ERR_ALIGN;
+  mmvq::NormRope a;
+  a.q = {q, ldq, hq, yq, ldyq, hyq, q_weight, n_heads};
+  a.k = {k, ldk, hk, yk, ldyk, hyk, k_weight, n_kv_heads};
+  a.positions = positions;
+  a.ld_positions = ld_positions;
+  a.n_axes = n_axes;
+  a.table = table;
+  a.rot = rot_dim;
+  a.eps = eps;
+  a.norm = !(flags & MMVQ_ROPE_NO_NORM);
+  a.interleaved = flags & MMVQ_ROPE_INTERLEAVED;
+  a.n_tokens = n_tokens;
+  a.status = status;
+  return mmvq::launch_norm_rope(a, dtype, head_dim, (cudaStream_t)stream);
+}
+
+int mmvq_route_topk(int dtype, const void* logits, int64_t ld, int n_tokens, int n_experts, int k,
+                    int scoring, const float* bias, int n_groups, int top_groups,
+                    int renormalize, float scale, int32_t* topk, float* weights, int32_t* status,
+                    mmvq_stream_t stream) {
+  const int size = kv4_dtype_bytes(dtype);
+  if (!size || (scoring != MMVQ_SCORE_SOFTMAX && scoring != MMVQ_SCORE_SIGMOID))
+    return MMVQ_ERR_TYPE;
+  if (n_tokens < 0 || n_experts < 1 || n_experts > mmvq::kRouteMaxExperts || ld < n_experts ||
+      k < 1 || k > mmvq::kRouteMaxTopk || n_groups < 1 || n_groups > mmvq::kRouteMaxGroups ||
+      n_experts % n_groups || top_groups < 1 || top_groups > n_groups ||
+      k > top_groups * (n_experts / n_groups) || !(scale > -INFINITY && scale < INFINITY))
+    return MMVQ_ERR_SHAPE;
+  if (n_tokens == 0) return MMVQ_OK;
+  if (!logits || !topk || !weights) return MMVQ_ERR_NULL;
+  if (!aligned(logits, size) || !aligned(bias, 4) || !aligned(topk, 4) || !aligned(weights, 4) ||
+      !aligned(status, 4))
+    return MMVQ_ERR_ALIGN;
+  mmvq::RouteTopk a;
+  a.logits = logits;
+  a.ld = ld;
+  a.n_tokens = n_tokens;
+  a.n_experts = n_experts;
+  a.k = k;
+  a.sigmoid = scoring == MMVQ_SCORE_SIGMOID;
+  a.renormalize = renormalize != 0;
+  a.bias = bias;
+  a.n_groups = n_groups;
+  a.top_groups = top_groups;
+  a.scale = scale;
+  a.topk = topk;
+  a.weights = weights;
+  a.status = status;
+  return mmvq::launch_route_topk(a, dtype, (cudaStream_t)stream);
+}
+
+int mmvq_combine_experts(int dtype, const float* y, int64_t n_positions, int H,
+                         const int32_t* topk, const float* weights, int n_tokens, int k,
+                         const int32_t* token_offsets, int n_experts, const int32_t* slot_of,
+                         const void* residual, int64_t ldr, const void* shared, int64_t lds,
+                         const float* shared_gate, void* out, int64_t ldo, int32_t* status,
+                         mmvq_stream_t stream) {
+  const int size = kv4_dtype_bytes(dtype);
+  if (!size) return MMVQ_ERR_TYPE;
+  if (n_tokens < 0 || k < 1 || k > mmvq::kCombineMaxTopk || (int64_t)n_tokens * k > 65536 ||
+      n_experts < 1 || n_experts > 4096 || H < 1 || H > (1 << 24) || n_positions < 0 || ldo < H ||
+      (residual && ldr < H) || (shared && lds < H))
+    return MMVQ_ERR_SHAPE;
+  if (n_tokens == 0) return MMVQ_OK;
+  if (!y || !topk || !weights || !token_offsets || !slot_of || !out || (shared_gate && !shared))
+    return MMVQ_ERR_NULL;
+  if (!aligned(y, 4) || !aligned(topk, 4) || !aligned(weights, 4) || !aligned(token_offsets, 4) ||
+      !aligned(slot_of, 4) || !aligned(residual, size) || !aligned(shared, size) ||
+      !aligned(shared_gate, 4) || !aligned(out, size) || !aligned(status, 4))
+    return MMVQ_ERR_ALIGN;
+  mmvq::CombineExperts a;
+  a.y = y;
+  a.n_positions = n_positions;
+  a.H = H;
+  a.topk = topk;
+  a.weights = weights;
+  a.n_tokens = n_tokens;
+  a.k = k;
+  a.offsets = token_offsets;
+  a.n_experts = n_experts;
+  a.slot_of = slot_of;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.shared = shared;
+  a.lds = lds;
+  a.gate = shared_gate;
+  a.out = out;
+  a.ldo = ldo;
+  a.status = status;
+  return mmvq::launch_combine_experts(a, dtype, (cudaStream_t)stream);
+}
+
+int mmvq_token_logprobs(int dtype, const void* logits, int64_t ld, int n_rows, int vocab,
+                        float scale, const int32_t* tokens, int n_tokens, int top, float* lse,
+                        float* entropy, float* logprobs, int32_t* top_ids, float* top_logprobs,
+                        int32_t* status, mmvq_stream_t stream) {
+  const int size = kv4_dtype_bytes(dtype);
+  if (!size) return MMVQ_ERR_TYPE;
+  if (n_rows < 0 || vocab < 1 || vocab > (1 << 24) || ld < vocab || n_tokens < 0 ||
+      n_tokens > 65536 || top < 0 || top > mmvq::kLogprobsMaxTop || !(scale > 0.0f) ||
+      !(scale < INFINITY))
+    return MMVQ_ERR_SHAPE;
+  if (n_rows == 0) return MMVQ_OK;
+  if (!logits || (n_tokens > 0 && (!tokens || !logprobs)) ||
+      (top > 0 && (!top_ids || !top_logprobs)))
+    return MMVQ_ERR_NULL;
+  if (!aligned(logits, size) || !aligned(tokens, 4) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+      !aligned(logprobs, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4) ||
+      !aligned(status, 4))
+    return MMVQ_ERR_ALIGN;
+  mmvq::TokenLogprobs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.rows = n_rows;
+  a.vocab = vocab;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.n_tokens = n_tokens;
+  a.top = top;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.logprobs = logprobs;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.status = status;
+  return mmvq::launch_token_logprobs(a, dtype, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -72,6 +72,15 @@ SIGNATURES = {
     "mmvq_kv4_attention": (_I, [_I, _P, _I64, _I64, _I, ctypes.c_float, _I, _I, _P, _P, _P, _I64,
                                 _I, _I, _I, _P, _I64, _P, _P, _I, _I, _P, _P, _P]),
     "mmvq_kv4_attention_workspace_bytes": (_I64, [_I]),
+    "mmvq_norm_rope": (_I, [_I, _P, _I64, _I64, _I, _P, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I,
+                            _P, _P, ctypes.c_float, ctypes.c_uint, _P, _I64, _I64, _P, _I64, _I64,
+                            _P, _P]),
+    "mmvq_route_topk": (_I, [_I, _P, _I64, _I, _I, _I, _I, _P, _I, _I, _I, ctypes.c_float, _P, _P,
+                             _P, _P]),
+    "mmvq_combine_experts": (_I, [_I, _P, _I64, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64,
+                                  _P, _P, _I64, _P, _P]),
+    "mmvq_token_logprobs": (_I, [_I, _P, _I64, _I, _I, ctypes.c_float, _P, _I, _I, _P, _P, _P, _P,
+                                 _P, _P, _P]),
 }
 
 
@@ -633,3 +642,242 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
                                     out.data_ptr(), _ptr(lse), *where, n, workspace.data_ptr(),
                                     _ptr(status), _stream(stream)), "mmvq_kv4_attention")
     return out if lse is None else (out, lse)
+
+
+# ------------------------------------- the layer's steps between the products
+
+ROPE_INTERLEAVED = 1
+ROPE_NO_NORM = 2
+_SCORING = {"softmax": 0, "sigmoid": 1}  # mmvq_scoring
+
+
+def _on(t: torch.Tensor, stream):
+    """The number of a tensor's device, which has to be the one that the call runs on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev != (torch.cuda.current_device() if stream is None else stream.device_index):
+        raise ValueError("the tensors are on another device than the call's stream")
+    return dev
+
+
+def _plain(t, dtype, shape, dev, name):
+    """A contiguous tensor of this type and shape on the device (None passes): its address."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the call's device")
+    return t.data_ptr()
+
+
+def _layer_status(status, dev):
+    if status is not None and (status.dtype is not torch.int32 or status.get_device() != dev or
+                               status.numel() < 1):
+        raise ValueError("status must be an int32 tensor on the call's device")
+    return _ptr(status)
+
+
+def _rows(t, dtype, shape, dev, name):
+    """A [rows, n] tensor with unit inner stride (None passes): its address and row stride."""
+    if t is None:
+        return None, 0
+    ld, one = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
+            (one != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
+        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} with unit inner stride and rows "
+                         "that do not overlap, on the call's device")
+    return t.data_ptr(), max(ld, shape[1])
+
+
+def _inverse_two_pi(bits: int) -> int:
+    """2^bits / (2 pi), rounded down; pi by Machin's formula in whole numbers."""
+    one = 1 << (bits + 32)
+
+    def arctan_of_inverse(n):
+        term = one // n
+        total, i, sign = term, 1, 1
+        while term:
+            term //= n * n
+            i, sign = i + 2, -sign
+            total += sign * (term // i)
+        return total
+    pi = 4 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))
+    return (one << bits) // (2 * pi)
+
+
+def rope_table(inv_freq, sections=None, axis_of=None, device="cuda") -> torch.Tensor:
+    """The table of norm_rope, int64 [2, rot_dim/2], made once and kept: inv_freq, the angle of
+    each pair per position in radians (numbers or a tensor, taken as 64-bit floats), and the axis
+    whose position turns it: axis_of, a number for each pair, or sections, the pairs of axis 0, 1,
+    ... one after another (neither: axis 0)."""
+    freq = [float(f) for f in (inv_freq.double().tolist() if isinstance(inv_freq, torch.Tensor)
+                               else inv_freq)]
+    if not freq or not all(abs(f) < 2.0 ** 64 for f in freq):
+        raise ValueError("inv_freq must be numbers below 2^64")
+    if sections is not None and axis_of is not None:
+        raise ValueError("sections or axis_of, not both")
+    if sections is not None:
+        axis_of = [a for a, n in enumerate(sections) for _ in range(n)]
+    axis_of = [0] * len(freq) if axis_of is None else [int(a) for a in axis_of]
+    if len(axis_of) != len(freq) or not all(0 <= a < 4 for a in axis_of):
+        raise ValueError("an axis (0-3) for each of inv_freq")
+    bits = 1300  # 64 of the fraction and, for the smallest doubles, their 1074 behind it
+    inv = _inverse_two_pi(bits)
+    steps = []
+    for f in freq:
+        num, den = f.as_integer_ratio()  # den is a power of two
+        step = ((num * inv << 64) // den + (1 << (bits - 1)) >> bits) % (1 << 64)
+        steps.append(step - (1 << 64) if step >= 1 << 63 else step)
+    return torch.tensor([steps, axis_of], dtype=torch.int64, device=device)
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
+              table: torch.Tensor, *, q_weight: torch.Tensor | None = None,
+              k_weight: torch.Tensor | None = None, eps: float | None = 1e-6,
+              interleaved: bool = False, out: tuple | None = None,
+              status: torch.Tensor | None = None, stream=None):
+    """RMS norm of every head of q [n, heads, head_dim] and k [n, kv heads, head_dim] (None:
+    queries alone), times q_weight and k_weight [head_dim] fp32 (None: ones), then the rotation by
+    the token's position -> (q, k), contiguous or written to out (which may be q and k themselves).
+    positions: int32 [n], or [axes, n]; table: rope_table; eps=None leaves the norm out;
+    interleaved pairs neighbours instead of halves.  (mmvq_norm_rope)"""
+    dev = _on(q, stream)
+    n, heads, dim = q.shape
+    dtype, _, _, ldq, hq = _kv4_rows(q, 0, dim, dev, "q")
+    if out is None:
+        yq = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
+        yk = None if k is None else _made(stream, torch.empty_like, k,
+                                          memory_format=torch.contiguous_format)
+    else:
+        yq, yk = out
+        if (k is None) != (yk is None):
+            raise ValueError("out must be (q, k), k None where k is")
+    dtype_y, n_y, _, ldyq, hyq = _kv4_rows(yq, heads, dim, dev, "out[0]")
+    kv = ldk = hk = ldyk = hyk = 0
+    if k is not None:
+        dtype_k, n_k, kv, ldk, hk = _kv4_rows(k, 0, dim, dev, "k")
+        dtype_yk, n_yk, _, ldyk, hyk = _kv4_rows(yk, kv, dim, dev, "out[1]")
+        if dtype_k != dtype or n_k != n or dtype_yk != dtype or n_yk != n:
+            raise ValueError("q, k and out must have the same tokens and type")
+    if dtype_y != dtype or n_y != n:
+        raise ValueError("q, k and out must have the same tokens and type")
+    pos_shape, ld_pos = positions.shape, positions.stride(0)
+    if positions.dtype is not torch.int32 or positions.get_device() != dev or \
+            pos_shape[-1] != n or len(pos_shape) > 2 or (positions.stride(-1) != 1 and n > 1):
+        raise ValueError(f"positions must be an int32 tensor [{n}] or [axes, {n}] with unit inner "
+                         "stride on the call's device")
+    axes, ld_pos = (1, 0) if len(pos_shape) == 1 else (pos_shape[0], ld_pos)
+    half = table.shape[1]
+    if table.dtype is not torch.int64 or table.dim() != 2 or table.shape[0] != 2 or \
+            table.get_device() != dev or not table.is_contiguous():
+        raise ValueError("table must be a rope_table on the call's device")
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_NO_NORM if eps is None else 0)
+    _check(lib().mmvq_norm_rope(dtype, q.data_ptr(), ldq, hq, heads, _ptr(k), ldk, hk, kv, dim, n,
+                                positions.data_ptr(), ld_pos, axes, table.data_ptr(), 2 * half,
+                                _plain(q_weight, torch.float32, (dim,), dev, "q_weight"),
+                                _plain(k_weight, torch.float32, (dim,), dev, "k_weight"),
+                                0.0 if eps is None else eps, flags, yq.data_ptr(), ldyq, hyq,
+                                _ptr(yk), ldyk, hyk, _layer_status(status, dev),
+                                _stream(stream)), "mmvq_norm_rope")
+    return yq, yk
+
+
+def route_topk(logits: torch.Tensor, k: int, *, scoring: str = "softmax",
+               bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int | None = None,
+               renormalize: bool = True, scale: float = 1.0, out: tuple | None = None,
+               status: torch.Tensor | None = None, stream=None):
+    """Router logits [n, experts] -> (topk [n, k] int32, weights [n, k] fp32): the k experts of the
+    largest score (softmax or sigmoid of the logits) + bias [experts] fp32, among the top_groups
+    (all by default) of n_groups runs of experts whose two best add up to most; weights are their
+    scores, renormalised to sum to 1 before scale.  What route_groups, expert_ffn and
+    combine_experts take.  (mmvq_route_topk)"""
+    dev = _on(logits, stream)
+    n, experts = logits.shape
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None or scoring not in _SCORING:
+        raise ValueError("logits must be float32, float16 or bfloat16, scoring softmax or sigmoid")
+    address, ld = _rows(logits, logits.dtype, (n, experts), dev, "logits")
+    if out is None:
+        out = (_made(stream, torch.empty, (n, k), dtype=torch.int32, device=logits.device),
+               _made(stream, torch.empty, (n, k), dtype=torch.float32, device=logits.device))
+    topk, weights = out
+    _check(lib().mmvq_route_topk(dtype, address, ld, n, experts, k, _SCORING[scoring],
+                                 _plain(bias, torch.float32, (experts,), dev, "bias"), n_groups,
+                                 n_groups if top_groups is None else top_groups,
+                                 1 if renormalize else 0, scale,
+                                 _plain(topk, torch.int32, (n, k), dev, "out[0]"),
+                                 _plain(weights, torch.float32, (n, k), dev, "out[1]"),
+                                 _layer_status(status, dev), _stream(stream)), "mmvq_route_topk")
+    return topk, weights
+
+
+def combine_experts(y: torch.Tensor, topk: torch.Tensor, weights: torch.Tensor,
+                    offsets: torch.Tensor, slot_of: torch.Tensor, *,
+                    residual: torch.Tensor | None = None, shared: torch.Tensor | None = None,
+                    shared_gate: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+                    out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """out [n, H] = residual + sigmoid(shared_gate) * shared + the experts' rows y [positions, H]
+    fp32 times weights [n, k], where offsets and slot_of are the lists of topk [n, k] (route_groups,
+    expert_ffn).  residual and shared [n, H] (either may be missing) have out's type: dtype, theirs,
+    or float32.  shared_gate: fp32 [n], None for a weight of 1.  (mmvq_combine_experts)"""
+    dev = _on(y, stream)
+    n, k = topk.shape
+    positions, H = y.shape
+    if dtype is None:
+        dtype = next((t.dtype for t in (out, residual, shared) if t is not None), torch.float32)
+    number = _DTYPES.get(dtype)
+    if number is None:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    if out is None:
+        out = _made(stream, torch.empty, (n, H), dtype=dtype, device=y.device)
+    residual_at, ldr = _rows(residual, dtype, (n, H), dev, "residual")
+    shared_at, lds = _rows(shared, dtype, (n, H), dev, "shared")
+    out_at, ldo = _rows(out, dtype, (n, H), dev, "out")
+    i32, f32, experts = torch.int32, torch.float32, offsets.numel() - 1
+    if slot_of.numel() < n * k:
+        raise ValueError(f"slot_of must hold {n * k} slots")
+    _check(lib().mmvq_combine_experts(number, _plain(y, f32, (positions, H), dev, "y"), positions,
+                                      H, _plain(topk, i32, (n, k), dev, "topk"),
+                                      _plain(weights, f32, (n, k), dev, "weights"), n, k,
+                                      _plain(offsets, i32, (experts + 1,), dev, "offsets"), experts,
+                                      _plain(slot_of, i32, slot_of.shape, dev, "slot_of"),
+                                      residual_at, ldr, shared_at, lds,
+                                      _plain(shared_gate, f32, (n,), dev, "shared_gate"), out_at,
+                                      ldo, _layer_status(status, dev), _stream(stream)),
+           "mmvq_combine_experts")
+    return out
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, *, top: int = 0,
+                   scale: float = 1.0, out: dict | None = None,
+                   status: torch.Tensor | None = None, stream=None) -> dict:
+    """Of the softmax of scale * logits [n, vocab]: a dict of lse [n], entropy [n], logprobs [n, m]
+    of the given tokens [n, m] int32, and the `top` likeliest tokens, top_ids [n, top] int32 and
+    top_logprobs [n, top].  out: such a dict to write to; lse and entropy may be missing in it.
+    (mmvq_token_logprobs)"""
+    dev = _on(logits, stream)
+    n, vocab = logits.shape
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
+        raise ValueError("logits must be float32, float16 or bfloat16")
+    address, ld = _rows(logits, logits.dtype, (n, vocab), dev, "logits")
+    m = 0 if tokens is None else tokens.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    if out is None:
+        make = lambda shape, kind: _made(stream, torch.empty, shape, dtype=kind,  # noqa: E731
+                                         device=logits.device)
+        out = dict(lse=make((n,), f32), entropy=make((n,), f32), logprobs=make((n, m), f32),
+                   top_ids=make((n, top), i32), top_logprobs=make((n, top), f32))
+    get = out.get
+    _check(lib().mmvq_token_logprobs(dtype, address, ld, n, vocab, scale,
+                                     _plain(tokens, i32, (n, m), dev, "tokens"), m, top,
+                                     _plain(get("lse"), f32, (n,), dev, "lse"),
+                                     _plain(get("entropy"), f32, (n,), dev, "entropy"),
+                                     _plain(get("logprobs"), f32, (n, m), dev, "logprobs"),
+                                     _plain(get("top_ids"), i32, (n, top), dev, "top_ids"),
+                                     _plain(get("top_logprobs"), f32, (n, top), dev,
+                                            "top_logprobs"),
+                                     _layer_status(status, dev), _stream(stream)),
+           "mmvq_token_logprobs")
+    return out

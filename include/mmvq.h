@@ -129,11 +129,21 @@ enum mmvq_status {
   MMVQ_ERR_ROUTING = -6, /* routing lists rejected (host-side limits) */
   MMVQ_ERR_CUDA = -7,    /* a CUDA launch or attribute call failed */
   MMVQ_ERR_SCRATCH = -8, /* mmvq_expert_ffn_noalloc: intermediates exceed its fixed scratch */
-  MMVQ_ERR_VALUE = -9    /* mmvq_kv4_append (*status): a non-finite input was clamped */
+  MMVQ_ERR_VALUE = -9    /* *status: a non-finite input was clamped (mmvq_kv4_append) or left out */
 };
 
-/* Element types of the plain tensors of the key/value cache calls (GGUF's numbers). */
+/* Element types of the plain tensors of the key/value cache calls and of the layer's steps (GGUF's
+ * numbers). */
 enum mmvq_dtype { MMVQ_F32 = 0, MMVQ_F16 = 1, MMVQ_BF16 = 30 };
+
+/* Flags of mmvq_norm_rope. */
+enum mmvq_rope_flags {
+  MMVQ_ROPE_INTERLEAVED = 1, /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
+  MMVQ_ROPE_NO_NORM = 2      /* rotation alone */
+};
+
+/* Scores of mmvq_route_topk. */
+enum mmvq_scoring { MMVQ_SCORE_SOFTMAX = 0, MMVQ_SCORE_SIGMOID = 1 };
 
 /* Version of this ABI (major*10000 + minor*100 + patch).  Entry points and status codes that are
  * only added leave it as it is; a caller that can do without one looks it up by name. */
@@ -505,6 +515,105 @@ MMVQ_API int mmvq_kv4_attention(int dtype, const void* q, int64_t ldq, int64_t h
 /* Bytes of the workspace of mmvq_kv4_attention, whatever the batch; -1 on a
  * bad head_dim.  Host-only. */
 MMVQ_API int64_t mmvq_kv4_attention_workspace_bytes(int head_dim);
+
+/*
+ * The layer's steps between its products (no counterpart on the pages, whose
+ * engine has them in other files).  dtype: mmvq_dtype of q, k, logits, the
+ * residual and shared rows and what is written in their place (else
+ * MMVQ_ERR_TYPE), each aligned to its element; everything is computed in fp32
+ * and rounded once.  status (may be NULL) is written only where something is
+ * wrong.  n_tokens (n_rows) = 0: nothing happens.
+ */
+
+/*
+ * RMS norm of every query and key head, then the rotation by the token's
+ * position.  q [n_tokens][n_heads][head_dim] and k [n_tokens][n_kv_heads]
+ * [head_dim], ldq/ldk elements from token to token and hq/hk from head to head
+ * (>= 0, the values of a head side by side); yq, yk the same with their own
+ * strides, and may be q and k themselves (same strides; no other overlap).
+ * n_kv_heads = 0: queries alone.  z = x / sqrt(mean(x^2) + eps) * weight over
+ * the head's values (q_weight, k_weight: fp32 [head_dim], NULL for ones;
+ * MMVQ_ROPE_NO_NORM: z = x).  Of the first rot_dim values of z, pair i, (i, i +
+ * rot_dim/2) or (2i, 2i+1) with MMVQ_ROPE_INTERLEAVED, turns by the angle
+ * positions[axis * ld_positions + token] * f_i; the others stay.  table: int64
+ * [2][rot_dim/2], 8-byte aligned, kept by the caller: first the step of each
+ * pair, f_i / (2 pi) of a turn as a 64-bit fraction (times 2^64, modulo 2^64),
+ * then its axis.  Positions are any int32; an angle is within 2^-32 turns of
+ * the exact one.  An axis outside [0, n_axes) leaves its pairs as they are and
+ * sets *status to MMVQ_ERR_SHAPE.
+ * Limits: head_dim 64, 128 or 256; rot_dim even, 2..head_dim; 1..1024 query
+ * heads, 0..1024 key heads, fewer than 2^32 rows in all; 1..4 axes; 0 <= eps < inf.
+ */
+MMVQ_API int mmvq_norm_rope(int dtype, const void* q, int64_t ldq, int64_t hq, int n_heads,
+                            const void* k, int64_t ldk, int64_t hk, int n_kv_heads, int head_dim,
+                            int n_tokens, const int32_t* positions, int64_t ld_positions,
+                            int n_axes, const int64_t* table, int rot_dim, const float* q_weight,
+                            const float* k_weight, float eps, unsigned int flags, void* yq,
+                            int64_t ldyq, int64_t hyq, void* yk, int64_t ldyk, int64_t hyk,
+                            int32_t* status, mmvq_stream_t stream);
+
+/*
+ * Experts of each token and their weights, as mmvq_route_groups,
+ * mmvq_expert_ffn and mmvq_combine_experts take them.  logits [n_tokens][ld],
+ * ld >= n_experts.  The score of an expert is the softmax or the sigmoid of its
+ * logit, its value score + bias (fp32 [n_experts], NULL for zeros).  The experts
+ * form n_groups runs of equal length; the top_groups of them whose two largest
+ * values add up to most stay (all where top_groups = n_groups).  topk [n_tokens]
+ * [k]: the experts of the largest values among them, in falling order, of equal
+ * ones the lower id (of groups too).  The order is that of the values in 64
+ * bits; without bias and with all groups, that of the logits.  weights
+ * [n_tokens][k]: the scores (without bias), with renormalize over their sum,
+ * times scale.
+ * Logits that are not finite are never chosen (NaN and +inf set *status to
+ * MMVQ_ERR_VALUE), nor are experts with a bias of NaN or -inf; where fewer than
+ * k can be, the last entries are -1 with weight 0.  (The routing calls leave
+ * out such slots and set their own status to MMVQ_ERR_ROUTING.)
+ * Limits: n_experts up to 1024, a multiple of n_groups; k up to 32 and to the
+ * experts of top_groups groups; up to 32 groups; scale finite.
+ */
+MMVQ_API int mmvq_route_topk(int dtype, const void* logits, int64_t ld, int n_tokens,
+                             int n_experts, int k, int scoring, const float* bias, int n_groups,
+                             int top_groups, int renormalize, float scale, int32_t* topk,
+                             float* weights, int32_t* status, mmvq_stream_t stream);
+
+/*
+ * The experts' rows back at their tokens: out[t] = residual[t] + g * shared[t] +
+ * sum over j of weights[t][j] * y[p(t,j)], with g = sigmoid(shared_gate[t]) (1
+ * where shared_gate is NULL), in fp32, j in rising order.  y: fp32
+ * [n_positions][H], as mmvq_expert_ffn and mmvq_grouped write it; p(t,j) is the
+ * position of slot t*k + j in the lists of the same topk (token_offsets
+ * [n_experts+1], slot_of, from mmvq_route_groups or mmvq_expert_ffn).  residual,
+ * shared and out are of dtype, ldr/lds/ldo >= H elements from row to row;
+ * residual and shared may be NULL, and out may be either of them.  Slots with
+ * expert -1 add nothing; other ids outside [0, n_experts), and slots that the
+ * lists do not hold, add nothing and set *status to MMVQ_ERR_ROUTING.
+ * Limits: n_tokens*k <= 65536, k <= 256, n_experts <= 4096, H <= 2^24.
+ */
+MMVQ_API int mmvq_combine_experts(int dtype, const float* y, int64_t n_positions, int H,
+                                  const int32_t* topk, const float* weights, int n_tokens, int k,
+                                  const int32_t* token_offsets, int n_experts,
+                                  const int32_t* slot_of, const void* residual, int64_t ldr,
+                                  const void* shared, int64_t lds, const float* shared_gate,
+                                  void* out, int64_t ldo, int32_t* status, mmvq_stream_t stream);
+
+/*
+ * What a row of logits says: of the softmax p of scale * logits[row] (vocab
+ * values, ld >= vocab elements from row to row) lse = log sum exp, entropy =
+ * -sum p log p, logprobs [n_rows][n_tokens] = log p of the given tokens (int32
+ * [n_rows][n_tokens]), top_ids and top_logprobs [n_rows][top]: the likeliest
+ * tokens in falling order, of equal ones the lower id.  lse and entropy
+ * [n_rows] may be NULL; with n_tokens or top 0 so may their arrays.
+ * A logit of -inf has no probability: log p = -inf, and it is no alternative
+ * (entries past the last one: id -1, -inf).  A row of nothing else: lse and
+ * logprobs -inf, entropy 0, no alternatives.  A row with NaN or +inf: NaN, ids
+ * -1, and *status is set to MMVQ_ERR_VALUE.  A token outside [0, vocab) has
+ * logprob NaN and sets *status to MMVQ_ERR_ROUTING.
+ * Limits: vocab <= 2^24, n_tokens <= 65536, top <= 32, 0 < scale < inf.
+ */
+MMVQ_API int mmvq_token_logprobs(int dtype, const void* logits, int64_t ld, int n_rows, int vocab,
+                                 float scale, const int32_t* tokens, int n_tokens, int top,
+                                 float* lse, float* entropy, float* logprobs, int32_t* top_ids,
+                                 float* top_logprobs, int32_t* status, mmvq_stream_t stream);
 
 /* Bytes of the planar form of a rows x K matrix of `type` (MMVQ_Q6_K,
  * MMVQ_Q5_K or MMVQ_Q4_K); -1 on a bad type or shape. */
