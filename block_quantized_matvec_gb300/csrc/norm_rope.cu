@@ -6,8 +6,15 @@
 // the table's step wraps as the angle does, so a position of 2^31 loses 2^-34
 // turns, and sin and cos are taken of a remainder within an eighth of a turn.
 //
-// A warp per row; a lane holds pairs lane, lane + 32, ..., those past rot / 2
-// made of neighbours that do not turn.
+// Rows are read and written once and little is computed, so memory bounds the
+// kernel where there are many.  norm_rope_vec_kernel: a lane holds two 16-byte
+// vectors of a row, those whose values turn with one another (i and i + rot/2:
+// the vectors rot/2 apart; 2i and 2i + 1: neighbours), so that D / (2 * 16 bytes)
+// lanes share a row and only the mean square crosses lanes.  A warp stays with a
+// token: its lanes share out the sines and cosines, then every lane keeps the
+// weights times those of its own pairs for all heads, four numbers a pair.
+// Halves that are no multiple of a vector and rows off 16 bytes take
+// norm_rope_any_kernel: a warp per row, two values at a time.
 #include "layer.cuh"
 #include "typed.cuh"
 
@@ -23,8 +30,18 @@ __device__ __forceinline__ float2 turn(uint64_t phase) {
   return quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
+// cos and sin of pair i's angle at token t; no angle where its axis is none.
+__device__ __forceinline__ float2 pair_turn(const NormRope& a, int i, int64_t t) {
+  const int64_t axis = a.table[a.rot / 2 + i];
+  if (axis < 0 || axis >= a.n_axes) {
+    if (a.status) *a.status = MMVQ_ERR_SHAPE;
+    return make_float2(1.0f, 0.0f);
+  }
+  return turn((uint64_t)a.table[i] * (uint64_t)(int64_t)a.positions[axis * a.ld_positions + t]);
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) norm_rope_kernel(const NormRope a) {
+__global__ void __launch_bounds__(128) norm_rope_any_kernel(const NormRope a) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kPairs = D / 64;
@@ -63,29 +80,150 @@ __global__ void __launch_bounds__(128) norm_rope_kernel(const NormRope a) {
   for (int j = 0; j < kPairs; ++j) {
     const int i = lane + 32 * j;
     if (i < half) {
-      const int64_t axis = a.table[half + i];
-      if (axis >= 0 && axis < a.n_axes) {
-        const int64_t pos = a.positions[axis * a.ld_positions + t];
-        const float2 w = turn((uint64_t)a.table[i] * (uint64_t)pos);
-        const float p = v[j][0] * w.x - v[j][1] * w.y, q = v[j][0] * w.y + v[j][1] * w.x;
-        v[j][0] = p;
-        v[j][1] = q;
-      } else if (a.status) {
-        *a.status = MMVQ_ERR_SHAPE;
-      }
+      const float2 w = pair_turn(a, i, t);
+      const float p = v[j][0] * w.x - v[j][1] * w.y, q = v[j][0] * w.y + v[j][1] * w.x;
+      v[j][0] = p;
+      v[j][1] = q;
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) y[at[j][e]] = from_f32<T>(v[j][e]);
   }
 }
 
+constexpr int kRopeWarps = 8;
+constexpr int kRopeWarpsWanted = 152 * 24;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_vec_kernel(const NormRope a, int splits) {
+  constexpr int V = kVec<T>, kLanes = D / (2 * V), kRows = 32 / kLanes;  // lanes of a row, rows of a warp
+  __shared__ float2 turns[kRopeWarps][D / 2];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t unit = blockIdx.x * kRopeWarps + warp;
+  const uint32_t t32 = unit / splits;
+  if (t32 >= (uint32_t)a.n_tokens) return;
+  const int64_t t = t32;
+  // the token's rows, kRows at a time: queries, then keys; this warp's share of those steps
+  const int q_steps = (a.q.heads + kRows - 1) / kRows, steps = q_steps + (a.k.heads + kRows - 1) / kRows;
+  const int part = unit - t32 * splits;
+  const int lo = (int)((int64_t)steps * part / splits), hi = (int)((int64_t)steps * (part + 1) / splits);
+
+  const int u = lane % kLanes, mine = lane / kLanes, half = a.rot / 2;
+  const int turning = half / V;  // vectors of a half
+  const bool halves = u < turning && !a.interleaved;
+  const int v0 = V * (halves ? u : 2 * u), v1 = halves ? v0 + half : v0 + V;
+  for (int i = lane; i < half; i += 32) turns[warp][i] = pair_turn(a, i, t);
+  __syncwarp();
+
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const RopeHeads& r = kind ? a.k : a.q;
+    const int base = kind ? q_steps : 0;
+    const int begin = max(lo, base) - base, end = min(hi, kind ? steps : q_steps) - base;
+    if (begin >= end) continue;
+    const T* x = static_cast<const T*>(r.x) + t * r.ldx;
+    T* y = static_cast<T*>(r.y) + t * r.ldy;
+    auto load = [&](int step, uint4& p, uint4& q) {
+      const int h = step * kRows + mine;
+      if (h < r.heads) {
+        p = *reinterpret_cast<const uint4*>(x + h * r.hx + v0);
+        q = *reinterpret_cast<const uint4*>(x + h * r.hx + v1);
+      }
+    };
+    uint4 p = make_uint4(0u, 0u, 0u, 0u), q = p;
+    load(begin, p, q);
+    // weights of values i of v0 and v1, and with them the turn of their pair
+    float aa[V], ab[V], ba[V], bb[V];  // out0 = x0 * aa - x1 * ab, out1 = x0 * ba + x1 * bb
+    {
+      float w[2 * V];
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) w[i] = 1.0f;
+      if (a.norm && r.weight) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(r.weight + v0 + i), g = *reinterpret_cast<const float4*>(r.weight + v1 + i);
+          w[i] = f.x, w[i + 1] = f.y, w[i + 2] = f.z, w[i + 3] = f.w;
+          w[V + i] = g.x, w[V + i + 1] = g.y, w[V + i + 2] = g.z, w[V + i + 3] = g.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 c = u * V + i < half ? turns[warp][u * V + i] : make_float2(1.0f, 0.0f);
+        const float w0 = a.interleaved ? w[2 * i] : w[i], w1 = a.interleaved ? w[2 * i + 1] : w[V + i];
+        aa[i] = w0 * c.x;
+        ab[i] = w1 * c.y;
+        ba[i] = w0 * c.y;
+        bb[i] = w1 * c.x;
+      }
+    }
+#pragma unroll 1
+    for (int step = begin; step < end; ++step) {
+      float v[2 * V];
+      unpack16<T>(p, v);
+      unpack16<T>(q, v + V);
+      if (step + 1 < end) load(step + 1, p, q);
+      float scale = 1.0f;
+      if (a.norm) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) sum = fmaf(v[i], v[i], sum);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        scale = rsqrtf(sum * (1.0f / D) + a.eps);
+      }
+      float out[2 * V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float x0 = (a.interleaved ? v[2 * i] : v[i]) * scale, x1 = (a.interleaved ? v[2 * i + 1] : v[V + i]) * scale;
+        const float o0 = x0 * aa[i] - x1 * ab[i], o1 = x0 * ba[i] + x1 * bb[i];
+        v[i] = o0;
+        out[i] = o1;
+      }
+      // back in the vectors' order
+      float f[2 * V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (a.interleaved) {
+          f[2 * i] = v[i];
+          f[2 * i + 1] = out[i];
+        } else {
+          f[i] = v[i];
+          f[V + i] = out[i];
+        }
+      }
+      const int h = step * kRows + mine;
+      if (h < r.heads) {
+        *reinterpret_cast<uint4*>(y + h * r.hy + v0) = pack16<T>(f);
+        *reinterpret_cast<uint4*>(y + h * r.hy + v1) = pack16<T>(f + V);
+      }
+    }
+  }
+}
+
+// Whether 16-byte accesses reach every vector of these heads.
+static bool rope_vectors(const RopeHeads& r, int size) {
+  const int V = 16 / size;
+  return reinterpret_cast<uintptr_t>(r.x) % 16 == 0 && reinterpret_cast<uintptr_t>(r.y) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(r.weight) % 16 == 0 && r.ldx % V == 0 && r.hx % V == 0 && r.ldy % V == 0 && r.hy % V == 0;
+}
+
 int launch_norm_rope(const NormRope& a, int dtype, int head_dim, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.n_tokens * (a.q.heads + a.k.heads);
-  const dim3 grid((unsigned)((rows + 3) / 4));
   return with_dtype(dtype, [&](auto v) {
     using T = decltype(v);
-    auto kern = head_dim == 64 ? norm_rope_kernel<T, 64> : head_dim == 128 ? norm_rope_kernel<T, 128> : norm_rope_kernel<T, 256>;
-    return launch_pdl(kern, grid, dim3(128), 0, stream, a);
+    const int size = (int)sizeof(T), V = kVec<T>;
+    if (rope_vectors(a.q, size) && (!a.k.heads || rope_vectors(a.k, size)) && (a.interleaved || a.rot / 2 % V == 0)) {
+      // Few tokens: a token's heads are shared out to as many warps as fill the GPU, up to one step each.
+      const int rows = 64 * V / head_dim;
+      const int steps = (a.q.heads + rows - 1) / rows + (a.k.heads + rows - 1) / rows;
+      const int splits = (int)min((int64_t)steps, max((int64_t)1, (int64_t)kRopeWarpsWanted / a.n_tokens));
+      const int64_t units = (int64_t)a.n_tokens * splits;
+      auto kern = head_dim == 64 ? norm_rope_vec_kernel<T, 64> : head_dim == 128 ? norm_rope_vec_kernel<T, 128> : norm_rope_vec_kernel<T, 256>;
+      return launch_pdl(kern, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)), dim3(32 * kRopeWarps), 0, stream, a, splits);
+    }
+    const int64_t rows = (int64_t)a.n_tokens * (a.q.heads + a.k.heads);
+    auto kern = head_dim == 64 ? norm_rope_any_kernel<T, 64> : head_dim == 128 ? norm_rope_any_kernel<T, 128> : norm_rope_any_kernel<T, 256>;
+    return launch_pdl(kern, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);
   });
 }
 
