@@ -660,8 +660,8 @@ int mmvq_token_logprobs(int dtype, const void* logits, int64_t ld, int n_rows, i
   const int size = kv4_dtype_bytes(dtype);
   if (!size) return MMVQ_ERR_TYPE;
   if (n_rows < 0 || vocab < 1 || vocab > (1 << 24) || ld < vocab || n_tokens < 0 ||
-      n_tokens > 65536 || top < 0 || top > mmvq::kLogprobsMaxTop || !(scale > 0.0f) ||
-      !(scale < INFINITY))
+      n_tokens > 65536 || top < 0 || top > mmvq::kLogprobsMaxTop || !(scale >= 0x1p-64f) ||
+      !(scale < 0x1p64f))
     return MMVQ_ERR_SHAPE;
   if (n_rows == 0) return MMVQ_OK;
   if (!logits || (n_tokens > 0 && (!tokens || !logprobs)) ||

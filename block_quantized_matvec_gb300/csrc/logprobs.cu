@@ -6,115 +6,535 @@
 // every difference is of terms of one sign, so that a row that is all but
 // certain keeps its digits.
 //
-// A CTA per row: the maximum, the sums, then one pass for each alternative.
+// One pass.  Each warp keeps its best `live` logits (those asked for, at least
+// eight) in order, one a lane, and the sums over all others, of 2^y and 2^y y with
+// y = (x - C) log2(e) - R: R is near the list's last, so that terms are summed at
+// their own size also where the first stands far above, and C is 0 but where
+// x log2(e) would leave fp32's range.  A logit that enters the list is taken out
+// of the sums, one that leaves it is added to them, also where lists are merged at
+// the end; what remains besides the sums is the list, whose first is m.
+//
+// What it spends: about 44 instructions for 8 logits of 16 bits (a maximum in
+// pairs, conversions, two packed fp32 operations and an ex2 each).  Lists are
+// entered rarely: from its first vectors, and again from three times as many, each
+// CTA finds a bound that `live` values reach, by halving the span of its threads'
+// largest ones, and a warp looks closer only where the largest of a batch reaches
+// the bound or its list's last; the code for that is kept small, since 16 warps
+// that wait for instructions cost more than the ones they run.
+//
+// A row is shared out to the CTAs of a cluster where rows are few; the first one
+// reads the others' lists and sums from their shared memory.
+#include <cooperative_groups.h>
+
 #include "layer.cuh"
 #include "typed.cuh"
 
 namespace mmvq {
 
-constexpr int kRowThreads = 512;
+namespace cg = cooperative_groups;
 
-// The larger value, of equal ones the lower place.
-struct Best {
-  float v;
-  int i;
-};
-__device__ __forceinline__ Best better(Best a, Best b) {
-  return b.v > a.v || (b.v == a.v && b.i < a.i) ? b : a;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// How far above R the list's last may stand, in powers of two, before R follows:
+// the entropy's sum cancels by that much at most.
+constexpr float kSlack = 3.0f;
+constexpr float kFar = 0x1p100f;  // |x log2(e)| from which on C is taken off first
+constexpr int kUnroll = 4;   // 16-byte loads of a thread in flight: a batch
+constexpr int kLeast = 8;    // a list's entries, however few are asked for
+constexpr int kAgain = 2;    // the batch at which the bound is found again
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-__device__ __forceinline__ Best warp_best(Best b) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    b = better(b, Best{__shfl_xor_sync(0xffffffffu, b.v, o), __shfl_xor_sync(0xffffffffu, b.i, o)});
-  return b;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};"
+      " fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};"
+      " add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Four 32-bit words of -inf of the type.
+template <typename T>
+__device__ __forceinline__ uint4 minus_infinity() {
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+  return make_uint4(w, w, w, w);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) logprobs_kernel(const TokenLogprobs a) {
-  __shared__ Best part[kRowThreads / 32];
-  __shared__ float sums[2][kRowThreads / 32];
+using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+
+// The largest of the values of n vectors, NaN where one is.
+template <typename T, int n>
+__device__ __forceinline__ float vectors_max(const uint4* r) {
+  if constexpr (sizeof(T) == 4) {
+    float m = __uint_as_float(r[0].x);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      m = max_nan(m, max_nan(__uint_as_float(r[i].x), __uint_as_float(r[i].y)));
+      m = max_nan(m, max_nan(__uint_as_float(r[i].z), __uint_as_float(r[i].w)));
+    }
+    return m;
+  } else {
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const Pair<T>*>(&w); };
+    Pair<T> m = pair(r[0].x);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      m = __hmax2_nan(m, __hmax2_nan(pair(r[i].x), pair(r[i].y)));
+      m = __hmax2_nan(m, __hmax2_nan(pair(r[i].z), pair(r[i].w)));
+    }
+    return max_nan(to_f32(m.x), to_f32(m.y));
+  }
+}
+
+// Value i of a vector; i differs from lane to lane.
+template <typename T>
+__device__ __forceinline__ float vector_value(const uint4& r, int i) {
+  constexpr int kPer = kVec<T> / 4;
+  const int w = i / kPer;
+  const uint32_t word = w < 2 ? (w == 0 ? r.x : r.y) : (w == 2 ? r.z : r.w);
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(word);
+  } else {
+    const uint16_t h = (uint16_t)(i & 1 ? word >> 16 : word);
+    return to_f32(*reinterpret_cast<const T*>(&h));
+  }
+}
+// Value i of a vector (the same i in all lanes) to -inf.
+template <typename T>
+__device__ __forceinline__ void vector_clear(uint4& r, int i) {
+  constexpr int kPer = kVec<T> / 4;
+  const uint32_t inf = minus_infinity<T>().x, mask = sizeof(T) == 4 ? 0xffffffffu : i & 1 ? 0xffff0000u : 0xffffu;
+  const int w = i / kPer;
+  if (w == 0) r.x = (r.x & ~mask) | (inf & mask);
+  if (w == 1) r.y = (r.y & ~mask) | (inf & mask);
+  if (w == 2) r.z = (r.z & ~mask) | (inf & mask);
+  if (w == 3) r.w = (r.w & ~mask) | (inf & mask);
+}
+
+// A vector that is partly outside the row: value by value.
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T* x, int first, int vocab) {
+  uint4 r = minus_infinity<T>();
+  T v[kVec<T>];
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) {
+    v[i] = from_f32<T>(-INFINITY);
+    if (first + i >= 0 && first + i < vocab) v[i] = x[first + i];
+  }
+  memcpy(&r, v, sizeof(r));
+  return r;
+}
+
+// What a warp, a CTA or a row has seen.
+struct RowPart {
+  float v[32];
+  int id[32];
+  float s, t, C, R;
+  int bad;
+};
+
+// A warp's list (one entry a lane, lanes from `live` on empty) and sums (a lane's share).
+struct RowState {
+  float v;
+  int id;
+  float2 s2, t2;  // shares of the sums of 2^y and 2^y y
+  float C, R;     // reference; R = -inf: nothing seen yet
+  bool bad;       // a NaN or +inf was
+
+  __device__ __forceinline__ void add(float x, float L) {
+    const float y = fmaxf(fmaf(x - C, L, -R), -200.0f), e = exp2_approx(y);
+    s2.x += e;
+    t2.x = fmaf(e, y, t2.x);
+  }
+  // The sums stated for another reference, which is not below this one.
+  __device__ __forceinline__ void refer(float to_c, float to_r, float L) {
+    if (R > -INFINITY) {
+      const float d = fmaxf(fmaf(C - to_c, L, R - to_r), -1000.0f), f = exp2_approx(d);
+      t2.x = f * fmaf(d, s2.x, t2.x);
+      t2.y = f * fmaf(d, s2.y, t2.y);
+      s2.x *= f;
+      s2.y *= f;
+    }
+    C = to_c;
+    R = to_r;
+  }
+  // The value m as the reference.
+  __device__ __forceinline__ void refer(float m, float L) {
+    const bool far = !(fabsf(m * L) < kFar);
+    refer(far ? m : 0.0f, far ? 0.0f : m * L, L);
+  }
+  __device__ __forceinline__ void write(RowPart& p, int lane) {
+    const float s = warp_sum(s2.x + s2.y), t = warp_sum(t2.x + t2.y);
+    const bool any = __any_sync(0xffffffffu, bad);
+    p.v[lane] = v;
+    p.id[lane] = id;
+    if (lane == 0) {
+      p.s = s;
+      p.t = t;
+      p.C = C;
+      p.R = R;
+      p.bad = any;
+    }
+  }
+  __device__ __forceinline__ void read(const RowPart& p, int lane) {
+    v = p.v[lane];
+    id = p.id[lane];
+    s2 = make_float2(lane == 0 ? p.s : 0.0f, 0.0f);
+    t2 = make_float2(lane == 0 ? p.t : 0.0f, 0.0f);
+    C = p.C;
+    R = p.R;
+    bad = p.bad;
+  }
+};
+
+__device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
+
+// b's list and sums into a's: of 32 + 32 entries in falling order the lane's and
+// the other list's opposite one; the better of the two are the best 32.
+__device__ __forceinline__ void merge(RowState& a, const RowState& b, int live, int lane, float L) {
+  RowState o = b;
+  if (b.R > -INFINITY) {
+    if (a.R == -INFINITY || fmaf(b.C - a.C, L, b.R - a.R) > 0.0f)
+      a.refer(b.C, b.R, L);
+    else
+      o.refer(a.C, a.R, L);
+    a.s2 = add2(a.s2, o.s2);
+    a.t2 = add2(a.t2, o.t2);
+  }
+  a.bad |= b.bad;
+  float w = __shfl_sync(0xffffffffu, b.v, 31 - lane);
+  int j = __shfl_sync(0xffffffffu, b.id, 31 - lane);
+  if (before(w, j, a.v, a.id)) {
+    const float v = a.v;
+    const int i = a.id;
+    a.v = w, a.id = j;
+    w = v, j = i;
+  }
+#pragma unroll
+  for (int o2 = 16; o2; o2 >>= 1) {
+    const float ov = __shfl_xor_sync(0xffffffffu, a.v, o2);
+    const int oi = __shfl_xor_sync(0xffffffffu, a.id, o2);
+    const bool lower = !(lane & o2);  // keeps the better of the two
+    if (before(ov, oi, a.v, a.id) == lower) a.v = ov, a.id = oi;
+  }
+  const float more = lane >= live ? a.v : -INFINITY;
+  if (lane >= live) a.v = -INFINITY;
+  const float out = warp_max(fmaxf(w, more));  // the best of those that leave
+  if (out > -INFINITY) {
+    if (fmaf(out - a.C, L, -a.R) > kSlack) a.refer(out, L);
+    if (w > -INFINITY) a.add(w, L);
+    if (more > -INFINITY) a.add(more, L);
+  }
+}
+
+// The lists and sums of n warps, warp w's in w's state, into warp 0's.
+__device__ __forceinline__ void merge_warps(RowState& st, RowPart* parts, int n, int live, int warp, int lane, float L) {
+  for (int step = 1; step < n; step *= 2) {
+    __syncthreads();
+    if (warp < n && (warp & (2 * step - 1)) == step) st.write(parts[warp], lane);
+    __syncthreads();
+    if (warp + step < n && (warp & (2 * step - 1)) == 0) {
+      RowState o;
+      o.read(parts[warp + step], lane);
+      merge(st, o, live, lane, L);
+    }
+  }
+}
+
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 1) logprobs_kernel(const TokenLogprobs a, int cluster) {
+  constexpr int V = kVec<T>, kThreads = 32 * kWarps;
+  __shared__ RowPart parts[kWarps];
+  __shared__ float2 ends[kWarps];
+  __shared__ float said[2];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.logits) + row * a.ld;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto block_best = [&](Best b) {
-    b = warp_best(b);
-    if (lane == 0) part[warp] = b;
-    __syncthreads();
-    b = part[0];
-    for (int w = 1; w < kRowThreads / 32; ++w) b = better(b, part[w]);
-    __syncthreads();
-    return b;
-  };
-  const Best none = {-INFINITY, 0x7fffffff};
-  Best top = none;
-  int bad = 0;
-  for (int i = tid; i < a.vocab; i += kRowThreads) {
-    const float v = to_f32(x[i]);
-    bad |= !(v < INFINITY);
-    if (v > -INFINITY) top = better(top, Best{v, i});
+  const int64_t row = blockIdx.x / cluster;
+  const int rank = blockIdx.x - (int)row * cluster;
+  const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+  const float L = a.scale * kLog2e;
+  const int live = max(kLeast, a.top);
+
+  // the row's vectors by address: the first and the last may be partly outside
+  const int ahead = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+  const int vectors = (a.vocab + ahead + V - 1) / V, share = (vectors + cluster - 1) / cluster;
+  const int lo = rank * share, hi = min(vectors, lo + share);
+  const int whole = (a.vocab + ahead) / V;  // vectors from here on are not
+  // the first given token of this thread, long before it is needed
+  float given = 0.0f;
+  bool is_token = false;
+  if (rank == 0 && tid < a.n_tokens) {
+    const int id = a.tokens[row * a.n_tokens + tid];
+    is_token = id >= 0 && id < a.vocab;
+    if (is_token) given = to_f32(x[id]);
   }
-  bad = __syncthreads_or(bad);
-  top = block_best(top);
-  const bool empty = top.v == -INFINITY;
-  float s = 0.0f, e = 0.0f;
-  for (int i = tid; i < a.vocab; i += kRowThreads) {
-    const float d = (to_f32(x[i]) - top.v) * a.scale;
-    if (i != top.i && d > -200.0f) {  // also not NaN: -inf less -inf
-      const float p = expf(d);
-      s += p;
-      e = fmaf(p, d, e);
+
+  RowState st;
+  st.v = -INFINITY;
+  st.id = 0x7fffffff;
+  st.s2 = st.t2 = make_float2(0.0f, 0.0f);
+  st.C = 0.0f;
+  st.R = -INFINITY;
+  st.bad = false;
+  // entries are taken before (last_v, last_id); `look`: the smallest value that may be one
+  float last_v = -INFINITY, look = -INFINITY, largest = -INFINITY;
+  int last_id = 0x7fffffff;
+  const float2 L2 = make_float2(L, L);
+
+  const int batches = (hi - lo + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+#pragma unroll 1
+  for (int b = 0; b < batches; ++b) {
+    const int begin = lo + b * kThreads * kUnroll, first = begin + tid;
+    uint4 raw[kUnroll];
+    if (begin > 0 && begin + kThreads * kUnroll <= min(hi, whole)) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) raw[u] = ldg_nc_v4(x + (int64_t)(first + u * kThreads) * V - ahead);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int j = first + u * kThreads;
+        raw[u] = minus_infinity<T>();
+        if (j < hi) raw[u] = (j > 0 || ahead == 0) && j < whole ? ldg_nc_v4(x + (int64_t)j * V - ahead) : load_edge(x, j * V - ahead, a.vocab);
+      }
+    }
+    const float most = vectors_max<T, kUnroll>(raw);
+
+    if (b == 0 || b == kAgain) {
+      // a bound that at least `live` of the threads' largest reach
+      if (most < INFINITY) largest = fmaxf(largest, most);
+      const float up = warp_max(largest), down = -warp_max(largest > -INFINITY ? -largest : -INFINITY);
+      __syncthreads();
+      if (lane == 0) ends[warp] = make_float2(down, up);
+      if (__syncthreads_count(largest > -INFINITY) >= live) {
+        float l = INFINITY, h = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          l = fminf(l, ends[w].x);
+          h = fmaxf(h, ends[w].y);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const float mid = l + (h - l) * 0.5f;
+          if (__syncthreads_count(largest >= mid) >= live) l = mid; else h = mid;
+        }
+        if (l > last_v) {
+          last_v = look = l;
+          last_id = 0x7fffffff;
+          if (fmaf(l - st.C, L, -st.R) > kSlack) st.refer(l, L);
+        }
+      }
+    } else if (b < kAgain) {
+      if (most < INFINITY) largest = fmaxf(largest, most);
+    }
+
+    if (__any_sync(0xffffffffu, !(most < look) && most != -INFINITY)) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const float m = vectors_max<T, 1>(&raw[u]);
+        uint32_t lanes = __ballot_sync(0xffffffffu, !(m < look) && m != -INFINITY);
+#pragma unroll 1
+        while (lanes) {  // a lane's vector, its values one a lane
+          const int src = __ffs(lanes) - 1;
+          lanes &= lanes - 1;
+          const uint4 r = make_uint4(__shfl_sync(0xffffffffu, raw[u].x, src), __shfl_sync(0xffffffffu, raw[u].y, src),
+                                     __shfl_sync(0xffffffffu, raw[u].z, src), __shfl_sync(0xffffffffu, raw[u].w, src));
+          const float v = vector_value<T>(r, lane % V);
+          const int id = (first - lane + src + u * kThreads) * V - ahead + lane;
+          if (!(v < INFINITY)) st.bad = true;
+          uint32_t who = __ballot_sync(0xffffffffu, lane < V && v > -INFINITY && before(v, id, last_v, last_id));
+#pragma unroll 1
+          while (who) {
+            const int j = __ffs(who) - 1;
+            who &= who - 1;
+            const float c = __shfl_sync(0xffffffffu, v, j);
+            const int ci = __shfl_sync(0xffffffffu, id, j);
+            const int at = __popc(__ballot_sync(0xffffffffu, before(st.v, st.id, c, ci)));
+            if (at >= live) continue;
+            const float uv = __shfl_up_sync(0xffffffffu, st.v, 1);
+            const int ui = __shfl_up_sync(0xffffffffu, st.id, 1);
+            const float out = lane == live - 1 ? st.v : -INFINITY;
+            if (lane >= at && lane < live) {
+              st.v = lane == at ? c : uv;
+              st.id = lane == at ? ci : ui;
+            }
+            if (lane == src) vector_clear<T>(raw[u], j);
+            const float lv = __shfl_sync(0xffffffffu, st.v, live - 1);
+            const int li = __shfl_sync(0xffffffffu, st.id, live - 1);
+            if (before(lv, li, last_v, last_id)) {
+              last_v = lv;
+              last_id = li;
+              // later ids are higher, so equal values come too late
+              look = lv == 0.0f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(lv) + (lv > 0.0f ? 1 : -1));
+              if (fmaf(lv - st.C, L, -st.R) > kSlack) st.refer(lv, L);
+            }
+            if (out > -INFINITY) st.add(out, L);
+          }
+        }
+      }
+    }
+
+    if (st.R == -INFINITY) continue;  // all there was is in the list
+    // what is so small that it adds nothing, and -inf, enter as one finite value of that kind
+    const float2 R2 = make_float2(-st.R, -st.R);
+    const T least = from_f32<T>(fmaxf((st.R - 160.0f) / L, std::is_same<T, __half>::value ? -65504.0f : -3.0e38f));
+    if (st.C == 0.0f && fmaf(to_f32(least), L, -st.R) <= -150.0f) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float v[V];
+        if constexpr (sizeof(T) == 4) {
+          unpack16<T>(raw[u], v);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] = fmaxf(v[i], least);
+        } else {
+          Pair<T> both;
+          both.x = both.y = least;
+          uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const Pair<T> p = __hmax2(*reinterpret_cast<Pair<T>*>(&w[i]), both);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          unpack16<T>(make_uint4(w[0], w[1], w[2], w[3]), v);
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float2 y = fma2(make_float2(v[i], v[i + 1]), L2, R2);
+          const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          st.s2 = add2(st.s2, e);
+          st.t2 = fma2(e, y, st.t2);
+        }
+      }
+    } else {  // logits so large, or a scale so small, that the type has no such value
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) st.add(vector_value<T>(raw[u], i), L);
     }
   }
-  s = warp_sum(s);
-  e = warp_sum(e);
-  if (lane == 0) {
-    sums[0][warp] = s;
-    sums[1][warp] = e;
+
+  merge_warps(st, parts, kWarps, live, warp, lane, L);
+  if (cluster > 1) {
+    __syncthreads();
+    if (warp == 0) st.write(parts[0], lane);
+    cg::this_cluster().sync();
+    if (rank == 0) {
+      st.v = -INFINITY;
+      if (warp < cluster) st.read(*cg::this_cluster().map_shared_rank(&parts[0], warp), lane);
+    }
+    cg::this_cluster().sync();  // all are read: the others may leave
+    if (rank != 0) return;
+    merge_warps(st, parts, cluster, live, warp, lane, L);
   }
-  __syncthreads();
-  s = e = 0.0f;
-  for (int w = 0; w < kRowThreads / 32; ++w) {
-    s += sums[0][w];
-    e += sums[1][w];
-  }
-  const float drop = log1pf(s);
+
   const float nan = __int_as_float(0x7fc00000);
-  if (tid == 0) {
-    if (bad && a.status) *a.status = MMVQ_ERR_VALUE;
-    if (a.lse) a.lse[row] = bad ? nan : empty ? -INFINITY : fmaf(top.v, a.scale, drop);
-    if (a.entropy) a.entropy[row] = bad ? nan : empty ? 0.0f : drop - e / (1.0f + s);
-  }
-  for (int j = tid; j < a.n_tokens; j += kRowThreads) {
-    const int id = a.tokens[row * a.n_tokens + j];
-    float p = nan;
-    if (id < 0 || id >= a.vocab) {
-      if (a.status) *a.status = MMVQ_ERR_ROUTING;
-    } else if (!bad) {
-      p = empty ? -INFINITY : (to_f32(x[id]) - top.v) * a.scale - drop;
+  if (warp == 0) {
+    const bool bad = __any_sync(0xffffffffu, st.bad);
+    const float m = __shfl_sync(0xffffffffu, st.v, 0);
+    const bool empty = m == -INFINITY;
+    // x - m, at most 0, and what its two roundings left
+    const float diff = st.v - m, back = diff - st.v, d = diff * a.scale;
+    float e = 0.0f, ed = 0.0f;
+    if (lane > 0 && d > -200.0f) {
+      const float rest = fmaf(diff, a.scale, -d) + ((st.v - (diff - back)) - (m + back)) * a.scale;
+      e = fmaf(expf(d), rest, expf(d));
+      ed = e * d;
     }
-    a.logprobs[row * a.n_tokens + j] = p;
-  }
-  Best last = top;
-  for (int j = 0; j < a.top; ++j) {
-    if (tid == 0) {
-      const bool no = bad || last.v == -INFINITY;
-      a.top_ids[row * a.top + j] = no ? -1 : last.i;
-      a.top_logprobs[row * a.top + j] = bad ? nan : no ? -INFINITY : (last.v - top.v) * a.scale - drop;
+    const float s = warp_sum(st.s2.x + st.s2.y), t = warp_sum(st.t2.x + st.t2.y);
+    if (lane == 0 && st.R > -INFINITY && s > 0.0f) {
+      // From the reference to m, and what L's rounding makes of the mean x: both exponents
+      // can be large where the sums are small, hence in 64 bits.
+      const double exact = (double)a.scale * 1.4426950408889634074;
+      const double Y = fmax(-400.0, (double)st.R + ((double)st.C - (double)m) * exact + (double)((t / s + st.R) / L) * (exact - (double)L));
+      const double near = rint(Y);
+      const float f = ldexpf(exp2f((float)(Y - near)), (int)near);
+      e = f * s;
+      ed = f * kLn2 * fmaf((float)Y, s, t);
     }
-    Best b = none;
-    for (int i = tid; i < a.vocab; i += kRowThreads) {
-      const float v = to_f32(x[i]);
-      if (v > -INFINITY && (v < last.v || (v == last.v && i > last.i))) b = better(b, Best{v, i});
+    const float S = warp_sum(e), E = warp_sum(ed);
+    const float drop = log1pf(S);
+    if (lane == 0) {
+      if (bad && a.status) *a.status = MMVQ_ERR_VALUE;
+      if (a.lse) a.lse[row] = bad ? nan : empty ? -INFINITY : fmaf(m, a.scale, drop);
+      if (a.entropy) a.entropy[row] = bad ? nan : empty ? 0.0f : drop - E / (1.0f + S);
+      said[0] = bad ? nan : m;
+      said[1] = drop;
     }
-    last = block_best(b);
+    if (lane < a.top) {
+      const bool no = bad || st.v == -INFINITY;
+      a.top_ids[row * a.top + lane] = no ? -1 : st.id;
+      a.top_logprobs[row * a.top + lane] = bad ? nan : no ? -INFINITY : d - drop;
+    }
   }
+  if (a.n_tokens == 0) return;
+  __syncthreads();
+  const float m = said[0], drop = said[1];
+  for (int j = tid; j < a.n_tokens; j += kThreads) {
+    if (j != tid) {
+      const int id = a.tokens[row * a.n_tokens + j];
+      is_token = id >= 0 && id < a.vocab;
+      if (is_token) given = to_f32(x[id]);
+    }
+    if (!is_token && a.status) *a.status = MMVQ_ERR_ROUTING;
+    a.logprobs[row * a.n_tokens + j] = !is_token || m != m ? nan : m == -INFINITY ? m : (given - m) * a.scale - drop;
+  }
+}
+
+template <typename T, int kWarps>
+static int launch_rows(const TokenLogprobs& a, int cluster, cudaStream_t stream) {
+  auto kern = logprobs_kernel<T, kWarps>;
+  if (cluster > 8) {  // more than every device takes: to be allowed once on each
+    static int per_device[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MMVQ_ERR_CUDA;
+    if (!__atomic_load_n(&per_device[dev], __ATOMIC_ACQUIRE)) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return MMVQ_ERR_CUDA;
+      __atomic_store_n(&per_device[dev], 1, __ATOMIC_RELEASE);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.rows * cluster);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, cluster) == cudaSuccess ? MMVQ_OK : MMVQ_ERR_CUDA;
 }
 
 int launch_token_logprobs(const TokenLogprobs& a, int dtype, cudaStream_t stream) {
   return with_dtype(dtype, [&](auto v) {
-    return launch_pdl(logprobs_kernel<decltype(v)>, dim3((unsigned)a.rows), dim3(kRowThreads), 0, stream, a);
+    using T = decltype(v);
+    const int vectors = (a.vocab + 2 * kVec<T> - 1) / kVec<T>;
+    if (vectors <= 32 * 2 * kUnroll) return launch_rows<T, 1>(a, 1, stream);
+    if (vectors <= 128 * 2 * kUnroll) return launch_rows<T, 4>(a, 1, stream);
+    // As many CTAs to a row as still have a batch of vectors each, up to two CTAs an SM in all.
+    int cluster = 1;
+    while (cluster < 16 && (int64_t)a.rows * cluster * 2 <= 2 * 152 && vectors >= 2 * cluster * 512 * kUnroll / 2) cluster *= 2;
+    return launch_rows<T, 16>(a, cluster, stream);
   });
 }
 
