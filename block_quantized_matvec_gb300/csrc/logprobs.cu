@@ -15,12 +15,15 @@
 // the end; what remains besides the sums is the list, whose first is m.
 //
 // What it spends: about 44 instructions for 8 logits of 16 bits (a maximum in
-// pairs, conversions, two packed fp32 operations and an ex2 each).  Lists are
-// entered rarely: from its first vectors, and again from three times as many, each
-// CTA finds a bound that `live` values reach, by halving the span of its threads'
-// largest ones, and a warp looks closer only where the largest of a batch reaches
-// the bound or its list's last; the code for that is kept small, since 16 warps
-// that wait for instructions cost more than the ones they run.
+// pairs, conversions, two packed fp32 operations and an ex2 each), so the row comes
+// through a ring of asynchronous copies, each thread's own, and CTAs are small: four
+// rows an SM, which wait for one another at no barrier.  Lists are entered rarely:
+// from its first batch of vectors, and again from three times as many and so on, each
+// CTA finds a bound that `live` values reach, by counting its threads' largest ones
+// in 64 bins; a warp looks closer only where the largest of a batch reaches the bound
+// or its list's last, and then at a lane's vectors one value a lane.  (Code for that
+// unrolled over the batch's values took 688 us for 2048 rows of 151936 in place of
+// 192: the warps waited for instructions.)
 //
 // A row is shared out to the CTAs of a cluster where rows are few; the first one
 // reads the others' lists and sums from their shared memory.
@@ -39,9 +42,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the entropy's sum cancels by that much at most.
 constexpr float kSlack = 3.0f;
 constexpr float kFar = 0x1p100f;  // |x log2(e)| from which on C is taken off first
-constexpr int kUnroll = 4;   // 16-byte loads of a thread in flight: a batch
+constexpr int kUnroll = 4;   // 16-byte vectors of a thread in a batch
+constexpr int kStages = 3;   // batches of the ring
+constexpr int kBins = 64;    // of the bound's count
 constexpr int kLeast = 8;    // a list's entries, however few are asked for
-constexpr int kAgain = 2;    // the batch at which the bound is found again
+constexpr int kAgain = 4;    // the bound is found again after three times as many batches as before
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
@@ -64,6 +69,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
+}
+// 16 bytes to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -102,31 +111,6 @@ __device__ __forceinline__ float vectors_max(const uint4* r) {
     }
     return max_nan(to_f32(m.x), to_f32(m.y));
   }
-}
-
-// Value i of a vector; i differs from lane to lane.
-template <typename T>
-__device__ __forceinline__ float vector_value(const uint4& r, int i) {
-  constexpr int kPer = kVec<T> / 4;
-  const int w = i / kPer;
-  const uint32_t word = w < 2 ? (w == 0 ? r.x : r.y) : (w == 2 ? r.z : r.w);
-  if constexpr (sizeof(T) == 4) {
-    return __uint_as_float(word);
-  } else {
-    const uint16_t h = (uint16_t)(i & 1 ? word >> 16 : word);
-    return to_f32(*reinterpret_cast<const T*>(&h));
-  }
-}
-// Value i of a vector (the same i in all lanes) to -inf.
-template <typename T>
-__device__ __forceinline__ void vector_clear(uint4& r, int i) {
-  constexpr int kPer = kVec<T> / 4;
-  const uint32_t inf = minus_infinity<T>().x, mask = sizeof(T) == 4 ? 0xffffffffu : i & 1 ? 0xffff0000u : 0xffffu;
-  const int w = i / kPer;
-  if (w == 0) r.x = (r.x & ~mask) | (inf & mask);
-  if (w == 1) r.y = (r.y & ~mask) | (inf & mask);
-  if (w == 2) r.z = (r.z & ~mask) | (inf & mask);
-  if (w == 3) r.w = (r.w & ~mask) | (inf & mask);
 }
 
 // A vector that is partly outside the row: value by value.
@@ -260,11 +244,13 @@ __device__ __forceinline__ void merge_warps(RowState& st, RowPart* parts, int n,
 }
 
 template <typename T, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 1) logprobs_kernel(const TokenLogprobs a, int cluster) {
+__global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) logprobs_kernel(const TokenLogprobs a, int cluster) {
   constexpr int V = kVec<T>, kThreads = 32 * kWarps;
   __shared__ RowPart parts[kWarps];
   __shared__ float2 ends[kWarps];
   __shared__ float said[2];
+  __shared__ int count[kBins];
+  extern __shared__ uint4 ring[];  // [kStages][kUnroll][kThreads]
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -297,33 +283,49 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 1) logprobs_ke
   st.bad = false;
   // entries are taken before (last_v, last_id); `look`: the smallest value that may be one
   float last_v = -INFINITY, look = -INFINITY, largest = -INFINITY;
-  int last_id = 0x7fffffff;
+  int last_id = 0x7fffffff, next = 0;
+  const float one_over_L = 1.0f / L;
   const float2 L2 = make_float2(L, L);
 
   const int batches = (hi - lo + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-#pragma unroll 1
-  for (int b = 0; b < batches; ++b) {
+  // vector u of this thread in a stage
+  auto slot = [&](int b, int u) { return ring + ((b % kStages) * kUnroll + u) * kThreads + tid; };
+  auto fetch = [&](int b) {
     const int begin = lo + b * kThreads * kUnroll, first = begin + tid;
-    uint4 raw[kUnroll];
     if (begin > 0 && begin + kThreads * kUnroll <= min(hi, whole)) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) raw[u] = ldg_nc_v4(x + (int64_t)(first + u * kThreads) * V - ahead);
-    } else {
-#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) copy16(slot(b, u), x + (int64_t)(first + u * kThreads) * V - ahead);
+    } else if (b < batches) {
+#pragma unroll 1
       for (int u = 0; u < kUnroll; ++u) {
         const int j = first + u * kThreads;
-        raw[u] = minus_infinity<T>();
-        if (j < hi) raw[u] = (j > 0 || ahead == 0) && j < whole ? ldg_nc_v4(x + (int64_t)j * V - ahead) : load_edge(x, j * V - ahead, a.vocab);
+        if (j >= hi) *slot(b, u) = minus_infinity<T>();
+        else if ((j > 0 || ahead == 0) && j < whole) copy16(slot(b, u), x + (int64_t)j * V - ahead);
+        else *slot(b, u) = load_edge(x, j * V - ahead, a.vocab);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int b = 0; b < kStages - 1; ++b) fetch(b);
+#pragma unroll 1
+  for (int b = 0; b < batches; ++b) {
+    fetch(b + kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    uint4 raw[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) raw[u] = *slot(b, u);
     const float most = vectors_max<T, kUnroll>(raw);
+    if (most < INFINITY) largest = fmaxf(largest, most);
 
-    if (b == 0 || b == kAgain) {
+    if (b == next) {  // 0, 2, 8, 32, ...
+      next = max(2, kAgain * next);
       // a bound that at least `live` of the threads' largest reach
-      if (most < INFINITY) largest = fmaxf(largest, most);
       const float up = warp_max(largest), down = -warp_max(largest > -INFINITY ? -largest : -INFINITY);
-      __syncthreads();
+      if (kWarps > 1) __syncthreads(); else __syncwarp();
       if (lane == 0) ends[warp] = make_float2(down, up);
+      if (tid < kBins) count[tid] = 0;
+      if (kBins > kThreads && tid + kThreads < kBins) count[tid + kThreads] = 0;
       if (__syncthreads_count(largest > -INFINITY) >= live) {
         float l = INFINITY, h = -INFINITY;
 #pragma unroll
@@ -331,71 +333,80 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 1) logprobs_ke
           l = fminf(l, ends[w].x);
           h = fmaxf(h, ends[w].y);
         }
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          const float mid = l + (h - l) * 0.5f;
-          if (__syncthreads_count(largest >= mid) >= live) l = mid; else h = mid;
+        const float per = h - l < INFINITY && h - l > 1e-30f ? (kBins - 0.5f) / (h - l) : 0.0f;  // bins a unit
+        if (largest > -INFINITY) atomicAdd(&count[min((int)((largest - l) * per), kBins - 1)], 1);
+        __syncthreads();
+        // the highest bin that `live` stand in or above; its lower end less a hundredth of it, for the roundings
+        const int c1 = count[2 * lane + 1], c0 = count[2 * lane];
+        int above = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int n = __shfl_down_sync(0xffffffffu, above, o);
+          if (lane + o < 32) above += n;
         }
+        const int pair = 31 - __clz(__ballot_sync(0xffffffffu, above >= live));
+        const int odd = __shfl_sync(0xffffffffu, above - c0 >= live, pair);
+        const int bin = 2 * pair + odd;
+        if (bin > 0 && per > 0.0f) l = fmaxf(l, fmaf((float)bin - 0.01f, 1.0f / per, l));
         if (l > last_v) {
           last_v = look = l;
           last_id = 0x7fffffff;
           if (fmaf(l - st.C, L, -st.R) > kSlack) st.refer(l, L);
         }
       }
-    } else if (b < kAgain) {
-      if (most < INFINITY) largest = fmaxf(largest, most);
     }
 
-    if (__any_sync(0xffffffffu, !(most < look) && most != -INFINITY)) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const float m = vectors_max<T, 1>(&raw[u]);
-        uint32_t lanes = __ballot_sync(0xffffffffu, !(m < look) && m != -INFINITY);
+    uint32_t lanes = __ballot_sync(0xffffffffu, !(most < look) && most != -INFINITY);
+    if (lanes) {
+      const int begin = lo + b * kThreads * kUnroll + warp * 32;
+      __syncwarp();  // the lanes' copies
 #pragma unroll 1
-        while (lanes) {  // a lane's vector, its values one a lane
-          const int src = __ffs(lanes) - 1;
-          lanes &= lanes - 1;
-          const uint4 r = make_uint4(__shfl_sync(0xffffffffu, raw[u].x, src), __shfl_sync(0xffffffffu, raw[u].y, src),
-                                     __shfl_sync(0xffffffffu, raw[u].z, src), __shfl_sync(0xffffffffu, raw[u].w, src));
-          const float v = vector_value<T>(r, lane % V);
-          const int id = (first - lane + src + u * kThreads) * V - ahead + lane;
-          if (!(v < INFINITY)) st.bad = true;
-          uint32_t who = __ballot_sync(0xffffffffu, lane < V && v > -INFINITY && before(v, id, last_v, last_id));
+      while (lanes) {  // a lane's vectors, their values one a lane
+        const int src = __ffs(lanes) - 1;
+        lanes &= lanes - 1;
+        const int u = min(lane / V, kUnroll - 1);
+        T* p = reinterpret_cast<T*>(slot(b, u) - lane + src) + lane % V;
+        const int id = (begin + src + u * kThreads) * V - ahead + lane % V;
+        const float v = lane < kUnroll * V ? to_f32(*p) : -INFINITY;
+        if (!(v < INFINITY)) st.bad = true;
+        uint32_t who = __ballot_sync(0xffffffffu, v > -INFINITY && before(v, id, last_v, last_id));
 #pragma unroll 1
-          while (who) {
-            const int j = __ffs(who) - 1;
-            who &= who - 1;
-            const float c = __shfl_sync(0xffffffffu, v, j);
-            const int ci = __shfl_sync(0xffffffffu, id, j);
-            const int at = __popc(__ballot_sync(0xffffffffu, before(st.v, st.id, c, ci)));
-            if (at >= live) continue;
-            const float uv = __shfl_up_sync(0xffffffffu, st.v, 1);
-            const int ui = __shfl_up_sync(0xffffffffu, st.id, 1);
-            const float out = lane == live - 1 ? st.v : -INFINITY;
-            if (lane >= at && lane < live) {
-              st.v = lane == at ? c : uv;
-              st.id = lane == at ? ci : ui;
-            }
-            if (lane == src) vector_clear<T>(raw[u], j);
-            const float lv = __shfl_sync(0xffffffffu, st.v, live - 1);
-            const int li = __shfl_sync(0xffffffffu, st.id, live - 1);
-            if (before(lv, li, last_v, last_id)) {
-              last_v = lv;
-              last_id = li;
-              // later ids are higher, so equal values come too late
-              look = lv == 0.0f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(lv) + (lv > 0.0f ? 1 : -1));
-              if (fmaf(lv - st.C, L, -st.R) > kSlack) st.refer(lv, L);
-            }
-            if (out > -INFINITY) st.add(out, L);
+        while (who) {
+          const int j = __ffs(who) - 1;
+          who &= who - 1;
+          const float c = __shfl_sync(0xffffffffu, v, j);
+          const int ci = __shfl_sync(0xffffffffu, id, j);
+          const int at = __popc(__ballot_sync(0xffffffffu, before(st.v, st.id, c, ci)));
+          if (at >= live) continue;
+          const float uv = __shfl_up_sync(0xffffffffu, st.v, 1);
+          const int ui = __shfl_up_sync(0xffffffffu, st.id, 1);
+          const float out = lane == live - 1 ? st.v : -INFINITY;
+          if (lane >= at && lane < live) {
+            st.v = lane == at ? c : uv;
+            st.id = lane == at ? ci : ui;
           }
+          if (lane == j) *p = from_f32<T>(-INFINITY);
+          const float lv = __shfl_sync(0xffffffffu, st.v, live - 1);
+          const int li = __shfl_sync(0xffffffffu, st.id, live - 1);
+          if (before(lv, li, last_v, last_id)) {
+            last_v = lv;
+            last_id = li;
+            // the ids of later batches are higher, so equal values come too late
+            look = lv == 0.0f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(lv) + (lv > 0.0f ? 1 : -1));
+            if (fmaf(lv - st.C, L, -st.R) > kSlack) st.refer(lv, L);
+          }
+          if (out > -INFINITY) st.add(out, L);
         }
       }
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) raw[u] = *slot(b, u);
     }
 
     if (st.R == -INFINITY) continue;  // all there was is in the list
     // what is so small that it adds nothing, and -inf, enter as one finite value of that kind
     const float2 R2 = make_float2(-st.R, -st.R);
-    const T least = from_f32<T>(fmaxf((st.R - 160.0f) / L, std::is_same<T, __half>::value ? -65504.0f : -3.0e38f));
+    const T least = from_f32<T>(fmaxf((st.R - 160.0f) * one_over_L, std::is_same<T, __half>::value ? -65504.0f : -3.0e38f));
     if (st.C == 0.0f && fmaf(to_f32(least), L, -st.R) <= -150.0f) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -427,7 +438,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 1) logprobs_ke
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll 1
-        for (int i = 0; i < V; ++i) st.add(vector_value<T>(raw[u], i), L);
+        for (int i = 0; i < V; ++i) st.add(to_f32(reinterpret_cast<const T*>(slot(b, u))[i]), L);
     }
   }
 
@@ -501,18 +512,20 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 1) logprobs_ke
 template <typename T, int kWarps>
 static int launch_rows(const TokenLogprobs& a, int cluster, cudaStream_t stream) {
   auto kern = logprobs_kernel<T, kWarps>;
-  if (cluster > 8) {  // more than every device takes: to be allowed once on each
-    static int per_device[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MMVQ_ERR_CUDA;
-    if (!__atomic_load_n(&per_device[dev], __ATOMIC_ACQUIRE)) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return MMVQ_ERR_CUDA;
-      __atomic_store_n(&per_device[dev], 1, __ATOMIC_RELEASE);
-    }
+  const int smem = kStages * kUnroll * 32 * kWarps * 16;
+  static int per_device[64];  // whether the kernel has its attributes there
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MMVQ_ERR_CUDA;
+  if (!__atomic_load_n(&per_device[dev], __ATOMIC_ACQUIRE)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return MMVQ_ERR_CUDA;
+    __atomic_store_n(&per_device[dev], 1, __ATOMIC_RELEASE);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * cluster);
   cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -531,6 +544,7 @@ int launch_token_logprobs(const TokenLogprobs& a, int dtype, cudaStream_t stream
     const int vectors = (a.vocab + 2 * kVec<T> - 1) / kVec<T>;
     if (vectors <= 32 * 2 * kUnroll) return launch_rows<T, 1>(a, 1, stream);
     if (vectors <= 128 * 2 * kUnroll) return launch_rows<T, 4>(a, 1, stream);
+    if (a.rows > 304) return launch_rows<T, 8>(a, 1, stream);
     // As many CTAs to a row as still have a batch of vectors each, up to two CTAs an SM in all.
     int cluster = 1;
     while (cluster < 16 && (int64_t)a.rows * cluster * 2 <= 2 * 152 && vectors >= 2 * cluster * 512 * kUnroll / 2) cluster *= 2;
