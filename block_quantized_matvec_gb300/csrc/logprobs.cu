@@ -27,6 +27,8 @@
 //
 // A row is shared out to the CTAs of a cluster where rows are few; the first one
 // reads the others' lists and sums from their shared memory.
+#include <cfloat>
+
 #include <cooperative_groups.h>
 
 #include "layer.cuh"
@@ -42,8 +44,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the entropy's sum cancels by that much at most.
 constexpr float kSlack = 3.0f;
 constexpr float kFar = 0x1p100f;  // |x log2(e)| from which on C is taken off first
-constexpr int kUnroll = 4;   // 16-byte vectors of a thread in a batch
-constexpr int kStages = 3;   // batches of the ring
+constexpr int kStages = 2;   // batches of the ring
 constexpr int kBins = 64;    // of the bound's count
 constexpr int kLeast = 8;    // a list's entries, however few are asked for
 constexpr int kAgain = 4;    // the bound is found again after three times as many batches as before
@@ -51,23 +52,6 @@ constexpr int kAgain = 4;    // the bound is found again after three times as ma
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{.reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};"
-      " fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w;}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{.reg .b64 x, y, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};"
-      " add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w;}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 // 16 bytes to shared memory, asynchronously.
@@ -191,42 +175,56 @@ struct RowState {
 
 __device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
 
-// b's list and sums into a's: of 32 + 32 entries in falling order the lane's and
-// the other list's opposite one; the better of the two are the best 32.
-__device__ __forceinline__ void merge(RowState& a, const RowState& b, int live, int lane, float L) {
-  RowState o = b;
-  if (b.R > -INFINITY) {
-    if (a.R == -INFINITY || fmaf(b.C - a.C, L, b.R - a.R) > 0.0f)
-      a.refer(b.C, b.R, L);
-    else
-      o.refer(a.C, a.R, L);
-    a.s2 = add2(a.s2, o.s2);
-    a.t2 = add2(a.t2, o.t2);
-  }
-  a.bad |= b.bad;
-  float w = __shfl_sync(0xffffffffu, b.v, 31 - lane);
-  int j = __shfl_sync(0xffffffffu, b.id, 31 - lane);
+// One step of a sort: of this lane's entry and that of lane ^ o, the better one where `keep`.
+__device__ __forceinline__ void exchange(float& v, int& id, int o, bool keep) {
+  const float ov = __shfl_xor_sync(0xffffffffu, v, o);
+  const int oi = __shfl_xor_sync(0xffffffffu, id, o);
+  if (before(ov, oi, v, id) == keep) v = ov, id = oi;
+}
+// The warp's 32 entries in falling order (a bitonic sort).
+__device__ __forceinline__ void sort(float& v, int& id, int lane) {
+#pragma unroll
+  for (int n = 2; n <= 32; n *= 2)
+#pragma unroll
+    for (int o = n / 2; o; o >>= 1) exchange(v, id, o, !(lane & o) == !(lane & n));
+}
+
+// The entries (v, id), in falling order, into a's list: of 32 + 32 the lane's and the
+// opposite one of the others; the better of the two are the best 32.  What leaves the
+// list goes into the sums.
+__device__ __forceinline__ void absorb(RowState& a, float v, int id, int live, int lane, float L) {
+  float w = __shfl_sync(0xffffffffu, v, 31 - lane);
+  const int j = __shfl_sync(0xffffffffu, id, 31 - lane);
   if (before(w, j, a.v, a.id)) {
-    const float v = a.v;
-    const int i = a.id;
+    const float x = a.v;
     a.v = w, a.id = j;
-    w = v, j = i;
+    w = x;
   }
 #pragma unroll
-  for (int o2 = 16; o2; o2 >>= 1) {
-    const float ov = __shfl_xor_sync(0xffffffffu, a.v, o2);
-    const int oi = __shfl_xor_sync(0xffffffffu, a.id, o2);
-    const bool lower = !(lane & o2);  // keeps the better of the two
-    if (before(ov, oi, a.v, a.id) == lower) a.v = ov, a.id = oi;
-  }
+  for (int o = 16; o; o >>= 1) exchange(a.v, a.id, o, !(lane & o));
   const float more = lane >= live ? a.v : -INFINITY;
-  if (lane >= live) a.v = -INFINITY;
+  if (lane >= live) a.v = -INFINITY, a.id = 0x7fffffff;
   const float out = warp_max(fmaxf(w, more));  // the best of those that leave
   if (out > -INFINITY) {
     if (fmaf(out - a.C, L, -a.R) > kSlack) a.refer(out, L);
     if (w > -INFINITY) a.add(w, L);
     if (more > -INFINITY) a.add(more, L);
   }
+}
+
+// b's list and sums into a's.
+__device__ __forceinline__ void merge(RowState& a, const RowState& b, int live, int lane, float L) {
+  if (b.R > -INFINITY) {
+    RowState o = b;
+    if (a.R == -INFINITY || fmaf(b.C - a.C, L, b.R - a.R) > 0.0f)
+      a.refer(b.C, b.R, L);
+    else
+      o.refer(a.C, a.R, L);
+    a.s2 = __fadd2_rn(a.s2, o.s2);
+    a.t2 = __fadd2_rn(a.t2, o.t2);
+  }
+  a.bad |= b.bad;
+  absorb(a, b.v, b.id, live, lane, L);
 }
 
 // The lists and sums of n warps, warp w's in w's state, into warp 0's.
@@ -243,8 +241,8 @@ __device__ __forceinline__ void merge_warps(RowState& st, RowPart* parts, int n,
   }
 }
 
-template <typename T, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) logprobs_kernel(const TokenLogprobs a, int cluster) {
+template <typename T, int kWarps, int kUnroll>  // kUnroll: 16-byte vectors of a thread in a batch
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 7 : 1) logprobs_kernel(const TokenLogprobs a, int cluster) {
   constexpr int V = kVec<T>, kThreads = 32 * kWarps;
   __shared__ RowPart parts[kWarps];
   __shared__ float2 ends[kWarps];
@@ -281,27 +279,47 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) lo
   st.C = 0.0f;
   st.R = -INFINITY;
   st.bad = false;
-  // entries are taken before (last_v, last_id); `look`: the smallest value that may be one
-  float last_v = -INFINITY, look = -INFINITY, largest = -INFINITY;
-  int last_id = 0x7fffffff, next = 0;
+  // values from last_v on may enter the list, in batches to come those from `look` on
+  float last_v = -FLT_MAX, look = -FLT_MAX, largest = -INFINITY;
+  int next = 0;
   const float one_over_L = 1.0f / L;
   const float2 L2 = make_float2(L, L);
+  // entries that are still to be sorted into the list, one a lane
+  float wait_v = -INFINITY;
+  int wait_id = 0x7fffffff, waiting = 0;
+  auto settle = [&]() {
+    sort(wait_v, wait_id, lane);
+    absorb(st, wait_v, wait_id, live, lane, L);
+    wait_v = -INFINITY;
+    wait_id = 0x7fffffff;
+    waiting = 0;
+    const float lv = __shfl_sync(0xffffffffu, st.v, live - 1);
+    if (lv >= last_v) {
+      last_v = lv;
+      // the ids of later batches are higher, so equal values come too late
+      look = lv == 0.0f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(lv) + (lv > 0.0f ? 1 : -1));
+      if (fmaf(lv - st.C, L, -st.R) > kSlack) st.refer(lv, L);
+    }
+  };
 
   const int batches = (hi - lo + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  // vector u of this thread in a stage
-  auto slot = [&](int b, int u) { return ring + ((b % kStages) * kUnroll + u) * kThreads + tid; };
+  const int inside = min(hi, whole) - kThreads * kUnroll;  // batches that begin behind it are not all whole vectors
+  // this thread's vectors of a stage, kThreads apart
+  auto stage = [&](int b) { return ring + (b % kStages) * kUnroll * kThreads + tid; };
   auto fetch = [&](int b) {
     const int begin = lo + b * kThreads * kUnroll, first = begin + tid;
-    if (begin > 0 && begin + kThreads * kUnroll <= min(hi, whole)) {
+    uint4* to = stage(b);
+    const T* from = x + ((int64_t)first * V - ahead);
+    if (begin > 0 && begin <= inside) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) copy16(slot(b, u), x + (int64_t)(first + u * kThreads) * V - ahead);
+      for (int u = 0; u < kUnroll; ++u) copy16(to + u * kThreads, from + u * kThreads * V);
     } else if (b < batches) {
 #pragma unroll 1
       for (int u = 0; u < kUnroll; ++u) {
         const int j = first + u * kThreads;
-        if (j >= hi) *slot(b, u) = minus_infinity<T>();
-        else if ((j > 0 || ahead == 0) && j < whole) copy16(slot(b, u), x + (int64_t)j * V - ahead);
-        else *slot(b, u) = load_edge(x, j * V - ahead, a.vocab);
+        if (j >= hi) to[u * kThreads] = minus_infinity<T>();
+        else if ((j > 0 || ahead == 0) && j < whole) copy16(to + u * kThreads, from + u * kThreads * V);
+        else to[u * kThreads] = load_edge(x, j * V - ahead, a.vocab);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -312,11 +330,15 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) lo
   for (int b = 0; b < batches; ++b) {
     fetch(b + kStages - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    uint4 raw[kUnroll];
+    uint4* const mine = stage(b);
+    float most;
+    {
+      uint4 raw[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) raw[u] = *slot(b, u);
-    const float most = vectors_max<T, kUnroll>(raw);
-    if (most < INFINITY) largest = fmaxf(largest, most);
+      for (int u = 0; u < kUnroll; ++u) raw[u] = mine[u * kThreads];
+      most = vectors_max<T, kUnroll>(raw);
+    }
+    if (most < INFINITY) largest = fmaxf(largest, most); else st.bad = true;
 
     if (b == next) {  // 0, 2, 8, 32, ...
       next = max(2, kAgain * next);
@@ -350,57 +372,42 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) lo
         if (bin > 0 && per > 0.0f) l = fmaxf(l, fmaf((float)bin - 0.01f, 1.0f / per, l));
         if (l > last_v) {
           last_v = look = l;
-          last_id = 0x7fffffff;
           if (fmaf(l - st.C, L, -st.R) > kSlack) st.refer(l, L);
         }
       }
     }
 
-    uint32_t lanes = __ballot_sync(0xffffffffu, !(most < look) && most != -INFINITY);
+    uint32_t lanes = __ballot_sync(0xffffffffu, most >= look);
     if (lanes) {
-      const int begin = lo + b * kThreads * kUnroll + warp * 32;
       __syncwarp();  // the lanes' copies
+      const int base = (lo + b * kThreads * kUnroll + warp * 32) * V - ahead;
 #pragma unroll 1
-      while (lanes) {  // a lane's vectors, their values one a lane
+      do {  // a lane's vectors, 32 of their values one a lane
         const int src = __ffs(lanes) - 1;
         lanes &= lanes - 1;
-        const int u = min(lane / V, kUnroll - 1);
-        T* p = reinterpret_cast<T*>(slot(b, u) - lane + src) + lane % V;
-        const int id = (begin + src + u * kThreads) * V - ahead + lane % V;
-        const float v = lane < kUnroll * V ? to_f32(*p) : -INFINITY;
-        if (!(v < INFINITY)) st.bad = true;
-        uint32_t who = __ballot_sync(0xffffffffu, v > -INFINITY && before(v, id, last_v, last_id));
-#pragma unroll 1
-        while (who) {
-          const int j = __ffs(who) - 1;
-          who &= who - 1;
-          const float c = __shfl_sync(0xffffffffu, v, j);
-          const int ci = __shfl_sync(0xffffffffu, id, j);
-          const int at = __popc(__ballot_sync(0xffffffffu, before(st.v, st.id, c, ci)));
-          if (at >= live) continue;
-          const float uv = __shfl_up_sync(0xffffffffu, st.v, 1);
-          const int ui = __shfl_up_sync(0xffffffffu, st.id, 1);
-          const float out = lane == live - 1 ? st.v : -INFINITY;
-          if (lane >= at && lane < live) {
-            st.v = lane == at ? c : uv;
-            st.id = lane == at ? ci : ui;
-          }
-          if (lane == j) *p = from_f32<T>(-INFINITY);
-          const float lv = __shfl_sync(0xffffffffu, st.v, live - 1);
-          const int li = __shfl_sync(0xffffffffu, st.id, live - 1);
-          if (before(lv, li, last_v, last_id)) {
-            last_v = lv;
-            last_id = li;
-            // the ids of later batches are higher, so equal values come too late
-            look = lv == 0.0f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(lv) + (lv > 0.0f ? 1 : -1));
-            if (fmaf(lv - st.C, L, -st.R) > kSlack) st.refer(lv, L);
-          }
-          if (out > -INFINITY) st.add(out, L);
-        }
-      }
-      __syncwarp();
+        T* p = reinterpret_cast<T*>(mine + src - lane + lane / V * kThreads) + lane % V;
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) raw[u] = *slot(b, u);
+        for (int g = 0; g < kUnroll * V; g += 32, p += 32 * kThreads) {
+          const float v = kUnroll * V >= 32 || lane < kUnroll * V ? to_f32(*p) : -INFINITY;
+          uint32_t who = __ballot_sync(0xffffffffu, v >= last_v && v < INFINITY);
+#pragma unroll 1
+          while (who) {
+            const int j = __ffs(who) - 1;
+            who &= who - 1;
+            const float c = __shfl_sync(0xffffffffu, v, j);
+            if (lane == waiting) {
+              wait_v = c;
+              wait_id = base + ((g + j) / V * kThreads + src) * V + j % V;
+            }
+            if (lane == j) *p = from_f32<T>(-INFINITY);
+            if (++waiting == 32) {
+              settle();
+              who &= __ballot_sync(0xffffffffu, v >= last_v);
+            }
+          }
+        }
+      } while (lanes);
+      __syncwarp();
     }
 
     if (st.R == -INFINITY) continue;  // all there was is in the list
@@ -410,15 +417,16 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) lo
     if (st.C == 0.0f && fmaf(to_f32(least), L, -st.R) <= -150.0f) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
+        const uint4 raw = mine[u * kThreads];
         float v[V];
         if constexpr (sizeof(T) == 4) {
-          unpack16<T>(raw[u], v);
+          unpack16<T>(raw, v);
 #pragma unroll
           for (int i = 0; i < V; ++i) v[i] = fmaxf(v[i], least);
         } else {
           Pair<T> both;
           both.x = both.y = least;
-          uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const Pair<T> p = __hmax2(*reinterpret_cast<Pair<T>*>(&w[i]), both);
@@ -428,20 +436,21 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) lo
         }
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-          const float2 y = fma2(make_float2(v[i], v[i + 1]), L2, R2);
+          const float2 y = __ffma2_rn(make_float2(v[i], v[i + 1]), L2, R2);
           const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          st.s2 = add2(st.s2, e);
-          st.t2 = fma2(e, y, st.t2);
+          st.s2 = __fadd2_rn(st.s2, e);
+          st.t2 = __ffma2_rn(e, y, st.t2);
         }
       }
     } else {  // logits so large, or a scale so small, that the type has no such value
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll 1
-        for (int i = 0; i < V; ++i) st.add(to_f32(reinterpret_cast<const T*>(slot(b, u))[i]), L);
+        for (int i = 0; i < V; ++i) st.add(to_f32(reinterpret_cast<const T*>(mine + u * kThreads)[i]), L);
     }
   }
 
+  settle();
   merge_warps(st, parts, kWarps, live, warp, lane, L);
   if (cluster > 1) {
     __syncthreads();
@@ -509,9 +518,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps >= 8 ? 32 / kWarps : 1) lo
   }
 }
 
-template <typename T, int kWarps>
+template <typename T, int kWarps, int kUnroll>
 static int launch_rows(const TokenLogprobs& a, int cluster, cudaStream_t stream) {
-  auto kern = logprobs_kernel<T, kWarps>;
+  auto kern = logprobs_kernel<T, kWarps, kUnroll>;
   const int smem = kStages * kUnroll * 32 * kWarps * 16;
   static int per_device[64];  // whether the kernel has its attributes there
   int dev = 0;
@@ -542,13 +551,12 @@ int launch_token_logprobs(const TokenLogprobs& a, int dtype, cudaStream_t stream
   return with_dtype(dtype, [&](auto v) {
     using T = decltype(v);
     const int vectors = (a.vocab + 2 * kVec<T> - 1) / kVec<T>;
-    if (vectors <= 32 * 2 * kUnroll) return launch_rows<T, 1>(a, 1, stream);
-    if (vectors <= 128 * 2 * kUnroll) return launch_rows<T, 4>(a, 1, stream);
-    if (a.rows > 304) return launch_rows<T, 8>(a, 1, stream);
+    if (vectors <= 32 * 8) return launch_rows<T, 1, 4>(a, 1, stream);
+    if (vectors <= 128 * 8 || a.rows > 2 * 152) return launch_rows<T, 4, 8>(a, 1, stream);
     // As many CTAs to a row as still have a batch of vectors each, up to two CTAs an SM in all.
     int cluster = 1;
-    while (cluster < 16 && (int64_t)a.rows * cluster * 2 <= 2 * 152 && vectors >= 2 * cluster * 512 * kUnroll / 2) cluster *= 2;
-    return launch_rows<T, 16>(a, cluster, stream);
+    while (cluster < 16 && (int64_t)a.rows * cluster * 2 <= 2 * 152 && vectors >= cluster * 512 * 4) cluster *= 2;
+    return launch_rows<T, 16, 4>(a, cluster, stream);
   });
 }
 
