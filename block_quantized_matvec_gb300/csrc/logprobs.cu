@@ -244,6 +244,8 @@ __device__ __forceinline__ void merge_warps(RowState& st, RowPart* parts, int n,
 template <typename T, int kWarps, int kUnroll>  // kUnroll: 16-byte vectors of a thread in a batch
 __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 7 : 1) logprobs_kernel(const TokenLogprobs a, int cluster) {
   constexpr int V = kVec<T>, kThreads = 32 * kWarps;
+  // a lane's values are looked at 32 at a time, or all at once where they are fewer
+  static_assert(kUnroll * V % 32 == 0 || kUnroll * V < 32);
   __shared__ RowPart parts[kWarps];
   __shared__ float2 ends[kWarps];
   __shared__ float said[2];

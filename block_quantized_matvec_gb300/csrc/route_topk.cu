@@ -8,13 +8,17 @@
 //
 // Which expert comes first is decided as in 64 bits.  Without bias and groups
 // the logits' own order decides, exactly.  Otherwise values are made in fp32,
-// whose error is at most kUlps half units of the score and of the sum; where
-// two neighbours in the order (or the last group in and the first one out) lie
-// nearer to one another than that, the warp makes the values that can matter
-// again in 64 bits and chooses by those.
+// whose error is at most kUlps of the score and of the sum; where two neighbours
+// in the order (or the last group in and the first one out) lie nearer to one
+// another than that, the warp makes the values that can matter again in 64 bits
+// and chooses by those.
 //
 // A warp per token; lane L holds the experts L * kPer .. + kPer - 1, so a lower
-// lane means a lower id.
+// lane means a lower id.  Bound by instructions, not by the few bytes: up to 8
+// experts of a lane are sorted once (28 exchanges of neighbours, which leave
+// equal values in order), so that each of the k rounds is a maximum over the
+// lanes' first ones and a shift in the lane that had it; more of them are
+// searched anew in every round, which then costs no more than the sorting would.
 #include "layer.cuh"
 #include "typed.cuh"
 
@@ -22,59 +26,91 @@ namespace mmvq {
 
 constexpr int kRouteWarps = 4;
 
-// sigmoid(x) times exp(-c) where c = min(top, 0): the largest of several stays
-// at a half or above however small they all are.
+// sigmoid(x)
+__device__ __forceinline__ float sigmoid(float x) {
+  const float t = expf(-fabsf(x)), r = __fdividef(1.0f, 1.0f + t);
+  return x >= 0.0f ? r : t * r;
+}
+// sigmoid(x) over exp(c), c = min(top, 0): the largest of several stays at a half or
+// above however small they all are.
 __device__ __forceinline__ float sigmoid_over(float x, float c) {
   return expf(fminf(x, 0.0f) - c) / (1.0f + expf(-fabsf(x)));
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+// What the choice in 64 bits needs: places for the experts' values and for a list of ids.
+struct WideScratch {
+  double* value;  // [n_experts] of this warp
+  int* list;      // [32]
+};
 
 template <typename T, int kPer>
 struct RouteRow {
   const RouteTopk& a;
   const T* x;
   int lane, group_size;
-  double* wide;  // [n_experts] of this warp
   float top, total;  // softmax: the largest logit and the sum of exp(x - top)
 
   __device__ __forceinline__ int expert(int i) const { return lane * kPer + i; }
-  __device__ __forceinline__ bool finite(float v) const { return fabsf(v) < INFINITY; }
   __device__ __forceinline__ float score(float v) const {
-    return a.sigmoid ? sigmoid_over(v, 0.0f) : expf(v - top) / total;
+    return a.sigmoid ? sigmoid(v) : __fdividef(expf(v - top), total);
+  }
+  // The value in 64 bits; z: the softmax's sum (any positive number where only the order counts).
+  __device__ __forceinline__ double wide(int e, double z) const {
+    const double l = (double)to_f32(x[e]);
+    const double d = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
+    return a.bias ? d + (double)a.bias[e] : d;
   }
 
-  // In 64 bits: values of experts of kept groups that are at least `cut` in fp32 (all where cut is -inf), the
-  // groups chosen again where `groups` says so; then the k best.  Lane j leaves with the id of choice j, or -1.
-  __device__ __noinline__ int choose_wide(uint32_t keep, float cut, bool groups, const float (&v)[kPer]) {
-    double z = 0.0;
-    if (!a.sigmoid) {
+  // The choice in 64 bits among the experts with may[i] >= cut, the groups chosen again where
+  // `groups` says so.  Lane j leaves with the id of choice j, or -1.
+  __device__ __noinline__ int choose_wide(const float* may, float cut, bool groups, WideScratch w) {
+    double z = 1.0;
+    if (!a.sigmoid && a.bias) {
+      z = 0.0;
       for (int i = 0; i < kPer; ++i) {
         const float l = expert(i) < a.n_experts ? to_f32(x[expert(i)]) : INFINITY;
-        if (finite(l)) z += exp((double)l - (double)top);
+        if (fabsf(l) < INFINITY) z += exp((double)l - (double)top);
       }
-      for (int o = 16; o; o >>= 1) z += shfl_xor_f64(z, o);
+      for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    }
+    if (!groups) {  // mostly a few: one a lane, ranked by comparing all with all
+      int n = 0;
+      for (int i = 0; i < kPer; ++i) {
+        const bool in = may[i] > -INFINITY && may[i] >= cut;
+        const uint32_t m = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(m & ((1u << lane) - 1u));
+        if (in && at < 32) w.list[at] = expert(i);
+        n += __popc(m);
+      }
+      __syncwarp();
+      if (n <= 32) {
+        const int id = lane < n ? w.list[lane] : 0x7fffffff;
+        const double d = lane < n ? wide(id, z) : 0.0;
+        int rank = 0;
+        for (int s = 0; s < n; ++s) {
+          const double o = __shfl_sync(0xffffffffu, d, s);
+          const int oi = __shfl_sync(0xffffffffu, id, s);
+          rank += o > d || (o == d && oi < id);
+        }
+        __syncwarp();
+        if (lane < n) w.list[rank] = id;
+        __syncwarp();
+        return lane < min(n, a.k) ? w.list[lane] : -1;
+      }
     }
     const double minus = -(double)INFINITY;
-#pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
       const int e = expert(i);
-      if (e >= a.n_experts) break;
-      const float l = to_f32(x[e]);
-      double d = minus;
-      if (finite(l) && (groups || ((keep >> (e / group_size)) & 1)) && v[i] >= cut) {
-        d = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / z;
-        if (a.bias) d += (double)a.bias[e];
-      }
-      wide[e] = d;
+      if (e < a.n_experts) w.value[e] = may[i] > -INFINITY && may[i] >= cut ? wide(e, z) : minus;
     }
     __syncwarp();
+    uint32_t keep = 0xffffffffu;
     if (groups) {
       double two = minus;
       if (lane < a.n_groups) {
         double b1 = minus, b2 = minus;
         for (int e = lane * group_size; e < (lane + 1) * group_size; ++e) {
-          const double d = wide[e];
+          const double d = w.value[e];
           if (d > b1) { b2 = b1; b1 = d; } else if (d > b2) { b2 = d; }
         }
         two = b2 == minus ? b1 : b1 + b2;
@@ -92,16 +128,16 @@ struct RouteRow {
       int id = 0x7fffffff;
       for (int i = 0; i < kPer; ++i) {
         const int e = expert(i);
-        if (e < a.n_experts && ((keep >> (e / group_size)) & 1) && wide[e] > b) { b = wide[e]; id = e; }
+        if (e < a.n_experts && (!groups || ((keep >> (e / group_size)) & 1)) && w.value[e] > b) { b = w.value[e]; id = e; }
       }
       for (int o = 16; o; o >>= 1) {
-        const double ob = shfl_xor_f64(b, o);
+        const double ob = __shfl_xor_sync(0xffffffffu, b, o);
         const int oi = __shfl_xor_sync(0xffffffffu, id, o);
         if (ob > b || (ob == b && oi < id)) { b = ob; id = oi; }
       }
       if (b == minus) break;
       if (lane == j) mine = id;
-      if (id / kPer == lane) wide[id] = minus;
+      if (id / kPer == lane) w.value[id] = minus;
       __syncwarp();
     }
     return mine;
@@ -111,24 +147,36 @@ struct RouteRow {
 template <typename T, int kPer>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const RouteTopk a) {
   extern __shared__ double wide_all[];
+  __shared__ int list[kRouteWarps][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
   if (t >= a.n_tokens) return;
-  RouteRow<T, kPer> r{a, static_cast<const T*>(a.logits) + t * a.ld, lane, a.n_experts / a.n_groups, wide_all + warp * a.n_experts, 0.0f, 1.0f};
+  RouteRow<T, kPer> r{a, static_cast<const T*>(a.logits) + t * a.ld, lane, a.n_experts / a.n_groups, 0.0f, 1.0f};
   const bool grouped = a.top_groups < a.n_groups;
   const bool exact = !a.bias && !grouped;  // the logits' order is the scores'
-  // half units that a value's fp32 error stays within: exp, sum, quotient and the sum with the bias
+  // what a value's fp32 error stays within: exp, sum, quotient and the sum with the bias
   constexpr float kUlps = (kPer + 24) * 0x1p-24f;
 
-  float x[kPer], v[kPer];
+  float x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = -INFINITY;
+  constexpr int kBytes = kPer * (int)sizeof(T);
+  if (kBytes >= 16 && (lane + 1) * kPer <= a.n_experts && reinterpret_cast<uintptr_t>(r.x) % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += kVec<T>) {
+      if constexpr (kBytes >= 16) unpack16<T>(ldg_nc_v4(r.x + r.expert(i)), x + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (r.expert(i) < a.n_experts) x[i] = to_f32(r.x[r.expert(i)]);
+  }
   float top = -INFINITY;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    x[i] = -INFINITY;
-    if (r.expert(i) < a.n_experts) x[i] = to_f32(r.x[r.expert(i)]);
     if (!(x[i] < INFINITY)) {  // NaN or +inf
       bad = true;
       x[i] = -INFINITY;
@@ -136,16 +184,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     top = fmaxf(top, x[i]);
   }
   if (bad && a.status) *a.status = MMVQ_ERR_VALUE;
-  top = warp_max(top);
-  r.top = top == -INFINITY ? 0.0f : top;
   if (!a.sigmoid) {
+    top = warp_max(top);
+    r.top = top == -INFINITY ? 0.0f : top;
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) z += expf(x[i] - r.top);
     r.total = warp_sum(z);
   }
-  uint32_t keep = 0xffffffffu;
-  bool groups_near = false;  // two groups are too near to tell
+  float v[kPer];
   if (exact) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = x[i];
@@ -156,79 +203,119 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
       if (x[i] > -INFINITY) v[i] = r.score(x[i]) + (a.bias ? a.bias[r.expert(i)] : 0.0f);
     }
   }
-  if (grouped) {
-    // lane g's group: its two best, one after another
-    float two = -INFINITY, size = 0.0f;
-    for (int g = 0; g < a.n_groups; ++g) {
-      float b[2];
-      int skip = -1;
-      for (int n = 0; n < 2; ++n) {
-        float m = -INFINITY;
-        int id = -1;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int e = r.expert(i);
-          if (e / r.group_size == g && e != skip && v[i] > m) { m = v[i]; id = e; }
-        }
-        b[n] = warp_max(m);
-        const uint32_t who = __ballot_sync(0xffffffffu, m == b[n] && id >= 0);
-        skip = who ? __shfl_sync(0xffffffffu, id, __ffs(who) - 1) : -1;
-      }
-      if (lane == g) {
-        two = b[1] == -INFINITY ? b[0] : b[0] + b[1];
-        // scores are at most 1 and the value less the bias: an error of both values and of their sum
-        size = b[0] == -INFINITY ? 0.0f : 3.0f + fabsf(b[0]) + (b[1] == -INFINITY ? 0.0f : fabsf(b[1]));
-      }
-    }
-    int rank = 0;
-    float out = -INFINITY, in = INFINITY, most = 0.0f;
-    for (int g = 0; g < a.n_groups; ++g) {
-      const float other = __shfl_sync(0xffffffffu, two, g);
-      rank += other > two || (other == two && g < lane);
-    }
-    const bool kept = lane < a.n_groups && rank < a.top_groups;
-    keep = __ballot_sync(0xffffffffu, kept);
-    if (kept) in = two;
-    if (lane < a.n_groups && !kept) out = two;
-    in = -warp_max(-in);
-    out = warp_max(out);
-    most = warp_max(size);
-    groups_near = out > -INFINITY && in - out <= 2.0f * kUlps * most;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (r.expert(i) < a.n_experts && !((keep >> (r.expert(i) / r.group_size)) & 1)) v[i] = -INFINITY;
-  }
 
-  // k rounds of the best of all lanes; lane j keeps choice j, every lane the one after the last
-  int mine = -1;
-  float mv = -INFINITY, nv = -INFINITY;
-  int next = -1;
-  float left[kPer];
+  bool groups_near = false;  // two groups are too near to tell
+  if (grouped) {
+    const int lanes = r.group_size / kPer;  // of a group, where it has whole ones
+    const bool whole = lanes * kPer == r.group_size;
+    // my lane's group (lane g's, where groups have no lanes of their own): its two best
+    float b1 = -INFINITY, b2 = -INFINITY;
+    int group = lane;
+    if (whole) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) left[i] = v[i];
-  for (int j = 0; j <= a.k; ++j) {
-    float m = -INFINITY;
-    int at = 0;
+      for (int i = 0; i < kPer; ++i) {
+        b2 = fmaxf(b2, fminf(b1, v[i]));
+        b1 = fmaxf(b1, v[i]);
+      }
+      group = lane / lanes;
+      const int begin = group * lanes;
+      const float m1 = b1, m2 = b2;
+      for (int s = 1; s < lanes; ++s) {
+        const int from = begin + (lane - begin + s) % lanes;
+        const float o1 = __shfl_sync(0xffffffffu, m1, from), o2 = __shfl_sync(0xffffffffu, m2, from);
+        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+        b1 = fmaxf(b1, o1);
+      }
+    } else {
+      for (int g = 0; g < a.n_groups; ++g) {
+        float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (left[i] > m) { m = left[i]; at = i; }
-    const float b = warp_max(m);
-    if (b == -INFINITY) break;
-    const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
-    const int id = __shfl_sync(0xffffffffu, r.expert(at), who);
-    if (j == a.k) {
-      nv = b;
-      next = id;
-      break;
+        for (int i = 0; i < kPer; ++i)
+          if (r.expert(i) / r.group_size == g) {
+            m2 = fmaxf(m2, fminf(m1, v[i]));
+            m1 = fmaxf(m1, v[i]);
+          }
+        const float best = warp_max(m1);
+        // the best of one lane only: of what the others and its second have left
+        const uint32_t who = __ballot_sync(0xffffffffu, m1 == best);
+        const float second = warp_max(lane == __ffs(who) - 1 ? m2 : m1);
+        if (lane == g) b1 = best, b2 = second;
+      }
     }
-    if (lane == j) {
-      mine = id;
-      mv = b;
+    const bool real = group < a.n_groups;
+    const float two = b2 == -INFINITY ? b1 : b1 + b2;
+    // scores are at most 1: an error of both values and of their sum
+    const float size = b1 == -INFINITY || !real ? 0.0f : 3.0f + fabsf(b1) + (b2 == -INFINITY ? 0.0f : fabsf(b2));
+    int rank = 0;
+    for (int g = 0; g < a.n_groups; ++g) {
+      const float other = __shfl_sync(0xffffffffu, two, whole ? g * lanes : g);
+      rank += other > two || (other == two && g < group);
     }
-    if (lane == who) {
+    const bool kept = real && rank < a.top_groups;
+    const float in = -warp_max(kept ? -two : -INFINITY), out = warp_max(real && !kept ? two : -INFINITY);
+    groups_near = out > -INFINITY && in - out <= 2.0f * kUlps * warp_max(size);
+    if (!groups_near) {
+      const uint32_t keep = __ballot_sync(0xffffffffu, kept && !whole);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (i == at) left[i] = -INFINITY;
+        if (whole ? !kept : r.expert(i) < a.n_experts && !((keep >> (r.expert(i) / r.group_size)) & 1)) v[i] = -INFINITY;
+    }
+  }
+
+  // k rounds of the best of all lanes, once more for the one after the last; lane j keeps choice j
+  int mine = -1, next = -1;
+  float mv = -INFINITY, nv = -INFINITY;
+  if (!groups_near) {
+    float left[kPer];
+    int slot[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) left[i] = v[i], slot[i] = i;
+    constexpr bool kSorted = kPer <= 8;
+    if constexpr (kSorted) {
+#pragma unroll
+      for (int n = 0; n < kPer; ++n)
+#pragma unroll
+        for (int i = n & 1; i + 1 < kPer; i += 2) {
+          const bool swap = left[i + 1] > left[i];
+          const float hi = fmaxf(left[i], left[i + 1]), lo = fminf(left[i], left[i + 1]);
+          const int s = slot[i];
+          left[i] = hi, left[i + 1] = lo;
+          slot[i] = swap ? slot[i + 1] : s;
+          slot[i + 1] = swap ? s : slot[i + 1];
+        }
+    }
+    const int rounds = exact ? a.k : a.k + 1;
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) {
+      float m = left[0];
+      int at = slot[0];
+      if constexpr (!kSorted) {
+#pragma unroll
+        for (int i = 1; i < kPer; ++i)
+          if (left[i] > m) m = left[i], at = i;
+      }
+      const float b = warp_max(m);
+      if (b == -INFINITY) break;
+      const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
+      const int id = __shfl_sync(0xffffffffu, r.expert(at), who);
+      if (j == a.k) {
+        nv = b;
+        next = id;
+      } else if (lane == j) {
+        mine = id;
+        mv = b;
+      }
+      if (lane == who) {
+        if constexpr (kSorted) {
+#pragma unroll
+          for (int i = 0; i + 1 < kPer; ++i) left[i] = left[i + 1], slot[i] = slot[i + 1];
+          left[kPer - 1] = -INFINITY;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (i == at) left[i] = -INFINITY;
+        }
+      }
     }
   }
   float mx = mine >= 0 ? to_f32(r.x[mine]) : -INFINITY;
@@ -238,21 +325,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const float v1 = lane == a.k - 1 ? nv : fv;
     const int i1 = lane == a.k - 1 ? next : fi;
     bool close = false;
-    float slack = 0.0f;
     if (mine >= 0 && i1 >= 0) {
       const float x1 = to_f32(r.x[i1]), b0 = a.bias ? a.bias[mine] : 0.0f, b1 = a.bias ? a.bias[i1] : 0.0f;
-      slack = kUlps * (r.score(mx) + fabsf(mv) + r.score(x1) + fabsf(v1)) + 0x1p-120f;
+      const float slack = kUlps * (r.score(mx) + fabsf(mv) + r.score(x1) + fabsf(v1)) + 0x1p-120f;
       close = mv - v1 <= slack && !(mx == x1 && b0 == b1);
     }
     if (__any_sync(0xffffffffu, close) || groups_near) {
       // what can still be among the k: everything within the errors of the last choice
-      const float last = __shfl_sync(0xffffffffu, mine >= 0 ? mv : -INFINITY, a.k - 1);
+      const float last = __shfl_sync(0xffffffffu, mv, a.k - 1);
       float cut = last - 2.0f * kUlps * (2.0f + 2.0f * fabsf(last));
       if (groups_near || !(cut < INFINITY)) cut = -INFINITY;  // also where a bias is infinite
+      float may[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (groups_near && x[i] > -INFINITY) v[i] = 0.0f;  // all of them
-      mine = r.choose_wide(keep, cut, groups_near, v);
+      for (int i = 0; i < kPer; ++i) may[i] = v[i];
+      mine = r.choose_wide(may, cut, groups_near, WideScratch{wide_all + warp * a.n_experts, list[warp]});
       mx = mine >= 0 ? to_f32(r.x[mine]) : -INFINITY;
     }
   }
@@ -264,7 +350,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const float sum = warp_sum(w);
     if (mine >= 0) w = w / sum * a.scale;
   } else if (mine >= 0) {
-    w = r.score(mx) * a.scale;
+    w = (a.sigmoid ? sigmoid_over(mx, 0.0f) : expf(mx - r.top) / r.total) * a.scale;
   }
   if (lane < a.k) {
     a.topk[t * a.k + lane] = mine;
