@@ -43,109 +43,108 @@ struct WideScratch {
   int* list;      // [32]
 };
 
-template <typename T, int kPer>
+// A token's logits and what its scores need.
 struct RouteRow {
-  const RouteTopk& a;
-  const T* x;
+  const void* x;
   int lane, group_size;
   float top, total;  // softmax: the largest logit and the sum of exp(x - top)
-
-  __device__ __forceinline__ int expert(int i) const { return lane * kPer + i; }
-  __device__ __forceinline__ float score(float v) const {
-    return a.sigmoid ? sigmoid(v) : __fdividef(expf(v - top), total);
-  }
-  // The value in 64 bits; z: the softmax's sum (any positive number where only the order counts).
-  __device__ __forceinline__ double wide(int e, double z) const {
-    const double l = (double)to_f32(x[e]);
-    const double d = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
-    return a.bias ? d + (double)a.bias[e] : d;
-  }
-
-  // The choice in 64 bits among the experts with may[i] >= cut, the groups chosen again where
-  // `groups` says so.  Lane j leaves with the id of choice j, or -1.
-  __device__ __noinline__ int choose_wide(const float* may, float cut, bool groups, WideScratch w) {
-    double z = 1.0;
-    if (!a.sigmoid && a.bias) {
-      z = 0.0;
-      for (int i = 0; i < kPer; ++i) {
-        const float l = expert(i) < a.n_experts ? to_f32(x[expert(i)]) : INFINITY;
-        if (fabsf(l) < INFINITY) z += exp((double)l - (double)top);
-      }
-      for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    }
-    if (!groups) {  // mostly a few: one a lane, ranked by comparing all with all
-      int n = 0;
-      for (int i = 0; i < kPer; ++i) {
-        const bool in = may[i] > -INFINITY && may[i] >= cut;
-        const uint32_t m = __ballot_sync(0xffffffffu, in);
-        const int at = n + __popc(m & ((1u << lane) - 1u));
-        if (in && at < 32) w.list[at] = expert(i);
-        n += __popc(m);
-      }
-      __syncwarp();
-      if (n <= 32) {
-        const int id = lane < n ? w.list[lane] : 0x7fffffff;
-        const double d = lane < n ? wide(id, z) : 0.0;
-        int rank = 0;
-        for (int s = 0; s < n; ++s) {
-          const double o = __shfl_sync(0xffffffffu, d, s);
-          const int oi = __shfl_sync(0xffffffffu, id, s);
-          rank += o > d || (o == d && oi < id);
-        }
-        __syncwarp();
-        if (lane < n) w.list[rank] = id;
-        __syncwarp();
-        return lane < min(n, a.k) ? w.list[lane] : -1;
-      }
-    }
-    const double minus = -(double)INFINITY;
-    for (int i = 0; i < kPer; ++i) {
-      const int e = expert(i);
-      if (e < a.n_experts) w.value[e] = may[i] > -INFINITY && may[i] >= cut ? wide(e, z) : minus;
-    }
-    __syncwarp();
-    uint32_t keep = 0xffffffffu;
-    if (groups) {
-      double two = minus;
-      if (lane < a.n_groups) {
-        double b1 = minus, b2 = minus;
-        for (int e = lane * group_size; e < (lane + 1) * group_size; ++e) {
-          const double d = w.value[e];
-          if (d > b1) { b2 = b1; b1 = d; } else if (d > b2) { b2 = d; }
-        }
-        two = b2 == minus ? b1 : b1 + b2;
-      }
-      int rank = 0;
-      for (int g = 0; g < a.n_groups; ++g) {
-        const double other = __shfl_sync(0xffffffffu, two, g);
-        rank += other > two || (other == two && g < lane);
-      }
-      keep = __ballot_sync(0xffffffffu, lane < a.n_groups && rank < a.top_groups);
-    }
-    int mine = -1;
-    for (int j = 0; j < a.k; ++j) {
-      double b = minus;
-      int id = 0x7fffffff;
-      for (int i = 0; i < kPer; ++i) {
-        const int e = expert(i);
-        if (e < a.n_experts && (!groups || ((keep >> (e / group_size)) & 1)) && w.value[e] > b) { b = w.value[e]; id = e; }
-      }
-      for (int o = 16; o; o >>= 1) {
-        const double ob = __shfl_xor_sync(0xffffffffu, b, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, id, o);
-        if (ob > b || (ob == b && oi < id)) { b = ob; id = oi; }
-      }
-      if (b == minus) break;
-      if (lane == j) mine = id;
-      if (id / kPer == lane) w.value[id] = minus;
-      __syncwarp();
-    }
-    return mine;
-  }
 };
 
+// The value in 64 bits; z: the softmax's sum (any positive number where only the order counts).
+template <typename T>
+__device__ __forceinline__ double wide_value(const RouteTopk& a, const RouteRow& r, int e, double z) {
+  const double l = (double)to_f32(static_cast<const T*>(r.x)[e]);
+  const double d = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)r.top) / z;
+  return a.bias ? d + (double)a.bias[e] : d;
+}
+
+// The choice in 64 bits among the experts with may[i] >= cut, the groups chosen again where
+// `groups` says so.  Lane j leaves with the id of choice j, or -1.
 template <typename T, int kPer>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const RouteTopk a) {
+__device__ __noinline__ int choose_wide(const RouteTopk& a, const RouteRow r, const float* may, float cut, bool groups, WideScratch w) {
+  const T* x = static_cast<const T*>(r.x);
+  const int lane = r.lane, group_size = r.group_size;
+  double z = 1.0;
+  if (!a.sigmoid && a.bias) {
+    z = 0.0;
+    for (int i = 0; i < kPer; ++i) {
+      const float l = (lane * kPer + i) < a.n_experts ? to_f32(x[(lane * kPer + i)]) : INFINITY;
+      if (fabsf(l) < INFINITY) z += exp((double)l - (double)r.top);
+    }
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  if (!groups) {  // mostly a few: one a lane, ranked by comparing all with all
+    int n = 0;
+    for (int i = 0; i < kPer; ++i) {
+      const bool in = may[i] > -INFINITY && may[i] >= cut;
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      const int at = n + __popc(m & ((1u << lane) - 1u));
+      if (in && at < 32) w.list[at] = (lane * kPer + i);
+      n += __popc(m);
+    }
+    __syncwarp();
+    if (n <= 32) {
+      const int id = lane < n ? w.list[lane] : 0x7fffffff;
+      const double d = lane < n ? wide_value<T>(a, r, id, z) : 0.0;
+      int rank = 0;
+      for (int s = 0; s < n; ++s) {
+        const double o = __shfl_sync(0xffffffffu, d, s);
+        const int oi = __shfl_sync(0xffffffffu, id, s);
+        rank += o > d || (o == d && oi < id);
+      }
+      __syncwarp();
+      if (lane < n) w.list[rank] = id;
+      __syncwarp();
+      return lane < min(n, a.k) ? w.list[lane] : -1;
+    }
+  }
+  const double minus = -(double)INFINITY;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = (lane * kPer + i);
+    if (e < a.n_experts) w.value[e] = may[i] > -INFINITY && may[i] >= cut ? wide_value<T>(a, r, e, z) : minus;
+  }
+  __syncwarp();
+  uint32_t keep = 0xffffffffu;
+  if (groups) {
+    double two = minus;
+    if (lane < a.n_groups) {
+      double b1 = minus, b2 = minus;
+      for (int e = lane * group_size; e < (lane + 1) * group_size; ++e) {
+        const double d = w.value[e];
+        if (d > b1) { b2 = b1; b1 = d; } else if (d > b2) { b2 = d; }
+      }
+      two = b2 == minus ? b1 : b1 + b2;
+    }
+    int rank = 0;
+    for (int g = 0; g < a.n_groups; ++g) {
+      const double other = __shfl_sync(0xffffffffu, two, g);
+      rank += other > two || (other == two && g < lane);
+    }
+    keep = __ballot_sync(0xffffffffu, lane < a.n_groups && rank < a.top_groups);
+  }
+  int mine = -1;
+  for (int j = 0; j < a.k; ++j) {
+    double b = minus;
+    int id = 0x7fffffff;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = (lane * kPer + i);
+      if (e < a.n_experts && (!groups || ((keep >> (e / group_size)) & 1)) && w.value[e] > b) { b = w.value[e]; id = e; }
+    }
+    for (int o = 16; o; o >>= 1) {
+      const double ob = __shfl_xor_sync(0xffffffffu, b, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, id, o);
+      if (ob > b || (ob == b && oi < id)) { b = ob; id = oi; }
+    }
+    if (b == minus) break;
+    if (lane == j) mine = id;
+    if (id / kPer == lane) w.value[id] = minus;
+    __syncwarp();
+  }
+  return mine;
+}
+
+template <typename T, int kPer>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __grid_constant__ RouteTopk a) {
   extern __shared__ double wide_all[];
   __shared__ int list[kRouteWarps][32];
   grid_dependency_wait();
@@ -153,7 +152,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
   if (t >= a.n_tokens) return;
-  RouteRow<T, kPer> r{a, static_cast<const T*>(a.logits) + t * a.ld, lane, a.n_experts / a.n_groups, 0.0f, 1.0f};
+  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+  const int group_size = a.n_experts / a.n_groups, first = lane * kPer;  // my first expert
+  float softmax_top = 0.0f, total = 1.0f;
+  auto score = [&](float l) { return a.sigmoid ? sigmoid(l) : __fdividef(expf(l - softmax_top), total); };
   const bool grouped = a.top_groups < a.n_groups;
   const bool exact = !a.bias && !grouped;  // the logits' order is the scores'
   // what a value's fp32 error stays within: exp, sum, quotient and the sum with the bias
@@ -163,15 +165,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
 #pragma unroll
   for (int i = 0; i < kPer; ++i) x[i] = -INFINITY;
   constexpr int kBytes = kPer * (int)sizeof(T);
-  if (kBytes >= 16 && (lane + 1) * kPer <= a.n_experts && reinterpret_cast<uintptr_t>(r.x) % 16 == 0) {
+  if (kBytes >= 16 && (lane + 1) * kPer <= a.n_experts && reinterpret_cast<uintptr_t>(row) % 16 == 0) {
 #pragma unroll
     for (int i = 0; i < kPer; i += kVec<T>) {
-      if constexpr (kBytes >= 16) unpack16<T>(ldg_nc_v4(r.x + r.expert(i)), x + i);
+      if constexpr (kBytes >= 16) unpack16<T>(ldg_nc_v4(row + (first + i)), x + i);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (r.expert(i) < a.n_experts) x[i] = to_f32(r.x[r.expert(i)]);
+      if ((first + i) < a.n_experts) x[i] = to_f32(row[(first + i)]);
   }
   float top = -INFINITY;
   bool bad = false;
@@ -186,11 +188,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
   if (bad && a.status) *a.status = MMVQ_ERR_VALUE;
   if (!a.sigmoid) {
     top = warp_max(top);
-    r.top = top == -INFINITY ? 0.0f : top;
+    softmax_top = top == -INFINITY ? 0.0f : top;
     float z = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) z += expf(x[i] - r.top);
-    r.total = warp_sum(z);
+    for (int i = 0; i < kPer; ++i) z += expf(x[i] - softmax_top);
+    total = warp_sum(z);
   }
   float v[kPer];
   if (exact) {
@@ -200,14 +202,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       v[i] = -INFINITY;
-      if (x[i] > -INFINITY) v[i] = r.score(x[i]) + (a.bias ? a.bias[r.expert(i)] : 0.0f);
+      if (x[i] > -INFINITY) v[i] = score(x[i]) + (a.bias ? a.bias[(first + i)] : 0.0f);
+      if (!(v[i] > -INFINITY)) v[i] = -INFINITY;  // a bias of NaN: fmaxf and fminf would lose it
     }
   }
 
   bool groups_near = false;  // two groups are too near to tell
   if (grouped) {
-    const int lanes = r.group_size / kPer;  // of a group, where it has whole ones
-    const bool whole = lanes * kPer == r.group_size;
+    const int lanes = group_size / kPer;  // of a group, where it has whole ones
+    const bool whole = lanes * kPer == group_size;
     // my lane's group (lane g's, where groups have no lanes of their own): its two best
     float b1 = -INFINITY, b2 = -INFINITY;
     int group = lane;
@@ -220,8 +223,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
       group = lane / lanes;
       const int begin = group * lanes;
       const float m1 = b1, m2 = b2;
+      int from = lane;
       for (int s = 1; s < lanes; ++s) {
-        const int from = begin + (lane - begin + s) % lanes;
+        from = from + 1 < begin + lanes ? from + 1 : begin;
         const float o1 = __shfl_sync(0xffffffffu, m1, from), o2 = __shfl_sync(0xffffffffu, m2, from);
         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
         b1 = fmaxf(b1, o1);
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
         float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (r.expert(i) / r.group_size == g) {
+          if ((uint32_t)(first + i - g * group_size) < (uint32_t)group_size) {
             m2 = fmaxf(m2, fminf(m1, v[i]));
             m1 = fmaxf(m1, v[i]);
           }
@@ -254,11 +258,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const bool kept = real && rank < a.top_groups;
     const float in = -warp_max(kept ? -two : -INFINITY), out = warp_max(real && !kept ? two : -INFINITY);
     groups_near = out > -INFINITY && in - out <= 2.0f * kUlps * warp_max(size);
-    if (!groups_near) {
-      const uint32_t keep = __ballot_sync(0xffffffffu, kept && !whole);
+    if (!groups_near && whole) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (whole ? !kept : r.expert(i) < a.n_experts && !((keep >> (r.expert(i) / r.group_size)) & 1)) v[i] = -INFINITY;
+        if (!kept) v[i] = -INFINITY;
+    } else if (!groups_near) {
+      const uint32_t keep = __ballot_sync(0xffffffffu, kept);
+      for (int i = 0, g = first / group_size, next_at = (g + 1) * group_size; i < kPer; ++i) {
+        if (first + i == next_at) ++g, next_at += group_size;
+        if (first + i < a.n_experts && !((keep >> g) & 1)) v[i] = -INFINITY;
+      }
     }
   }
 
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
       const float b = warp_max(m);
       if (b == -INFINITY) break;
       const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
-      const int id = __shfl_sync(0xffffffffu, r.expert(at), who);
+      const int id = __shfl_sync(0xffffffffu, first + at, who);
       if (j == a.k) {
         nv = b;
         next = id;
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
       }
     }
   }
-  float mx = mine >= 0 ? to_f32(r.x[mine]) : -INFINITY;
+  float mx = mine >= 0 ? to_f32(row[mine]) : -INFINITY;
   if (!exact) {
     const float fv = __shfl_down_sync(0xffffffffu, mv, 1);
     const int fi = __shfl_down_sync(0xffffffffu, mine, 1);
@@ -326,8 +335,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const int i1 = lane == a.k - 1 ? next : fi;
     bool close = false;
     if (mine >= 0 && i1 >= 0) {
-      const float x1 = to_f32(r.x[i1]), b0 = a.bias ? a.bias[mine] : 0.0f, b1 = a.bias ? a.bias[i1] : 0.0f;
-      const float slack = kUlps * (r.score(mx) + fabsf(mv) + r.score(x1) + fabsf(v1)) + 0x1p-120f;
+      const float x1 = to_f32(row[i1]), b0 = a.bias ? a.bias[mine] : 0.0f, b1 = a.bias ? a.bias[i1] : 0.0f;
+      const float slack = kUlps * (score(mx) + fabsf(mv) + score(x1) + fabsf(v1)) + 0x1p-120f;
       close = mv - v1 <= slack && !(mx == x1 && b0 == b1);
     }
     if (__any_sync(0xffffffffu, close) || groups_near) {
@@ -338,8 +347,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
       float may[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) may[i] = v[i];
-      mine = r.choose_wide(may, cut, groups_near, WideScratch{wide_all + warp * a.n_experts, list[warp]});
-      mx = mine >= 0 ? to_f32(r.x[mine]) : -INFINITY;
+      mine = choose_wide<T, kPer>(a, RouteRow{row, lane, group_size, softmax_top, total}, may, cut, groups_near, WideScratch{wide_all + warp * a.n_experts, list[warp]});
+      mx = mine >= 0 ? to_f32(row[mine]) : -INFINITY;
     }
   }
 
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const float sum = warp_sum(w);
     if (mine >= 0) w = w / sum * a.scale;
   } else if (mine >= 0) {
-    w = (a.sigmoid ? sigmoid_over(mx, 0.0f) : expf(mx - r.top) / r.total) * a.scale;
+    w = (a.sigmoid ? sigmoid_over(mx, 0.0f) : expf(mx - softmax_top) / total) * a.scale;
   }
   if (lane < a.k) {
     a.topk[t * a.k + lane] = mine;
