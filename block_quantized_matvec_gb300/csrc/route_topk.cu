@@ -37,11 +37,12 @@ __device__ __forceinline__ float sigmoid_over(float x, float c) {
   return expf(fminf(x, 0.0f) - c) / (1.0f + expf(-fabsf(x)));
 }
 
-// What the choice in 64 bits needs: places for the experts' values and for a list of ids.
+// What choices in 64 bits need, for each warp: places for the experts' values and a list of ids.
 struct WideScratch {
-  double* value;  // [n_experts] of this warp
-  int* list;      // [32]
+  double* value;   // [n_experts]
+  uint16_t* list;  // [n_experts]
 };
+constexpr int kWideBytes = sizeof(double) + sizeof(uint16_t);  // an expert
 
 // A token's logits and what its scores need.
 struct RouteRow {
@@ -58,86 +59,106 @@ __device__ __forceinline__ double wide_value(const RouteTopk& a, const RouteRow&
   return a.bias ? d + (double)a.bias[e] : d;
 }
 
-// The choice in 64 bits among the experts with may[i] >= cut, the groups chosen again where
-// `groups` says so.  Lane j leaves with the id of choice j, or -1.
+// The experts with may[i] >= cut[i] in w.list, in order, and their number.
+template <int kPer>
+__device__ __forceinline__ int list_wide(const float* may, const float* cut, int lane, WideScratch w) {
+  int n = 0;
+#pragma unroll 1
+  for (int i = 0; i < kPer; ++i) n += __popc(__ballot_sync(0xffffffffu, may[i] > -INFINITY && may[i] >= cut[i]));
+  // lane by lane: the ids before mine are those of lower lanes
+  int mine = 0;
+  for (int i = 0; i < kPer; ++i) mine += may[i] > -INFINITY && may[i] >= cut[i];
+  int at = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  at -= mine;
+  for (int i = 0; i < kPer; ++i)
+    if (may[i] > -INFINITY && may[i] >= cut[i]) w.list[at++] = (uint16_t)(lane * kPer + i);
+  __syncwarp();
+  return n;
+}
+
+// The softmax's sum in 64 bits, which the order depends on where there is a bias; else 1.
 template <typename T, int kPer>
-__device__ __noinline__ int choose_wide(const RouteTopk& a, const RouteRow r, const float* may, float cut, bool groups, WideScratch w) {
-  const T* x = static_cast<const T*>(r.x);
-  const int lane = r.lane, group_size = r.group_size;
-  double z = 1.0;
-  if (!a.sigmoid && a.bias) {
-    z = 0.0;
-    for (int i = 0; i < kPer; ++i) {
-      const float l = (lane * kPer + i) < a.n_experts ? to_f32(x[(lane * kPer + i)]) : INFINITY;
-      if (fabsf(l) < INFINITY) z += exp((double)l - (double)r.top);
-    }
-    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
-  if (!groups) {  // mostly a few: one a lane, ranked by comparing all with all
-    int n = 0;
-    for (int i = 0; i < kPer; ++i) {
-      const bool in = may[i] > -INFINITY && may[i] >= cut;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      const int at = n + __popc(m & ((1u << lane) - 1u));
-      if (in && at < 32) w.list[at] = (lane * kPer + i);
-      n += __popc(m);
-    }
-    __syncwarp();
-    if (n <= 32) {
-      const int id = lane < n ? w.list[lane] : 0x7fffffff;
-      const double d = lane < n ? wide_value<T>(a, r, id, z) : 0.0;
-      int rank = 0;
-      for (int s = 0; s < n; ++s) {
-        const double o = __shfl_sync(0xffffffffu, d, s);
-        const int oi = __shfl_sync(0xffffffffu, id, s);
-        rank += o > d || (o == d && oi < id);
-      }
-      __syncwarp();
-      if (lane < n) w.list[rank] = id;
-      __syncwarp();
-      return lane < min(n, a.k) ? w.list[lane] : -1;
-    }
-  }
-  const double minus = -(double)INFINITY;
+__device__ __forceinline__ double wide_total(const RouteTopk& a, const RouteRow& r) {
+  if (a.sigmoid || !a.bias) return 1.0;
+  double z = 0.0;
+#pragma unroll 4
   for (int i = 0; i < kPer; ++i) {
-    const int e = (lane * kPer + i);
-    if (e < a.n_experts) w.value[e] = may[i] > -INFINITY && may[i] >= cut ? wide_value<T>(a, r, e, z) : minus;
+    const int e = r.lane * kPer + i;
+    const float l = e < a.n_experts ? to_f32(static_cast<const T*>(r.x)[e]) : INFINITY;
+    if (fabsf(l) < INFINITY) z += exp((double)l - (double)r.top);
+  }
+  for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  return z;
+}
+
+// The groups that stay, decided in 64 bits: bit g of the result.  Of each group only what can be
+// among its two best is made again: what is at least cut (may: the values in fp32).
+template <typename T, int kPer>
+__device__ __noinline__ uint32_t groups_wide(const RouteTopk& a, const RouteRow r, const float* may, const float* cut, WideScratch w) {
+  const double z = wide_total<T, kPer>(a, r), minus = -(double)INFINITY;
+  const int n = list_wide<kPer>(may, cut, r.lane, w);
+  for (int c = r.lane; c < n; c += 32) w.value[c] = wide_value<T>(a, r, w.list[c], z);
+  __syncwarp();
+  double two = minus;
+  if (r.lane < a.n_groups) {
+    double b1 = minus, b2 = minus;
+    for (int c = 0; c < n; ++c) {
+      if (w.list[c] / r.group_size != r.lane) continue;
+      const double d = w.value[c];
+      if (d > b1) { b2 = b1; b1 = d; } else if (d > b2) { b2 = d; }
+    }
+    two = b2 == minus ? b1 : b1 + b2;
   }
   __syncwarp();
-  uint32_t keep = 0xffffffffu;
-  if (groups) {
-    double two = minus;
-    if (lane < a.n_groups) {
-      double b1 = minus, b2 = minus;
-      for (int e = lane * group_size; e < (lane + 1) * group_size; ++e) {
-        const double d = w.value[e];
-        if (d > b1) { b2 = b1; b1 = d; } else if (d > b2) { b2 = d; }
-      }
-      two = b2 == minus ? b1 : b1 + b2;
-    }
-    int rank = 0;
-    for (int g = 0; g < a.n_groups; ++g) {
-      const double other = __shfl_sync(0xffffffffu, two, g);
-      rank += other > two || (other == two && g < lane);
-    }
-    keep = __ballot_sync(0xffffffffu, lane < a.n_groups && rank < a.top_groups);
+  int rank = 0;
+  for (int g = 0; g < a.n_groups; ++g) {
+    const double other = __shfl_sync(0xffffffffu, two, g);
+    rank += other > two || (other == two && g < r.lane);
   }
+  return __ballot_sync(0xffffffffu, r.lane < a.n_groups && rank < a.top_groups);
+}
+
+// The choice in 64 bits among the experts with may[i] >= cut[i].  Lane j leaves with the id of
+// choice j, or -1.
+template <typename T, int kPer>
+__device__ __noinline__ int choose_wide(const RouteTopk& a, const RouteRow r, const float* may, const float* cut, WideScratch w) {
+  const double z = wide_total<T, kPer>(a, r), minus = -(double)INFINITY;
+  const int lane = r.lane, n = list_wide<kPer>(may, cut, lane, w);
+  if (n <= 32) {  // mostly: one a lane, ranked by comparing all with all
+    const int id = lane < n ? w.list[lane] : 0x7fffffff;
+    const double d = lane < n ? wide_value<T>(a, r, id, z) : 0.0;
+    int rank = 0;
+    for (int s = 0; s < n; ++s) {
+      const double o = __shfl_sync(0xffffffffu, d, s);
+      const int oi = __shfl_sync(0xffffffffu, id, s);
+      rank += o > d || (o == d && oi < id);
+    }
+    __syncwarp();
+    if (lane < n) w.list[rank] = (uint16_t)id;
+    __syncwarp();
+    return lane < min(n, a.k) ? w.list[lane] : -1;
+  }
+  for (int c = lane; c < n; c += 32) w.value[c] = wide_value<T>(a, r, w.list[c], z);
+  __syncwarp();
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
     double b = minus;
-    int id = 0x7fffffff;
-    for (int i = 0; i < kPer; ++i) {
-      const int e = (lane * kPer + i);
-      if (e < a.n_experts && (!groups || ((keep >> (e / group_size)) & 1)) && w.value[e] > b) { b = w.value[e]; id = e; }
-    }
+    int at = 0x7fffffff;
+    for (int c = lane; c < n; c += 32)
+      if (w.value[c] > b) { b = w.value[c]; at = c; }
     for (int o = 16; o; o >>= 1) {
       const double ob = __shfl_xor_sync(0xffffffffu, b, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, id, o);
-      if (ob > b || (ob == b && oi < id)) { b = ob; id = oi; }
+      const int oi = __shfl_xor_sync(0xffffffffu, at, o);
+      if (ob > b || (ob == b && oi < at)) { b = ob; at = oi; }
     }
     if (b == minus) break;
-    if (lane == j) mine = id;
-    if (id / kPer == lane) w.value[id] = minus;
+    if (lane == j) mine = w.list[at];
+    __syncwarp();
+    if (lane == 0) w.value[at] = minus;
     __syncwarp();
   }
   return mine;
@@ -145,8 +166,7 @@ __device__ __noinline__ int choose_wide(const RouteTopk& a, const RouteRow r, co
 
 template <typename T, int kPer>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __grid_constant__ RouteTopk a) {
-  extern __shared__ double wide_all[];
-  __shared__ int list[kRouteWarps][32];
+  extern __shared__ double wide_all[];  // WideScratch of each warp: all values, then all lists
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -207,7 +227,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
     }
   }
 
-  bool groups_near = false;  // two groups are too near to tell
+  const WideScratch scratch{wide_all + warp * a.n_experts, reinterpret_cast<uint16_t*>(wide_all + kRouteWarps * a.n_experts) + warp * a.n_experts};
   if (grouped) {
     const int lanes = group_size / kPer;  // of a group, where it has whole ones
     const bool whole = lanes * kPer == group_size;
@@ -257,13 +277,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
     }
     const bool kept = real && rank < a.top_groups;
     const float in = -warp_max(kept ? -two : -INFINITY), out = warp_max(real && !kept ? two : -INFINITY);
-    groups_near = out > -INFINITY && in - out <= 2.0f * kUlps * warp_max(size);
-    if (!groups_near && whole) {
+    uint32_t keep = __ballot_sync(0xffffffffu, kept);  // bit of a group's lanes, or of the group
+    if (out > -INFINITY && in - out <= 2.0f * kUlps * warp_max(size)) {  // too near to tell
+      float may[kPer], cut[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = first + i;
+        const float second = __shfl_sync(0xffffffffu, b2, whole ? lane : min(e / group_size, 31));
+        may[i] = v[i];
+        cut[i] = second - 2.0f * kUlps * (2.0f + 2.0f * fabsf(second));
+        if (!(cut[i] < INFINITY)) cut[i] = -INFINITY;  // fewer than two, or a bias that is infinite
+      }
+      keep = groups_wide<T, kPer>(a, RouteRow{row, lane, group_size, softmax_top, total}, may, cut, scratch);
+      if (whole) keep = __ballot_sync(0xffffffffu, real && ((keep >> group) & 1));
+    }
+    if (whole) {
+      const bool stays = (keep >> lane) & 1;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (!kept) v[i] = -INFINITY;
-    } else if (!groups_near) {
-      const uint32_t keep = __ballot_sync(0xffffffffu, kept);
+        if (!stays) v[i] = -INFINITY;
+    } else {
       for (int i = 0, g = first / group_size, next_at = (g + 1) * group_size; i < kPer; ++i) {
         if (first + i == next_at) ++g, next_at += group_size;
         if (first + i < a.n_experts && !((keep >> g) & 1)) v[i] = -INFINITY;
@@ -274,56 +307,54 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
   // k rounds of the best of all lanes, once more for the one after the last; lane j keeps choice j
   int mine = -1, next = -1;
   float mv = -INFINITY, nv = -INFINITY;
-  if (!groups_near) {
-    float left[kPer];
-    int slot[kPer];
+  float left[kPer];
+  int slot[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) left[i] = v[i], slot[i] = i;
-    constexpr bool kSorted = kPer <= 8;
-    if constexpr (kSorted) {
+  for (int i = 0; i < kPer; ++i) left[i] = v[i], slot[i] = i;
+  constexpr bool kSorted = kPer <= 8;
+  if constexpr (kSorted) {
 #pragma unroll
-      for (int n = 0; n < kPer; ++n)
+    for (int n = 0; n < kPer; ++n)
 #pragma unroll
-        for (int i = n & 1; i + 1 < kPer; i += 2) {
-          const bool swap = left[i + 1] > left[i];
-          const float hi = fmaxf(left[i], left[i + 1]), lo = fminf(left[i], left[i + 1]);
-          const int s = slot[i];
-          left[i] = hi, left[i + 1] = lo;
-          slot[i] = swap ? slot[i + 1] : s;
-          slot[i + 1] = swap ? s : slot[i + 1];
-        }
-    }
-    const int rounds = exact ? a.k : a.k + 1;
+      for (int i = n & 1; i + 1 < kPer; i += 2) {
+        const bool swap = left[i + 1] > left[i];
+        const float hi = fmaxf(left[i], left[i + 1]), lo = fminf(left[i], left[i + 1]);
+        const int s = slot[i];
+        left[i] = hi, left[i + 1] = lo;
+        slot[i] = swap ? slot[i + 1] : s;
+        slot[i + 1] = swap ? s : slot[i + 1];
+      }
+  }
+  const int rounds = exact ? a.k : a.k + 1;
 #pragma unroll 1
-    for (int j = 0; j < rounds; ++j) {
-      float m = left[0];
-      int at = slot[0];
-      if constexpr (!kSorted) {
+  for (int j = 0; j < rounds; ++j) {
+    float m = left[0];
+    int at = slot[0];
+    if constexpr (!kSorted) {
 #pragma unroll
-        for (int i = 1; i < kPer; ++i)
-          if (left[i] > m) m = left[i], at = i;
-      }
-      const float b = warp_max(m);
-      if (b == -INFINITY) break;
-      const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
-      const int id = __shfl_sync(0xffffffffu, first + at, who);
-      if (j == a.k) {
-        nv = b;
-        next = id;
-      } else if (lane == j) {
-        mine = id;
-        mv = b;
-      }
-      if (lane == who) {
-        if constexpr (kSorted) {
+      for (int i = 1; i < kPer; ++i)
+        if (left[i] > m) m = left[i], at = i;
+    }
+    const float b = warp_max(m);
+    if (b == -INFINITY) break;
+    const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
+    const int id = __shfl_sync(0xffffffffu, first + at, who);
+    if (j == a.k) {
+      nv = b;
+      next = id;
+    } else if (lane == j) {
+      mine = id;
+      mv = b;
+    }
+    if (lane == who) {
+      if constexpr (kSorted) {
 #pragma unroll
-          for (int i = 0; i + 1 < kPer; ++i) left[i] = left[i + 1], slot[i] = slot[i + 1];
-          left[kPer - 1] = -INFINITY;
-        } else {
+        for (int i = 0; i + 1 < kPer; ++i) left[i] = left[i + 1], slot[i] = slot[i + 1];
+        left[kPer - 1] = -INFINITY;
+      } else {
 #pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (i == at) left[i] = -INFINITY;
-        }
+        for (int i = 0; i < kPer; ++i)
+          if (i == at) left[i] = -INFINITY;
       }
     }
   }
@@ -339,15 +370,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
       const float slack = kUlps * (score(mx) + fabsf(mv) + score(x1) + fabsf(v1)) + 0x1p-120f;
       close = mv - v1 <= slack && !(mx == x1 && b0 == b1);
     }
-    if (__any_sync(0xffffffffu, close) || groups_near) {
+    if (__any_sync(0xffffffffu, close)) {
       // what can still be among the k: everything within the errors of the last choice
-      const float last = __shfl_sync(0xffffffffu, mv, a.k - 1);
-      float cut = last - 2.0f * kUlps * (2.0f + 2.0f * fabsf(last));
-      if (groups_near || !(cut < INFINITY)) cut = -INFINITY;  // also where a bias is infinite
-      float may[kPer];
+      const float last = __shfl_sync(0xffffffffu, mv, a.k - 1), least = last - 2.0f * kUlps * (2.0f + 2.0f * fabsf(last));
+      float may[kPer], cut[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) may[i] = v[i];
-      mine = choose_wide<T, kPer>(a, RouteRow{row, lane, group_size, softmax_top, total}, may, cut, groups_near, WideScratch{wide_all + warp * a.n_experts, list[warp]});
+      for (int i = 0; i < kPer; ++i) {
+        may[i] = v[i];
+        cut[i] = least < INFINITY ? least : -INFINITY;  // also where a bias is infinite
+      }
+      mine = choose_wide<T, kPer>(a, RouteRow{row, lane, group_size, softmax_top, total}, may, cut, scratch);
       mx = mine >= 0 ? to_f32(row[mine]) : -INFINITY;
     }
   }
@@ -369,7 +401,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
 
 int launch_route_topk(const RouteTopk& a, int dtype, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.n_tokens + kRouteWarps - 1) / kRouteWarps));
-  const size_t smem = a.bias || a.top_groups < a.n_groups ? sizeof(double) * kRouteWarps * a.n_experts : 0;
+  const size_t smem = a.bias || a.top_groups < a.n_groups ? (size_t)kWideBytes * kRouteWarps * a.n_experts : 0;
   return with_dtype(dtype, [&](auto v) {
     using T = decltype(v);
     auto kern = a.n_experts <= 32    ? route_topk_kernel<T, 1>
