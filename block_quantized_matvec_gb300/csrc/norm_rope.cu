@@ -92,11 +92,13 @@ __global__ void __launch_bounds__(128) norm_rope_any_kernel(const NormRope a) {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeWarpsWanted = 152 * 24;
+constexpr int kRopeStages = 4;  // steps of a warp's ring of rows
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_vec_kernel(const NormRope a, int splits) {
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const __grid_constant__ NormRope a, int splits) {
   constexpr int V = kVec<T>, kLanes = D / (2 * V), kRows = 32 / kLanes;  // lanes of a row, rows of a warp
   __shared__ float2 turns[kRopeWarps][D / 2];
+  __shared__ uint4 ring[kRopeWarps][kRopeStages][2][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -111,92 +113,83 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_vec_kernel(const No
 
   const int u = lane % kLanes, mine = lane / kLanes, half = a.rot / 2;
   const int turning = half / V;  // vectors of a half
-  const bool halves = u < turning && !a.interleaved;
+  const bool halves = !kInterleaved && u < turning;
   const int v0 = V * (halves ? u : 2 * u), v1 = halves ? v0 + half : v0 + V;
+  auto fetch = [&](int step) {
+    if (step < hi) {
+      const RopeHeads& r = step < q_steps ? a.q : a.k;
+      const int h = (step < q_steps ? step : step - q_steps) * kRows + mine;
+      if (h < r.heads) {
+        const T* x = static_cast<const T*>(r.x) + t * r.ldx + h * r.hx;
+        uint4* to = &ring[warp][(step - lo) % kRopeStages][0][lane];
+        copy16(to, x + v0);
+        copy16(to + 32, x + v1);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kRopeStages - 1; ++s) fetch(lo + s);
   for (int i = lane; i < half; i += 32) turns[warp][i] = pair_turn(a, i, t);
   __syncwarp();
 
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    const RopeHeads& r = kind ? a.k : a.q;
-    const int base = kind ? q_steps : 0;
-    const int begin = max(lo, base) - base, end = min(hi, kind ? steps : q_steps) - base;
-    if (begin >= end) continue;
-    const T* x = static_cast<const T*>(r.x) + t * r.ldx;
-    T* y = static_cast<T*>(r.y) + t * r.ldy;
-    auto load = [&](int step, uint4& p, uint4& q) {
-      const int h = step * kRows + mine;
-      if (h < r.heads) {
-        p = *reinterpret_cast<const uint4*>(x + h * r.hx + v0);
-        q = *reinterpret_cast<const uint4*>(x + h * r.hx + v1);
-      }
-    };
-    uint4 p = make_uint4(0u, 0u, 0u, 0u), q = p;
-    load(begin, p, q);
-    // weights of values i of v0 and v1, and with them the turn of their pair
-    float aa[V], ab[V], ba[V], bb[V];  // out0 = x0 * aa - x1 * ab, out1 = x0 * ba + x1 * bb
-    {
-      float w[2 * V];
+  // weights of values i of v0 and v1, and with them the turn of their pair:
+  // out0 = x0 * aa - x1 * ab, out1 = x0 * ba + x1 * bb
+  float aa[V], ab[V], ba[V], bb[V];
+  auto weigh = [&](const float* weight) {
+    float w[2 * V];
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) w[i] = 1.0f;
-      if (a.norm && r.weight) {
+    for (int i = 0; i < 2 * V; ++i) w[i] = 1.0f;
+    if (a.norm && weight) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(r.weight + v0 + i), g = *reinterpret_cast<const float4*>(r.weight + v1 + i);
-          w[i] = f.x, w[i + 1] = f.y, w[i + 2] = f.z, w[i + 3] = f.w;
-          w[V + i] = g.x, w[V + i + 1] = g.y, w[V + i + 2] = g.z, w[V + i + 3] = g.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 c = u * V + i < half ? turns[warp][u * V + i] : make_float2(1.0f, 0.0f);
-        const float w0 = a.interleaved ? w[2 * i] : w[i], w1 = a.interleaved ? w[2 * i + 1] : w[V + i];
-        aa[i] = w0 * c.x;
-        ab[i] = w1 * c.y;
-        ba[i] = w0 * c.y;
-        bb[i] = w1 * c.x;
+      for (int i = 0; i < V; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(weight + v0 + i), g = *reinterpret_cast<const float4*>(weight + v1 + i);
+        w[i] = f.x, w[i + 1] = f.y, w[i + 2] = f.z, w[i + 3] = f.w;
+        w[V + i] = g.x, w[V + i + 1] = g.y, w[V + i + 2] = g.z, w[V + i + 3] = g.w;
       }
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 c = u * V + i < half ? turns[warp][u * V + i] : make_float2(1.0f, 0.0f);
+      const float w0 = kInterleaved ? w[2 * i] : w[i], w1 = kInterleaved ? w[2 * i + 1] : w[V + i];
+      aa[i] = w0 * c.x;
+      ab[i] = w1 * c.y;
+      ba[i] = w0 * c.y;
+      bb[i] = w1 * c.x;
+    }
+  };
+
 #pragma unroll 1
-    for (int step = begin; step < end; ++step) {
-      float v[2 * V];
-      unpack16<T>(p, v);
-      unpack16<T>(q, v + V);
-      if (step + 1 < end) load(step + 1, p, q);
-      float scale = 1.0f;
-      if (a.norm) {
-        float sum = 0.0f;
+  for (int step = lo; step < hi; ++step) {
+    if (step == lo || step == q_steps) weigh(step < q_steps ? a.q.weight : a.k.weight);
+    fetch(step + kRopeStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRopeStages - 1) : "memory");
+    const uint4* from = &ring[warp][(step - lo) % kRopeStages][0][lane];
+    float v[2 * V];
+    unpack16<T>(from[0], v);
+    unpack16<T>(from[32], v + V);
+    float scale = 1.0f;
+    if (a.norm) {
+      float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) sum = fmaf(v[i], v[i], sum);
+      for (int i = 0; i < 2 * V; ++i) sum = fmaf(v[i], v[i], sum);
 #pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        scale = rsqrtf(sum * (1.0f / D) + a.eps);
-      }
-      float out[2 * V];
+      for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      scale = rsqrtf(sum * (1.0f / D) + a.eps);
+    }
+    float out[2 * V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float x0 = (a.interleaved ? v[2 * i] : v[i]) * scale, x1 = (a.interleaved ? v[2 * i + 1] : v[V + i]) * scale;
-        const float o0 = x0 * aa[i] - x1 * ab[i], o1 = x0 * ba[i] + x1 * bb[i];
-        v[i] = o0;
-        out[i] = o1;
-      }
-      // back in the vectors' order
-      float f[2 * V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (a.interleaved) {
-          f[2 * i] = v[i];
-          f[2 * i + 1] = out[i];
-        } else {
-          f[i] = v[i];
-          f[V + i] = out[i];
-        }
-      }
-      const int h = step * kRows + mine;
-      if (h < r.heads) {
-        *reinterpret_cast<uint4*>(y + h * r.hy + v0) = pack16<T>(f);
-        *reinterpret_cast<uint4*>(y + h * r.hy + v1) = pack16<T>(f + V);
-      }
+    for (int i = 0; i < V; ++i) {
+      const int i0 = kInterleaved ? 2 * i : i, i1 = kInterleaved ? 2 * i + 1 : V + i;
+      out[i0] = scale * (v[i0] * aa[i] - v[i1] * ab[i]);
+      out[i1] = scale * (v[i0] * ba[i] + v[i1] * bb[i]);
+    }
+    const RopeHeads& r = step < q_steps ? a.q : a.k;
+    const int h = (step < q_steps ? step : step - q_steps) * kRows + mine;
+    if (h < r.heads) {
+      T* y = static_cast<T*>(r.y) + t * r.ldy + h * r.hy;
+      *reinterpret_cast<uint4*>(y + v0) = pack16<T>(out);
+      *reinterpret_cast<uint4*>(y + v1) = pack16<T>(out + V);
     }
   }
 }
@@ -218,7 +211,12 @@ int launch_norm_rope(const NormRope& a, int dtype, int head_dim, cudaStream_t st
       const int steps = (a.q.heads + rows - 1) / rows + (a.k.heads + rows - 1) / rows;
       const int splits = (int)min((int64_t)steps, max((int64_t)1, (int64_t)kRopeWarpsWanted / a.n_tokens));
       const int64_t units = (int64_t)a.n_tokens * splits;
-      auto kern = head_dim == 64 ? norm_rope_vec_kernel<T, 64> : head_dim == 128 ? norm_rope_vec_kernel<T, 128> : norm_rope_vec_kernel<T, 256>;
+      auto kern = a.interleaved ? (head_dim == 64    ? norm_rope_vec_kernel<T, 64, true>
+                                   : head_dim == 128 ? norm_rope_vec_kernel<T, 128, true>
+                                                     : norm_rope_vec_kernel<T, 256, true>)
+                                : (head_dim == 64    ? norm_rope_vec_kernel<T, 64, false>
+                                   : head_dim == 128 ? norm_rope_vec_kernel<T, 128, false>
+                                                     : norm_rope_vec_kernel<T, 256, false>);
       return launch_pdl(kern, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)), dim3(32 * kRopeWarps), 0, stream, a, splits);
     }
     const int64_t rows = (int64_t)a.n_tokens * (a.q.heads + a.k.heads);

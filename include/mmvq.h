@@ -532,7 +532,7 @@ MMVQ_API int64_t mmvq_kv4_attention_workspace_bytes(int head_dim);
  * (>= 0, the values of a head side by side); yq, yk the same with their own
  * strides, and may be q and k themselves (same strides; no other overlap).
  * n_kv_heads = 0: queries alone.  z = x / sqrt(mean(x^2) + eps) * weight over
- * the head's values (q_weight, k_weight: fp32 [head_dim], NULL for ones;
+ * the head's values, their squares within fp32 (q_weight, k_weight: fp32 [head_dim], NULL for ones;
  * MMVQ_ROPE_NO_NORM: z = x).  Of the first rot_dim values of z, pair i, (i, i +
  * rot_dim/2) or (2i, 2i+1) with MMVQ_ROPE_INTERLEAVED, turns by the angle
  * positions[axis * ld_positions + token] * f_i; the others stay.  table: int64
