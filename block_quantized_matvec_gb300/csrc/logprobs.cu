@@ -107,7 +107,7 @@ __device__ __noinline__ uint4 load_edge(const T* x, int first, int vocab) {
   return r;
 }
 
-// What a warp, a CTA or a row has seen.
+// What a CTA, or a row, has seen: its list in order, and the sums over all others.
 struct RowPart {
   float v[32];
   int id[32];
@@ -144,28 +144,6 @@ struct RowState {
   __device__ __forceinline__ void refer(float m, float L) {
     const bool far = !(fabsf(m * L) < kFar);
     refer(far ? m : 0.0f, far ? 0.0f : m * L, L);
-  }
-  __device__ __forceinline__ void write(RowPart& p, int lane) {
-    const float s = warp_sum(s2.x + s2.y), t = warp_sum(t2.x + t2.y);
-    const bool any = __any_sync(0xffffffffu, bad);
-    p.v[lane] = v;
-    p.id[lane] = id;
-    if (lane == 0) {
-      p.s = s;
-      p.t = t;
-      p.C = C;
-      p.R = R;
-      p.bad = any;
-    }
-  }
-  __device__ __forceinline__ void read(const RowPart& p, int lane) {
-    v = p.v[lane];
-    id = p.id[lane];
-    s2 = make_float2(lane == 0 ? p.s : 0.0f, 0.0f);
-    t2 = make_float2(lane == 0 ? p.t : 0.0f, 0.0f);
-    C = p.C;
-    R = p.R;
-    bad = p.bad;
   }
 };
 
@@ -208,32 +186,71 @@ __device__ __forceinline__ void absorb(RowState& a, float v, int id, int live, i
   }
 }
 
-// b's list and sums into a's.
-__device__ __forceinline__ void merge(RowState& a, const RowState& b, int live, int lane, float L) {
-  if (b.R > -INFINITY) {
-    RowState o = b;
-    if (a.R == -INFINITY || fmaf(b.C - a.C, L, b.R - a.R) > 0.0f)
-      a.refer(b.C, b.R, L);
-    else
-      o.refer(a.C, a.R, L);
-    a.s2 = __fadd2_rn(a.s2, o.s2);
-    a.t2 = __fadd2_rn(a.t2, o.t2);
-  }
-  a.bad |= b.bad;
-  absorb(a, b.v, b.id, live, lane, L);
-}
+// Where a CTA's warps bring their lists together.
+template <int kWarps>
+struct Meeting {
+  int2 entry[64 * kWarps];  // value and id
+  RowPart row;
+  int count[kWarps], bad[kWarps];
+  float s[kWarps], t[kWarps];
+};
 
-// The lists and sums of n warps, warp w's in w's state, into warp 0's.
-__device__ __forceinline__ void merge_warps(RowState& st, RowPart* parts, int n, int live, int warp, int lane, float L) {
-  for (int step = 1; step < n; step *= 2) {
-    __syncthreads();
-    if (warp < n && (warp & (2 * step - 1)) == step) st.write(parts[warp], lane);
-    __syncthreads();
-    if (warp + step < n && (warp & (2 * step - 1)) == 0) {
-      RowState o;
-      o.read(parts[warp + step], lane);
-      merge(st, o, live, lane, L);
+// The warps' lists (each its list and `waiting` entries) and sums as one, in warp 0's state.  A
+// handful of entries a warp: each thread takes one and counts those before it.
+template <int kWarps>
+__device__ __forceinline__ void join(Meeting<kWarps>& m, RowState& st, float wait_v, int wait_id, int waiting, int live, int warp, int lane, float L) {
+  const int tid = 32 * warp + lane;
+  const int listed = __popc(__ballot_sync(0xffffffffu, st.v > -INFINITY));
+  if (lane == 0) m.count[warp] = waiting + listed;
+  if (warp == 0) {
+    m.row.v[lane] = -INFINITY;
+    m.row.id[lane] = 0x7fffffff;
+  }
+  __syncthreads();
+  const int c = lane < kWarps ? m.count[lane] : 0;
+  const int n = __reduce_add_sync(0xffffffffu, c), base = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+  if (lane < waiting) m.entry[base + lane] = make_int2(__float_as_int(wait_v), wait_id);
+  if (lane < listed) m.entry[base + waiting + lane] = make_int2(__float_as_int(st.v), st.id);
+  __syncthreads();
+  for (int i = tid; i < n; i += 32 * kWarps) {
+    const float v = __int_as_float(m.entry[i].x);
+    const int id = m.entry[i].y;
+    int at = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const int2 o = m.entry[j];
+      at += before(__int_as_float(o.x), o.y, v, id);
     }
+    if (at < live) {
+      m.row.v[at] = v;
+      m.row.id[at] = id;
+    }
+  }
+  __syncthreads();
+  const float last = m.row.v[live - 1];
+  if (last > -INFINITY) {  // a full list: what comes after it goes into the sums
+    const int last_id = m.row.id[live - 1];
+    st.refer(last, L);
+    for (int i = tid; i < n; i += 32 * kWarps) {
+      const float v = __int_as_float(m.entry[i].x);
+      if (before(last, last_id, v, m.entry[i].y)) st.add(v, L);
+    }
+  }
+  const float s = warp_sum(st.s2.x + st.s2.y), t = warp_sum(st.t2.x + st.t2.y);
+  const bool bad = __any_sync(0xffffffffu, st.bad);
+  if (lane == 0) {
+    m.s[warp] = s;
+    m.t[warp] = t;
+    m.bad[warp] = bad;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const float ss = warp_sum(lane < kWarps ? m.s[lane] : 0.0f), tt = warp_sum(lane < kWarps ? m.t[lane] : 0.0f);
+    st.s2 = make_float2(lane == 0 ? ss : 0.0f, 0.0f);
+    st.t2 = make_float2(lane == 0 ? tt : 0.0f, 0.0f);
+    st.bad = __any_sync(0xffffffffu, lane < kWarps && m.bad[lane]);
+    st.v = m.row.v[lane];
+    st.id = m.row.id[lane];
   }
 }
 
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
   constexpr int V = kVec<T>, kThreads = 32 * kWarps;
   // a lane's values are looked at 32 at a time, or all at once where they are fewer
   static_assert(kUnroll * V % 32 == 0 || kUnroll * V < 32);
-  __shared__ RowPart parts[kWarps];
+  __shared__ Meeting<kWarps> meeting;
   __shared__ float2 ends[kWarps];
   __shared__ float said[2];
   __shared__ int count[kBins];
@@ -448,19 +465,48 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     }
   }
 
-  settle();
-  merge_warps(st, parts, kWarps, live, warp, lane, L);
+  join(meeting, st, wait_v, wait_id, waiting, live, warp, lane, L);
   if (cluster > 1) {
-    __syncthreads();
-    if (warp == 0) st.write(parts[0], lane);
+    if (tid == 0) {
+      meeting.row.s = st.s2.x;
+      meeting.row.t = st.t2.x;
+      meeting.row.C = st.C;
+      meeting.row.R = st.R;
+    }
+    if (warp == 0) meeting.row.bad = st.bad;
     cg::this_cluster().sync();
-    if (rank == 0) {
-      st.v = -INFINITY;
-      if (warp < cluster) st.read(*cg::this_cluster().map_shared_rank(&parts[0], warp), lane);
+    st.s2 = st.t2 = make_float2(0.0f, 0.0f);
+    st.C = 0.0f;
+    st.R = -INFINITY;
+    st.bad = false;
+    wait_v = -INFINITY;
+    if (rank == 0 && warp < cluster) {  // a CTA's to each warp
+      const RowPart& from = *cg::this_cluster().map_shared_rank(&meeting.row, warp);
+      wait_v = from.v[lane];
+      wait_id = from.id[lane];
+      if (lane == 0) {
+        st.s2.x = from.s;
+        st.t2.x = from.t;
+      }
+      st.C = from.C;
+      st.R = from.R;
+      st.bad = from.bad;
     }
     cg::this_cluster().sync();  // all are read: the others may leave
     if (rank != 0) return;
-    merge_warps(st, parts, cluster, live, warp, lane, L);
+    // what does not reach the best of the lists' last ones is not among the row's
+    st.v = -INFINITY;
+    const float last = __shfl_sync(0xffffffffu, wait_v, live - 1);
+    if (lane == 0) meeting.s[warp] = last;
+    __syncthreads();
+    const float least = warp_max(lane < kWarps ? meeting.s[lane] : -INFINITY);
+    __syncthreads();
+    if (least > -INFINITY) {
+      st.refer(least, L);
+      if (wait_v > -INFINITY && wait_v < least) st.add(wait_v, L);
+    }
+    waiting = __popc(__ballot_sync(0xffffffffu, wait_v > -INFINITY && wait_v >= least));  // the list's first ones
+    join(meeting, st, wait_v, wait_id, waiting, live, warp, lane, L);
   }
 
   const float nan = __int_as_float(0x7fc00000);
@@ -548,12 +594,20 @@ static int launch_rows(const TokenLogprobs& a, int cluster, cudaStream_t stream)
 int launch_token_logprobs(const TokenLogprobs& a, int dtype, cudaStream_t stream) {
   return with_dtype(dtype, [&](auto v) {
     using T = decltype(v);
+    constexpr int kSms = 152;
     const int vectors = (a.vocab + 2 * kVec<T> - 1) / kVec<T>;
-    if (vectors <= 32 * 8) return launch_rows<T, 1, 4>(a, 1, stream);
-    if (vectors <= 128 * 8 || a.rows > 2 * 152) return launch_rows<T, 4, 8>(a, 1, stream);
-    // As many CTAs to a row as still have a batch of vectors each, up to two CTAs an SM in all.
+    // Many short rows: a warp each (2048 x 1000 bf16 13.6 us, by CTAs of 4 warps 21.5; 16 x 1000 9.3 and 7.0).
+    if (vectors <= 160 && a.rows > 4 * kSms) return launch_rows<T, 1, 4>(a, 1, stream);
+    // CTAs of 4 warps, six an SM, spend less on a row than those of 16, two an SM, but need more rows to fill the
+    // GPU.  (bf16, 4 and 16 warps: 600 rows of 152000 54.6 and 47.9 us, of 50000 28.2 and 26.8; 1000 rows 75.5 and
+    // 78.8, 39.7 and 45.5; 152 and 300 rows of 4000 7.6 and 6.6, 7.6 and 8.1.  fp32, 1000 rows of 152000: 125 and 104.)
+    if (a.rows > (vectors <= 1024 ? 1 : vectors <= 32768 ? 4 : 8) * kSms) return launch_rows<T, 4, 8>(a, 1, stream);
+    // Few rows: a cluster's CTAs share one, as far as each has a batch and the GPU has places.  (One row of
+    // 152000 bf16 by 1, 2, 4, 8, 16 CTAs: 14.8, 13.3, 11.6, 10.0, 10.8 us; 64 rows by 1, 2, 4: 16.4, 13.8, 15.4;
+    // one row of 16000: 5.8, 8.1.)
     int cluster = 1;
-    while (cluster < 16 && (int64_t)a.rows * cluster * 2 <= 2 * 152 && vectors >= cluster * 512 * 4) cluster *= 2;
+    if (vectors > 4096)
+      while (cluster < 16 && vectors > 2500 * cluster && (int64_t)a.rows * 2 * cluster <= (cluster == 8 ? 64 : 128)) cluster *= 2;
     return launch_rows<T, 16, 4>(a, cluster, stream);
   });
 }
