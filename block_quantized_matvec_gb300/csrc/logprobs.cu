@@ -195,13 +195,22 @@ struct Meeting {
   float s[kWarps], t[kWarps];
 };
 
-// The warps' lists (each its list and `waiting` entries) and sums as one, in warp 0's state.  A
-// handful of entries a warp: each thread takes one and counts those before it.
+// The warps' lists (each its list and the entries waiting) and sums as one, in warp 0's state.  At
+// least `live` entries reach `least`, so what does not goes into the sums; of the others, a handful,
+// each thread takes one and counts those before it.
 template <int kWarps>
-__device__ __forceinline__ void join(Meeting<kWarps>& m, RowState& st, float wait_v, int wait_id, int waiting, int live, int warp, int lane, float L) {
+__device__ __forceinline__ void join(Meeting<kWarps>& m, RowState& st, float wait_v, int wait_id, float least, int live, int warp, int lane, float L) {
   const int tid = 32 * warp + lane;
-  const int listed = __popc(__ballot_sync(0xffffffffu, st.v > -INFINITY));
-  if (lane == 0) m.count[warp] = waiting + listed;
+  if (least > -INFINITY) {
+    if (fmaf(least - st.C, L, -st.R) > 0.0f) st.refer(least, L);
+    if (wait_v > -INFINITY && wait_v < least) st.add(wait_v, L);
+    if (st.v > -INFINITY && st.v < least) st.add(st.v, L);
+  }
+  const uint32_t waits = __ballot_sync(0xffffffffu, wait_v > -INFINITY && wait_v >= least);
+  const uint32_t lists = __ballot_sync(0xffffffffu, st.v > -INFINITY && st.v >= least);
+  const uint32_t below = (1u << lane) - 1u;
+  const int waiting = __popc(waits);
+  if (lane == 0) m.count[warp] = waiting + __popc(lists);
   if (warp == 0) {
     m.row.v[lane] = -INFINITY;
     m.row.id[lane] = 0x7fffffff;
@@ -209,8 +218,8 @@ __device__ __forceinline__ void join(Meeting<kWarps>& m, RowState& st, float wai
   __syncthreads();
   const int c = lane < kWarps ? m.count[lane] : 0;
   const int n = __reduce_add_sync(0xffffffffu, c), base = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
-  if (lane < waiting) m.entry[base + lane] = make_int2(__float_as_int(wait_v), wait_id);
-  if (lane < listed) m.entry[base + waiting + lane] = make_int2(__float_as_int(st.v), st.id);
+  if ((waits >> lane) & 1) m.entry[base + __popc(waits & below)] = make_int2(__float_as_int(wait_v), wait_id);
+  if ((lists >> lane) & 1) m.entry[base + waiting + __popc(lists & below)] = make_int2(__float_as_int(st.v), st.id);
   __syncthreads();
   for (int i = tid; i < n; i += 32 * kWarps) {
     const float v = __int_as_float(m.entry[i].x);
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
   st.R = -INFINITY;
   st.bad = false;
   // values from last_v on may enter the list, in batches to come those from `look` on
-  float last_v = -FLT_MAX, look = -FLT_MAX, largest = -INFINITY;
+  float last_v = -FLT_MAX, look = -FLT_MAX, largest = -INFINITY, bound = -INFINITY;
   int next = 0;
   const float one_over_L = 1.0f / L;
   const float2 L2 = make_float2(L, L);
@@ -385,6 +394,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
         const int odd = __shfl_sync(0xffffffffu, above - c0 >= live, pair);
         const int bin = 2 * pair + odd;
         if (bin > 0 && per > 0.0f) l = fmaxf(l, fmaf((float)bin - 0.01f, 1.0f / per, l));
+        bound = l;
         if (l > last_v) {
           last_v = look = l;
           if (fmaf(l - st.C, L, -st.R) > kSlack) st.refer(l, L);
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     }
   }
 
-  join(meeting, st, wait_v, wait_id, waiting, live, warp, lane, L);
+  join(meeting, st, wait_v, wait_id, bound, live, warp, lane, L);
   if (cluster > 1) {
     if (tid == 0) {
       meeting.row.s = st.s2.x;
@@ -501,12 +511,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     __syncthreads();
     const float least = warp_max(lane < kWarps ? meeting.s[lane] : -INFINITY);
     __syncthreads();
-    if (least > -INFINITY) {
-      st.refer(least, L);
-      if (wait_v > -INFINITY && wait_v < least) st.add(wait_v, L);
-    }
-    waiting = __popc(__ballot_sync(0xffffffffu, wait_v > -INFINITY && wait_v >= least));  // the list's first ones
-    join(meeting, st, wait_v, wait_id, waiting, live, warp, lane, L);
+    join(meeting, st, wait_v, wait_id, least, live, warp, lane, L);
   }
 
   const float nan = __int_as_float(0x7fc00000);
