@@ -14,11 +14,14 @@
 // and chooses by those.
 //
 // A warp per token; lane L holds the experts L * kPer .. + kPer - 1, so a lower
-// lane means a lower id.  Bound by instructions, not by the few bytes: up to 8
-// experts of a lane are sorted once (28 exchanges of neighbours, which leave
-// equal values in order), so that each of the k rounds is a maximum over the
-// lanes' first ones and a shift in the lane that had it; more of them are
-// searched anew in every round, which then costs no more than the sorting would.
+// lane means a lower id.  Bound by instructions, not by the few bytes.  The lanes'
+// best ones are sorted (values alone: a shuffle and a minimum or maximum a step);
+// as many experts as are needed reach the need-th of those, and the few that do are
+// put one to a lane, which counts how many come before it.  Where many are equal and
+// more than 32 reach it, the best is taken k times over.  (8192 tokens, 8 of 256 in
+// groups: every lane's experts sorted and the best taken k times 17.3 us.)
+#include <cfloat>
+
 #include "layer.cuh"
 #include "typed.cuh"
 
@@ -166,6 +169,7 @@ __device__ __noinline__ int choose_wide(const RouteTopk& a, const RouteRow r, co
 
 template <typename T, int kPer>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __grid_constant__ RouteTopk a) {
+  __shared__ int2 found[kRouteWarps][32];  // value and id
   extern __shared__ double wide_all[];  // WideScratch of each warp: all values, then all lists
   grid_dependency_wait();
   grid_launch_dependents();
@@ -304,54 +308,71 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
     }
   }
 
-  // k rounds of the best of all lanes, once more for the one after the last; lane j keeps choice j
+  // the k best, in order, and the one after the last; lane j keeps choice j
   int mine = -1, next = -1;
   float mv = -INFINITY, nv = -INFINITY;
-  float left[kPer];
-  int slot[kPer];
+  const int need = exact ? a.k : a.k + 1;
+  int n = 33;  // experts that reach the bound
+  if (need <= 32) {
+    // as many lanes' best ones reach the need-th largest of them
+    float best = v[0];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) left[i] = v[i], slot[i] = i;
-  constexpr bool kSorted = kPer <= 8;
-  if constexpr (kSorted) {
+    for (int i = 1; i < kPer; ++i) best = fmaxf(best, v[i]);
 #pragma unroll
-    for (int n = 0; n < kPer; ++n)
+    for (int m = 2; m <= 32; m *= 2)
 #pragma unroll
-      for (int i = n & 1; i + 1 < kPer; i += 2) {
-        const bool swap = left[i + 1] > left[i];
-        const float hi = fmaxf(left[i], left[i + 1]), lo = fminf(left[i], left[i + 1]);
-        const int s = slot[i];
-        left[i] = hi, left[i + 1] = lo;
-        slot[i] = swap ? slot[i + 1] : s;
-        slot[i + 1] = swap ? s : slot[i + 1];
+      for (int o = m / 2; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, best, o);
+        best = !(lane & o) == !(lane & m) ? fmaxf(best, other) : fminf(best, other);
       }
+    const float bound = fmaxf(__shfl_sync(0xffffffffu, best, need - 1), -FLT_MAX);
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t m = __ballot_sync(0xffffffffu, v[i] >= bound);
+      const int at = n + __popc(m & ((1u << lane) - 1u));
+      if (v[i] >= bound && at < 32) found[warp][at] = make_int2(__float_as_int(v[i]), first + i);
+      n += __popc(m);
+    }
+    __syncwarp();
   }
-  const int rounds = exact ? a.k : a.k + 1;
+  if (n <= 32) {  // mostly: one a lane, which counts those before it
+    const int2 e = found[warp][lane < n ? lane : 0];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const int2 o = found[warp][j];
+      const float ov = __int_as_float(o.x), ev = __int_as_float(e.x);
+      rank += ov > ev || (ov == ev && o.y < e.y);
+    }
+    __syncwarp();
+    if (lane < n) found[warp][rank] = e;
+    __syncwarp();
+    const int2 c = found[warp][lane], after = found[warp][a.k & 31];
+    if (lane < min(n, a.k)) mine = c.y, mv = __int_as_float(c.x);
+    if (a.k < n) next = after.y, nv = __int_as_float(after.x);
+  } else {
+    float left[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) left[i] = v[i];
 #pragma unroll 1
-  for (int j = 0; j < rounds; ++j) {
-    float m = left[0];
-    int at = slot[0];
-    if constexpr (!kSorted) {
+    for (int j = 0; j < need; ++j) {
+      float m = left[0];
+      int at = 0;
 #pragma unroll
       for (int i = 1; i < kPer; ++i)
         if (left[i] > m) m = left[i], at = i;
-    }
-    const float b = warp_max(m);
-    if (b == -INFINITY) break;
-    const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
-    const int id = __shfl_sync(0xffffffffu, first + at, who);
-    if (j == a.k) {
-      nv = b;
-      next = id;
-    } else if (lane == j) {
-      mine = id;
-      mv = b;
-    }
-    if (lane == who) {
-      if constexpr (kSorted) {
-#pragma unroll
-        for (int i = 0; i + 1 < kPer; ++i) left[i] = left[i + 1], slot[i] = slot[i + 1];
-        left[kPer - 1] = -INFINITY;
-      } else {
+      const float b = warp_max(m);
+      if (b == -INFINITY) break;
+      const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
+      const int id = __shfl_sync(0xffffffffu, first + at, who);
+      if (j == a.k) {
+        nv = b;
+        next = id;
+      } else if (lane == j) {
+        mine = id;
+        mv = b;
+      }
+      if (lane == who) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
           if (i == at) left[i] = -INFINITY;
