@@ -652,13 +652,14 @@ _SCORING = {"softmax": 0, "sigmoid": 1}  # mmvq_scoring
 
 
 def _on(t: torch.Tensor, stream):
-    """The number of a tensor's device, which has to be the one that the call runs on."""
+    """The number of a tensor's device, which has to be the one that the call runs on, and the
+    stream's handle."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors")
     if dev != (torch.cuda.current_device() if stream is None else stream.device_index):
         raise ValueError("the tensors are on another device than the call's stream")
-    return dev
+    return dev, _stream(stream)
 
 
 def _plain(t, dtype, shape, dev, name):
@@ -671,10 +672,11 @@ def _plain(t, dtype, shape, dev, name):
 
 
 def _layer_status(status, dev):
-    if status is not None and (status.dtype is not torch.int32 or status.get_device() != dev or
-                               status.numel() < 1):
+    if status is None:
+        return None
+    if status.dtype is not torch.int32 or status.get_device() != dev or status.numel() < 1:
         raise ValueError("status must be an int32 tensor on the call's device")
-    return _ptr(status)
+    return status.data_ptr()
 
 
 def _rows(t, dtype, shape, dev, name):
@@ -741,7 +743,7 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     the token's position -> (q, k), contiguous or written to out (which may be q and k themselves).
     positions: int32 [n], or [axes, n]; table: rope_table; eps=None leaves the norm out;
     interleaved pairs neighbours instead of halves.  (mmvq_norm_rope)"""
-    dev = _on(q, stream)
+    dev, on = _on(q, stream)
     n, heads, dim = q.shape
     dtype, _, _, ldq, hq = _kv4_rows(q, 0, dim, dev, "q")
     if out is None:
@@ -761,15 +763,15 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
             raise ValueError("q, k and out must have the same tokens and type")
     if dtype_y != dtype or n_y != n:
         raise ValueError("q, k and out must have the same tokens and type")
-    pos_shape, ld_pos = positions.shape, positions.stride(0)
-    if positions.dtype is not torch.int32 or positions.get_device() != dev or \
-            pos_shape[-1] != n or len(pos_shape) > 2 or (positions.stride(-1) != 1 and n > 1):
+    shape, strides = positions.shape, positions.stride()
+    axes, ld_pos = (1, 0) if len(shape) == 1 else (shape[0], strides[0])
+    if positions.dtype is not torch.int32 or positions.get_device() != dev or shape[-1] != n or \
+            len(shape) > 2 or (strides[-1] != 1 and n > 1):
         raise ValueError(f"positions must be an int32 tensor [{n}] or [axes, {n}] with unit inner "
                          "stride on the call's device")
-    axes, ld_pos = (1, 0) if len(pos_shape) == 1 else (pos_shape[0], ld_pos)
-    half = table.shape[1]
-    if table.dtype is not torch.int64 or table.dim() != 2 or table.shape[0] != 2 or \
-            table.get_device() != dev or not table.is_contiguous():
+    two, half = table.shape
+    if table.dtype is not torch.int64 or two != 2 or table.get_device() != dev or \
+            not table.is_contiguous():
         raise ValueError("table must be a rope_table on the call's device")
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_NO_NORM if eps is None else 0)
     _check(lib().mmvq_norm_rope(dtype, q.data_ptr(), ldq, hq, heads, _ptr(k), ldk, hk, kv, dim, n,
@@ -777,8 +779,7 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
                                 _plain(q_weight, torch.float32, (dim,), dev, "q_weight"),
                                 _plain(k_weight, torch.float32, (dim,), dev, "k_weight"),
                                 0.0 if eps is None else eps, flags, yq.data_ptr(), ldyq, hyq,
-                                _ptr(yk), ldyk, hyk, _layer_status(status, dev),
-                                _stream(stream)), "mmvq_norm_rope")
+                                _ptr(yk), ldyk, hyk, _layer_status(status, dev), on), "mmvq_norm_rope")
     return yq, yk
 
 
@@ -791,7 +792,7 @@ def route_topk(logits: torch.Tensor, k: int, *, scoring: str = "softmax",
     (all by default) of n_groups runs of experts whose two best add up to most; weights are their
     scores, renormalised to sum to 1 before scale.  What route_groups, expert_ffn and
     combine_experts take.  (mmvq_route_topk)"""
-    dev = _on(logits, stream)
+    dev, on = _on(logits, stream)
     n, experts = logits.shape
     dtype = _DTYPES.get(logits.dtype)
     if dtype is None or scoring not in _SCORING:
@@ -807,7 +808,7 @@ def route_topk(logits: torch.Tensor, k: int, *, scoring: str = "softmax",
                                  1 if renormalize else 0, scale,
                                  _plain(topk, torch.int32, (n, k), dev, "out[0]"),
                                  _plain(weights, torch.float32, (n, k), dev, "out[1]"),
-                                 _layer_status(status, dev), _stream(stream)), "mmvq_route_topk")
+                                 _layer_status(status, dev), on), "mmvq_route_topk")
     return topk, weights
 
 
@@ -821,7 +822,7 @@ def combine_experts(y: torch.Tensor, topk: torch.Tensor, weights: torch.Tensor,
     fp32 times weights [n, k], where offsets and slot_of are the lists of topk [n, k] (route_groups,
     expert_ffn).  residual and shared [n, H] (either may be missing) have out's type: dtype, theirs,
     or float32.  shared_gate: fp32 [n], None for a weight of 1.  (mmvq_combine_experts)"""
-    dev = _on(y, stream)
+    dev, on = _on(y, stream)
     n, k = topk.shape
     positions, H = y.shape
     if dtype is None:
@@ -844,7 +845,7 @@ def combine_experts(y: torch.Tensor, topk: torch.Tensor, weights: torch.Tensor,
                                       _plain(slot_of, i32, slot_of.shape, dev, "slot_of"),
                                       residual_at, ldr, shared_at, lds,
                                       _plain(shared_gate, f32, (n,), dev, "shared_gate"), out_at,
-                                      ldo, _layer_status(status, dev), _stream(stream)),
+                                      ldo, _layer_status(status, dev), on),
            "mmvq_combine_experts")
     return out
 
@@ -856,7 +857,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, *, 
     of the given tokens [n, m] int32, and the `top` likeliest tokens, top_ids [n, top] int32 and
     top_logprobs [n, top].  out: such a dict to write to; lse and entropy may be missing in it.
     (mmvq_token_logprobs)"""
-    dev = _on(logits, stream)
+    dev, on = _on(logits, stream)
     n, vocab = logits.shape
     dtype = _DTYPES.get(logits.dtype)
     if dtype is None:
@@ -878,6 +879,6 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, *, 
                                      _plain(get("top_ids"), i32, (n, top), dev, "top_ids"),
                                      _plain(get("top_logprobs"), f32, (n, top), dev,
                                             "top_logprobs"),
-                                     _layer_status(status, dev), _stream(stream)),
+                                     _layer_status(status, dev), on),
            "mmvq_token_logprobs")
     return out
