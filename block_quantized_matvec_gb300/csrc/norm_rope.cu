@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(128) norm_rope_any_kernel(const NormRope a) {
 }
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeWarpsWanted = 152 * 24;
+constexpr int kRopeWarpsAtOnce = 152 * 24;
 constexpr int kRopeStages = 4;  // steps of a warp's ring of rows
 
 template <typename T, int D, bool kInterleaved>
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const
 
   const int u = lane % kLanes, mine = lane / kLanes, half = a.rot / 2;
   const int turning = half / V;  // vectors of a half
-  const bool halves = !kInterleaved && u < turning;
-  const int v0 = V * (halves ? u : 2 * u), v1 = halves ? v0 + half : v0 + V;
+  // neighbouring lanes have neighbouring vectors, so that no 32-byte sector is fetched twice
+  const int v0 = V * (kInterleaved || u < turning ? u : u + turning), v1 = V * (!kInterleaved && u < turning ? u + turning : u + kLanes);
   auto fetch = [&](int step) {
     if (step < hi) {
       const RopeHeads& r = step < q_steps ? a.q : a.k;
@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float2 c = u * V + i < half ? turns[warp][u * V + i] : make_float2(1.0f, 0.0f);
+      const int pair = !kInterleaved ? u * V + i : i < V / 2 ? v0 / 2 + i : v1 / 2 + i - V / 2;
+      const float2 c = pair < half ? turns[warp][pair] : make_float2(1.0f, 0.0f);
       const float w0 = kInterleaved ? w[2 * i] : w[i], w1 = kInterleaved ? w[2 * i + 1] : w[V + i];
       aa[i] = w0 * c.x;
       ab[i] = w1 * c.y;
@@ -206,10 +207,13 @@ int launch_norm_rope(const NormRope& a, int dtype, int head_dim, cudaStream_t st
     using T = decltype(v);
     const int size = (int)sizeof(T), V = kVec<T>;
     if (rope_vectors(a.q, size) && (!a.k.heads || rope_vectors(a.k, size)) && (a.interleaved || a.rot / 2 % V == 0)) {
-      // Few tokens: a token's heads are shared out to as many warps as fill the GPU, up to one step each.
+      // A token's heads are shared out to several warps: where tokens are few, to as many as fill the GPU, up to one
+      // step each; else in shares of four steps or more, for four rounds of warps, so that the last round costs
+      // little (7596 tokens of 36 x 256: 64.7 us with a warp a token, 59.3 so, 61.1 in eight rounds).
       const int rows = 64 * V / head_dim;
       const int steps = (a.q.heads + rows - 1) / rows + (a.k.heads + rows - 1) / rows;
-      const int splits = (int)min((int64_t)steps, max((int64_t)1, (int64_t)kRopeWarpsWanted / a.n_tokens));
+      const bool few = (int64_t)steps * a.n_tokens <= kRopeWarpsAtOnce;
+      const int splits = few ? steps : (int)min((int64_t)max(1, steps / 4), (4 * (int64_t)kRopeWarpsAtOnce + a.n_tokens - 1) / a.n_tokens);
       const int64_t units = (int64_t)a.n_tokens * splits;
       auto kern = a.interleaved ? (head_dim == 64    ? norm_rope_vec_kernel<T, 64, true>
                                    : head_dim == 128 ? norm_rope_vec_kernel<T, 128, true>
