@@ -553,6 +553,10 @@ int mmvq_norm_rope(int dtype, const void* q, int64_t ldq, int64_t hq, int n_head
   if (ldq < 0 || hq < 0 || ldk < 0 || hk < 0 || ldyq < 0 || hyq < 0 || ldyk < 0 || hyk < 0)
     return MMVQ_ERR_SHAPE;
   if ((int64_t)n_tokens * (n_heads + n_kv_heads) >= (int64_t)1 << 32) return MMVQ_ERR_SHAPE;
+  // rows that are written lie apart
+  if ((n_tokens > 1 && (ldyq < head_dim || (n_kv_heads > 0 && ldyk < head_dim))) ||
+      (n_heads > 1 && hyq < head_dim) || (n_kv_heads > 1 && hyk < head_dim))
+    return MMVQ_ERR_SHAPE;
   if (flags & ~(MMVQ_ROPE_INTERLEAVED | MMVQ_ROPE_NO_NORM)) return MMVQ_ERR_SHAPE;
   if (!(eps >= 0.0f) || !(eps < INFINITY)) return MMVQ_ERR_SHAPE;
   if (n_tokens == 0) return MMVQ_OK;

@@ -440,6 +440,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     const float2 R2 = make_float2(-st.R, -st.R);
     const T least = from_f32<T>(fmaxf((st.R - 160.0f) * one_over_L, std::is_same<T, __half>::value ? -65504.0f : -3.0e38f));
     if (st.C == 0.0f && fmaf(to_f32(least), L, -st.R) <= -150.0f) {
+      // a batch's sums by themselves: however long the row, few additions follow one another
+      float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const uint4 raw = mine[u * kThreads];
@@ -463,10 +465,12 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
         for (int i = 0; i < V; i += 2) {
           const float2 y = __ffma2_rn(make_float2(v[i], v[i + 1]), L2, R2);
           const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          st.s2 = __fadd2_rn(st.s2, e);
-          st.t2 = __ffma2_rn(e, y, st.t2);
+          s2 = __fadd2_rn(s2, e);
+          t2 = __ffma2_rn(e, y, t2);
         }
       }
+      st.s2 = __fadd2_rn(st.s2, s2);
+      st.t2 = __fadd2_rn(st.t2, t2);
     } else {  // logits so large, or a scale so small, that the type has no such value
 #pragma unroll 1
       for (int u = 0; u < kUnroll; ++u)

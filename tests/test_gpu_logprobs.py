@@ -158,3 +158,32 @@ def test_two_streams_at_once_and_replays():
         have = {name: t.clone() for name, t in out.items()}
         again = mmvq.token_logprobs(x[1], None, top=20)
         assert all(torch.equal(have[name], again[name]) for name in again)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n,V", [(1, 1000003), (400, 262144), (700, 150001), (3, 5000)])
+def test_even_rows_keep_their_sums(dtype, n, V):
+    """All logits but eight equal: every addition rounds the same way.  A batch's sums are at most 32 additions of a
+    thread, a row's at most 123 batches of it (one CTA of 512 threads to 1000003 fp32), then 10 of its warp and 8 of the
+    CTAs: below 180 half units in all, and the same again for exp and its argument's rounding (up to 8)."""
+    x = torch.full((n, V), 0.3, device="cuda").to(TYPES[dtype])
+    x[:, V // 2:V // 2 + 8] = 1.0                 # the rest lies below the list's last
+    got = mmvq.token_logprobs(x, None, top=8)
+    a, b = (float(t) for t in (x[0, 0], x[0, V // 2]))
+    total = 8 + (V - 8) * np.exp(a - b)           # of exp(x - the largest)
+    lse, entropy = b + np.log(total), np.log(total) - (V - 8) * np.exp(a - b) * (a - b) / total
+    for name, want in (("lse", lse), ("entropy", entropy)):
+        err = np.abs(host(got[name]).astype(np.float64) - want)
+        assert err.max() <= 200 * 2.0 ** -24 + 2 * 2.0 ** -24 * want, (name, err.max() / 2.0 ** -24)
+    assert np.array_equal(host(got["top_ids"]), np.tile(np.arange(V // 2, V // 2 + 8, dtype=np.int32), (n, 1)))
+
+
+def test_nothing_beside_the_outputs_is_written():
+    n, V, m, top = 5, 4001, 3, 4
+    x, tokens = rows(n, V, "bf16", 4)
+    want = mmvq.token_logprobs(x, tokens, top=top)
+    room = {name: torch.full((t.numel() + 64,), -7, dtype=t.dtype, device="cuda") for name, t in want.items()}
+    out = {name: room[name][32:32 + t.numel()].view(t.shape) for name, t in want.items()}
+    mmvq.token_logprobs(x, tokens, top=top, out=out)
+    for name, t in want.items():
+        assert torch.equal(out[name], t) and bool((room[name][:32] == -7).all()) and bool((room[name][-32:] == -7).all())

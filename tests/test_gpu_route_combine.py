@@ -127,6 +127,32 @@ def test_route_takes_rows_of_wider_ones_and_other_streams():
     assert mmvq.route_topk(x[:0], 8)[0].shape == (0, 8)
 
 
+def test_route_writes_nothing_beside_its_outputs():
+    for n, E, k in ((3, 40, 5), (1, 1000, 32), (6, 8, 1)):
+        x = torch.randn((n, E), device="cuda", generator=torch.Generator("cuda").manual_seed(n))
+        ids, w = mmvq.route_topk(x, k)
+        rooms = [torch.full((n * k + 64,), -7, dtype=t.dtype, device="cuda") for t in (ids, w)]
+        out = [r[32:32 + n * k].view(n, k) for r in rooms]
+        mmvq.route_topk(x, k, out=tuple(out))
+        for r, o, t in zip(rooms, out, (ids, w)):
+            assert torch.equal(o, t) and bool((r[:32] == -7).all()) and bool((r[-32:] == -7).all())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_more_equal_values_than_a_warp_has_lanes(scoring):
+    """Ties of more than 32 experts at the last choice, in and out of groups, and as many choices as there can be."""
+    for E, k, groups, top in ((256, 8, 1, 1), (1024, 32, 1, 1), (96, 32, 1, 1), (512, 32, 4, 2), (40, 32, 1, 1), (33, 32, 1, 1)):
+        x = torch.zeros((6, E), device="cuda")
+        x[1, E // 2:] = 1.0
+        x[2, ::3] = -1.0
+        x[3, E - 1] = 5.0
+        x[4] = (torch.arange(E, device="cuda") // 7).float()
+        x[5, :] = float("-inf")
+        x[5, E - 3:] = 0.5
+        for bias in (None, torch.zeros(E, device="cuda"), (torch.arange(E, device="cuda") % 2) * 0.25):
+            check_route(x, k, scoring, bias, groups, top)
+
+
 # ------------------------------------------------------------------ combine --
 
 def lists(topk, E):

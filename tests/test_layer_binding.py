@@ -37,7 +37,7 @@ def lib():
         (dict(table=None), NULL), (dict(head_dim=96), SHAPE), (dict(head_dim=0), SHAPE), (dict(n_tokens=-1), SHAPE), (dict(n_heads=0), SHAPE),
         (dict(n_heads=1025), SHAPE), (dict(n_kv_heads=-1), SHAPE), (dict(rot_dim=0), SHAPE), (dict(rot_dim=63), SHAPE), (dict(rot_dim=130), SHAPE),
         (dict(n_axes=0), SHAPE), (dict(n_axes=5), SHAPE), (dict(ld_positions=-1), SHAPE), (dict(ldq=-1), SHAPE), (dict(hk=-1), SHAPE),
-        (dict(hyk=-8), SHAPE), (dict(flags=4), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=NAN), SHAPE), (dict(eps=INF), SHAPE),
+        (dict(hyk=-8), SHAPE), (dict(hyq=0), SHAPE), (dict(ldyk=100), SHAPE), (dict(hyk=127), SHAPE), (dict(flags=4), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=NAN), SHAPE), (dict(eps=INF), SHAPE),
         (dict(n_tokens=2 ** 31 - 1), SHAPE), (dict(q=A + 2), ALIGN), (dict(dtype=1, yk=A + 1), ALIGN), (dict(table=A + 4), ALIGN),
         (dict(positions=A + 2), ALIGN), (dict(k_weight=A + 1), ALIGN), (dict(status=A + 1), ALIGN)]),
     ("mmvq_route_topk", ROUTE, [
