@@ -195,6 +195,40 @@ struct Meeting {
   float s[kWarps], t[kWarps];
 };
 
+// A bound that at least `live` of the threads' values reach and few more, -inf where that many are not
+// finite: the values are counted in bins from the least to the largest.
+template <int kWarps>
+__device__ __forceinline__ float bound_of(float value, int live, float2 (&ends)[kWarps], int (&count)[kBins], int warp, int lane) {
+  constexpr int kThreads = 32 * kWarps;
+  const int tid = 32 * warp + lane;
+  const float up = warp_max(value), down = -warp_max(value > -INFINITY ? -value : -INFINITY);
+  __syncthreads();
+  if (lane == 0) ends[warp] = make_float2(down, up);
+  if (tid < kBins) count[tid] = 0;
+  if (kBins > kThreads && tid + kThreads < kBins) count[tid + kThreads] = 0;
+  if (__syncthreads_count(value > -INFINITY) < live) return -INFINITY;
+  float l = INFINITY, h = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    l = fminf(l, ends[w].x);
+    h = fmaxf(h, ends[w].y);
+  }
+  const float per = h - l < INFINITY && h - l > 1e-30f ? (kBins - 0.5f) / (h - l) : 0.0f;  // bins a unit
+  if (value > -INFINITY) atomicAdd(&count[min((int)((value - l) * per), kBins - 1)], 1);
+  __syncthreads();
+  // the highest bin that `live` stand in or above; its lower end less a hundredth of it, for the roundings
+  const int c1 = count[2 * lane + 1], c0 = count[2 * lane];
+  int above = c0 + c1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_down_sync(0xffffffffu, above, o);
+    if (lane + o < 32) above += n;
+  }
+  const int pair = 31 - __clz(__ballot_sync(0xffffffffu, above >= live));
+  const int bin = 2 * pair + __shfl_sync(0xffffffffu, above - c0 >= live, pair);
+  return bin > 0 && per > 0.0f ? fmaxf(l, fmaf((float)bin - 0.01f, 1.0f / per, l)) : l;
+}
+
 // The warps' lists (each its list and the entries waiting) and sums as one, in warp 0's state.  At
 // least `live` entries reach `least`, so what does not goes into the sums; of the others, a handful,
 // each thread takes one and counts those before it.
@@ -366,34 +400,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
 
     if (b == next) {  // 0, 2, 8, 32, ...
       next = max(2, kAgain * next);
-      // a bound that at least `live` of the threads' largest reach
-      const float up = warp_max(largest), down = -warp_max(largest > -INFINITY ? -largest : -INFINITY);
-      if (kWarps > 1) __syncthreads(); else __syncwarp();
-      if (lane == 0) ends[warp] = make_float2(down, up);
-      if (tid < kBins) count[tid] = 0;
-      if (kBins > kThreads && tid + kThreads < kBins) count[tid + kThreads] = 0;
-      if (__syncthreads_count(largest > -INFINITY) >= live) {
-        float l = INFINITY, h = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          l = fminf(l, ends[w].x);
-          h = fmaxf(h, ends[w].y);
-        }
-        const float per = h - l < INFINITY && h - l > 1e-30f ? (kBins - 0.5f) / (h - l) : 0.0f;  // bins a unit
-        if (largest > -INFINITY) atomicAdd(&count[min((int)((largest - l) * per), kBins - 1)], 1);
-        __syncthreads();
-        // the highest bin that `live` stand in or above; its lower end less a hundredth of it, for the roundings
-        const int c1 = count[2 * lane + 1], c0 = count[2 * lane];
-        int above = c0 + c1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int n = __shfl_down_sync(0xffffffffu, above, o);
-          if (lane + o < 32) above += n;
-        }
-        const int pair = 31 - __clz(__ballot_sync(0xffffffffu, above >= live));
-        const int odd = __shfl_sync(0xffffffffu, above - c0 >= live, pair);
-        const int bin = 2 * pair + odd;
-        if (bin > 0 && per > 0.0f) l = fmaxf(l, fmaf((float)bin - 0.01f, 1.0f / per, l));
+      // at least `live` of the threads' largest reach it
+      const float l = bound_of<kWarps>(largest, live, ends, count, warp, lane);
+      if (l > -INFINITY) {
         bound = l;
         if (l > last_v) {
           last_v = look = l;
@@ -508,13 +517,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     }
     cg::this_cluster().sync();  // all are read: the others may leave
     if (rank != 0) return;
-    // what does not reach the best of the lists' last ones is not among the row's
     st.v = -INFINITY;
-    const float last = __shfl_sync(0xffffffffu, wait_v, live - 1);
-    if (lane == 0) meeting.s[warp] = last;
-    __syncthreads();
-    const float least = warp_max(lane < kWarps ? meeting.s[lane] : -INFINITY);
-    __syncthreads();
+    // what cannot be among the row's best: one row of 151936 with 32 alternatives 14.4 us with all lists compared, 9.4 so
+    const float least = bound_of<kWarps>(wait_v, live, ends, count, warp, lane);
     join(meeting, st, wait_v, wait_id, least, live, warp, lane, L);
   }
 
