@@ -651,14 +651,20 @@ ROPE_NO_NORM = 2
 _SCORING = {"softmax": 0, "sigmoid": 1}  # mmvq_scoring
 
 
+_F32, _I32 = torch.float32, torch.int32
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on(t: torch.Tensor, stream):
     """The number of a tensor's device, which has to be the one that the call runs on, and the
     stream's handle."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if dev != (torch.cuda.current_device() if stream is None else stream.device_index):
+    if dev != (_current_device() if stream is None else stream.device_index):
         raise ValueError("the tensors are on another device than the call's stream")
+    if stream is None and _raw_stream is not None:
+        return dev, _raw_stream(dev)
     return dev, _stream(stream)
 
 
@@ -671,10 +677,20 @@ def _plain(t, dtype, shape, dev, name):
     return t.data_ptr()
 
 
+def _list(t, dtype, n, dev, name):
+    """A contiguous tensor [n] of this type on the device (None passes): its address."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or t.dim() != 1 or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] on the call's device")
+    return t.data_ptr()
+
+
 def _layer_status(status, dev):
     if status is None:
         return None
-    if status.dtype is not torch.int32 or status.get_device() != dev or status.numel() < 1:
+    if status.dtype is not _I32 or status.get_device() != dev or status.numel() < 1:
         raise ValueError("status must be an int32 tensor on the call's device")
     return status.data_ptr()
 
@@ -683,12 +699,26 @@ def _rows(t, dtype, shape, dev, name):
     """A [rows, n] tensor with unit inner stride (None passes): its address and row stride."""
     if t is None:
         return None, 0
-    ld, one = t.stride()
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
-            (one != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
-        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} with unit inner stride and rows "
-                         "that do not overlap, on the call's device")
-    return t.data_ptr(), max(ld, shape[1])
+    n, m = shape
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        ld, one = t.stride()
+        if (one == 1 or m == 1) and (ld >= m or n <= 1):
+            return t.data_ptr(), ld if ld >= m else m
+    raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} with unit inner stride and rows "
+                     "that do not overlap, on the call's device")
+
+
+def _heads(x, y, dim, dev, name):
+    """Heads [n, heads, dim] and a tensor like them, both with unit inner stride: the shape, and the
+    addresses with their token and head strides."""
+    shape, dtype = x.shape, x.dtype
+    ld, h, one = x.stride()
+    ldy, hy, one_y = y.stride()
+    if y.shape != shape or shape[2] != dim or y.dtype is not dtype or x.get_device() != dev or \
+            y.get_device() != dev or ((one != 1 or one_y != 1) and shape[0]):
+        raise ValueError(f"{name} and its out must be [tokens, heads, {dim}] tensors of one type with unit "
+                         "inner stride on the call's device")
+    return shape, (x.data_ptr(), ld, h), (y.data_ptr(), ldy, hy)
 
 
 def _inverse_two_pi(bits: int) -> int:
@@ -745,24 +775,26 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     interleaved pairs neighbours instead of halves.  (mmvq_norm_rope)"""
     dev, on = _on(q, stream)
     n, heads, dim = q.shape
-    dtype, _, _, ldq, hq = _kv4_rows(q, 0, dim, dev, "q")
+    number = _DTYPES.get(q.dtype)
+    if number is None:
+        raise ValueError("q must be float32, float16 or bfloat16")
     if out is None:
         yq = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
         yk = None if k is None else _made(stream, torch.empty_like, k,
                                           memory_format=torch.contiguous_format)
     else:
         yq, yk = out
-        if (k is None) != (yk is None):
-            raise ValueError("out must be (q, k), k None where k is")
-    dtype_y, n_y, _, ldyq, hyq = _kv4_rows(yq, heads, dim, dev, "out[0]")
-    kv = ldk = hk = ldyk = hyk = 0
+    _, q_at, yq_at = _heads(q, yq, dim, dev, "q")
+    kv, k_at, yk_at = 0, (None, 0, 0), (None, 0, 0)
     if k is not None:
-        dtype_k, n_k, kv, ldk, hk = _kv4_rows(k, 0, dim, dev, "k")
-        dtype_yk, n_yk, _, ldyk, hyk = _kv4_rows(yk, kv, dim, dev, "out[1]")
-        if dtype_k != dtype or n_k != n or dtype_yk != dtype or n_yk != n:
-            raise ValueError("q, k and out must have the same tokens and type")
-    if dtype_y != dtype or n_y != n:
-        raise ValueError("q, k and out must have the same tokens and type")
+        if yk is None:
+            raise ValueError("out must be (q, k)")
+        shape, k_at, yk_at = _heads(k, yk, dim, dev, "k")
+        if shape[0] != n or k.dtype is not q.dtype:
+            raise ValueError("k must have the tokens and type of q")
+        kv = shape[1]
+    elif yk is not None:
+        raise ValueError("out must be (q, None) where k is None")
     shape, strides = positions.shape, positions.stride()
     axes, ld_pos = (1, 0) if len(shape) == 1 else (shape[0], strides[0])
     if positions.dtype is not torch.int32 or positions.get_device() != dev or shape[-1] != n or \
@@ -774,12 +806,12 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
             not table.is_contiguous():
         raise ValueError("table must be a rope_table on the call's device")
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_NO_NORM if eps is None else 0)
-    _check(lib().mmvq_norm_rope(dtype, q.data_ptr(), ldq, hq, heads, _ptr(k), ldk, hk, kv, dim, n,
-                                positions.data_ptr(), ld_pos, axes, table.data_ptr(), 2 * half,
-                                _plain(q_weight, torch.float32, (dim,), dev, "q_weight"),
-                                _plain(k_weight, torch.float32, (dim,), dev, "k_weight"),
-                                0.0 if eps is None else eps, flags, yq.data_ptr(), ldyq, hyq,
-                                _ptr(yk), ldyk, hyk, _layer_status(status, dev), on), "mmvq_norm_rope")
+    _check(lib().mmvq_norm_rope(number, *q_at, heads, *k_at, kv, dim, n, positions.data_ptr(),
+                                ld_pos, axes, table.data_ptr(), 2 * half,
+                                _list(q_weight, _F32, dim, dev, "q_weight"),
+                                _list(k_weight, _F32, dim, dev, "k_weight"),
+                                0.0 if eps is None else eps, flags, *yq_at, *yk_at,
+                                _layer_status(status, dev), on), "mmvq_norm_rope")
     return yq, yk
 
 
@@ -803,11 +835,11 @@ def route_topk(logits: torch.Tensor, k: int, *, scoring: str = "softmax",
                _made(stream, torch.empty, (n, k), dtype=torch.float32, device=logits.device))
     topk, weights = out
     _check(lib().mmvq_route_topk(dtype, address, ld, n, experts, k, _SCORING[scoring],
-                                 _plain(bias, torch.float32, (experts,), dev, "bias"), n_groups,
+                                 _list(bias, _F32, experts, dev, "bias"), n_groups,
                                  n_groups if top_groups is None else top_groups,
                                  1 if renormalize else 0, scale,
-                                 _plain(topk, torch.int32, (n, k), dev, "out[0]"),
-                                 _plain(weights, torch.float32, (n, k), dev, "out[1]"),
+                                 _plain(topk, _I32, (n, k), dev, "out[0]"),
+                                 _plain(weights, _F32, (n, k), dev, "out[1]"),
                                  _layer_status(status, dev), on), "mmvq_route_topk")
     return topk, weights
 
@@ -835,16 +867,16 @@ def combine_experts(y: torch.Tensor, topk: torch.Tensor, weights: torch.Tensor,
     residual_at, ldr = _rows(residual, dtype, (n, H), dev, "residual")
     shared_at, lds = _rows(shared, dtype, (n, H), dev, "shared")
     out_at, ldo = _rows(out, dtype, (n, H), dev, "out")
-    i32, f32, experts = torch.int32, torch.float32, offsets.numel() - 1
-    if slot_of.numel() < n * k:
+    experts, slots = offsets.numel() - 1, slot_of.numel()
+    if slots < n * k:
         raise ValueError(f"slot_of must hold {n * k} slots")
-    _check(lib().mmvq_combine_experts(number, _plain(y, f32, (positions, H), dev, "y"), positions,
-                                      H, _plain(topk, i32, (n, k), dev, "topk"),
-                                      _plain(weights, f32, (n, k), dev, "weights"), n, k,
-                                      _plain(offsets, i32, (experts + 1,), dev, "offsets"), experts,
-                                      _plain(slot_of, i32, slot_of.shape, dev, "slot_of"),
+    _check(lib().mmvq_combine_experts(number, _plain(y, _F32, (positions, H), dev, "y"), positions,
+                                      H, _plain(topk, _I32, (n, k), dev, "topk"),
+                                      _plain(weights, _F32, (n, k), dev, "weights"), n, k,
+                                      _list(offsets, _I32, experts + 1, dev, "offsets"), experts,
+                                      _list(slot_of, _I32, slots, dev, "slot_of"),
                                       residual_at, ldr, shared_at, lds,
-                                      _plain(shared_gate, f32, (n,), dev, "shared_gate"), out_at,
+                                      _list(shared_gate, _F32, n, dev, "shared_gate"), out_at,
                                       ldo, _layer_status(status, dev), on),
            "mmvq_combine_experts")
     return out
@@ -864,20 +896,19 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, *, 
         raise ValueError("logits must be float32, float16 or bfloat16")
     address, ld = _rows(logits, logits.dtype, (n, vocab), dev, "logits")
     m = 0 if tokens is None else tokens.shape[1]
-    f32, i32 = torch.float32, torch.int32
     if out is None:
         make = lambda shape, kind: _made(stream, torch.empty, shape, dtype=kind,  # noqa: E731
                                          device=logits.device)
-        out = dict(lse=make((n,), f32), entropy=make((n,), f32), logprobs=make((n, m), f32),
-                   top_ids=make((n, top), i32), top_logprobs=make((n, top), f32))
+        out = dict(lse=make((n,), _F32), entropy=make((n,), _F32), logprobs=make((n, m), _F32),
+                   top_ids=make((n, top), _I32), top_logprobs=make((n, top), _F32))
     get = out.get
     _check(lib().mmvq_token_logprobs(dtype, address, ld, n, vocab, scale,
-                                     _plain(tokens, i32, (n, m), dev, "tokens"), m, top,
-                                     _plain(get("lse"), f32, (n,), dev, "lse"),
-                                     _plain(get("entropy"), f32, (n,), dev, "entropy"),
-                                     _plain(get("logprobs"), f32, (n, m), dev, "logprobs"),
-                                     _plain(get("top_ids"), i32, (n, top), dev, "top_ids"),
-                                     _plain(get("top_logprobs"), f32, (n, top), dev,
+                                     _plain(tokens, _I32, (n, m), dev, "tokens"), m, top,
+                                     _list(get("lse"), _F32, n, dev, "lse"),
+                                     _list(get("entropy"), _F32, n, dev, "entropy"),
+                                     _plain(get("logprobs"), _F32, (n, m), dev, "logprobs"),
+                                     _plain(get("top_ids"), _I32, (n, top), dev, "top_ids"),
+                                     _plain(get("top_logprobs"), _F32, (n, top), dev,
                                             "top_logprobs"),
                                      _layer_status(status, dev), on),
            "mmvq_token_logprobs")

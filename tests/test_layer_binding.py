@@ -121,9 +121,10 @@ def launched(monkeypatch):
         seen.append(("launch", args[-1]))
         return mmvq.OK
     monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mmvq, "_current_device", lambda: 0)
     monkeypatch.setattr(mmvq, "lib", lambda: types.SimpleNamespace(**{n: launch for n in mmvq.SIGNATURES}))
     monkeypatch.setattr(mmvq, "_stream", lambda s: s and s.cuda_stream)
+    monkeypatch.setattr(mmvq, "_raw_stream", None)
     return seen
 
 
