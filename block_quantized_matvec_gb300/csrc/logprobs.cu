@@ -616,12 +616,12 @@ int launch_token_logprobs(const TokenLogprobs& a, int dtype, cudaStream_t stream
     // GPU.  (bf16, 4 and 16 warps: 600 rows of 152000 54.6 and 47.9 us, of 50000 28.2 and 26.8; 1000 rows 75.5 and
     // 78.8, 39.7 and 45.5; 152 and 300 rows of 4000 7.6 and 6.6, 7.6 and 8.1.  fp32, 1000 rows of 152000: 125 and 104.)
     if (a.rows > (vectors <= 1024 ? 1 : vectors <= 32768 ? 4 : 8) * kSms) return launch_rows<T, 4, 8>(a, 1, stream);
-    // Few rows: a cluster's CTAs share one, as far as each has a batch and the GPU has places.  (One row of
-    // 152000 bf16 by 1, 2, 4, 8, 16 CTAs: 14.8, 13.3, 11.6, 10.0, 10.8 us; 64 rows by 1, 2, 4: 16.4, 13.8, 15.4;
-    // one row of 16000: 5.8, 8.1.)
+    // Few rows: a cluster's CTAs share one, as far as each has a batch and the GPU has places.  (bf16, by 1, 2, 4, 8,
+    // 16 CTAs: one row of 152000 15.1, 13.2, 11.4, 9.9, 9.1 us, 15 rows 15.3, 13.4, 11.6, 11.1, 15.3, 64 rows 15.7, 14.1, 15.6;
+    // one row of 50000 9.9, 10.6, 9.2, 9.1, 8.9, of 16000 6.4, 8.9, 8.3.)
     int cluster = 1;
     if (vectors > 4096)
-      while (cluster < 16 && vectors > 2500 * cluster && (int64_t)a.rows * 2 * cluster <= (cluster == 8 ? 64 : 128)) cluster *= 2;
+      while (cluster < 16 && vectors > 2000 * cluster && (int64_t)a.rows * 2 * cluster <= (cluster == 8 ? 64 : 128)) cluster *= 2;
     return launch_rows<T, 16, 4>(a, cluster, stream);
   });
 }
