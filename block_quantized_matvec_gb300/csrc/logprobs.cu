@@ -321,15 +321,6 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
   const int vectors = (a.vocab + ahead + V - 1) / V, share = (vectors + cluster - 1) / cluster;
   const int lo = rank * share, hi = min(vectors, lo + share);
   const int whole = (a.vocab + ahead) / V;  // vectors from here on are not
-  // the first given token of this thread, long before it is needed
-  float given = 0.0f;
-  bool is_token = false;
-  if (rank == 0 && tid < a.n_tokens) {
-    const int id = a.tokens[row * a.n_tokens + tid];
-    is_token = id >= 0 && id < a.vocab;
-    if (is_token) given = to_f32(x[id]);
-  }
-
   RowState st;
   st.v = -INFINITY;
   st.id = 0x7fffffff;
@@ -384,6 +375,15 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
   };
 #pragma unroll
   for (int b = 0; b < kStages - 1; ++b) fetch(b);
+  // the first given token of this thread, under way with the first batch
+  float given = 0.0f;
+  bool is_token = false;
+  if (rank == 0 && tid < a.n_tokens) {
+    const int id = a.tokens[row * a.n_tokens + tid];
+    is_token = id >= 0 && id < a.vocab;
+    if (is_token) given = to_f32(x[id]);
+  }
+
 #pragma unroll 1
   for (int b = 0; b < batches; ++b) {
     fetch(b + kStages - 1);
