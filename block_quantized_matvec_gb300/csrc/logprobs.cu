@@ -189,7 +189,7 @@ __device__ __forceinline__ void absorb(RowState& a, float v, int id, int live, i
 // Where a CTA's warps bring their lists together.
 template <int kWarps>
 struct Meeting {
-  int2 entry[64 * kWarps];  // value and id
+  int2 entry[64 * kWarps];  // value and id; before, 64 of each warp that wait to be sorted
   RowPart row;
   int count[kWarps], bad[kWarps];
   float s[kWarps], t[kWarps];
@@ -333,15 +333,18 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
   int next = 0;
   const float one_over_L = 1.0f / L;
   const float2 L2 = make_float2(L, L);
-  // entries that are still to be sorted into the list, one a lane
-  float wait_v = -INFINITY;
-  int wait_id = 0x7fffffff, waiting = 0;
+  // entries that are still to be sorted into the list, this warp's part of the meeting's
+  int2* const wait = meeting.entry + 64 * warp;
+  int waiting = 0;  // below 32 but while a lane is looked at
   auto settle = [&]() {
-    sort(wait_v, wait_id, lane);
-    absorb(st, wait_v, wait_id, live, lane, L);
-    wait_v = -INFINITY;
-    wait_id = 0x7fffffff;
-    waiting = 0;
+    __syncwarp();
+    waiting -= 32;
+    const int2 e = wait[waiting + lane];
+    float v = __int_as_float(e.x);
+    int id = e.y;
+    __syncwarp();
+    sort(v, id, lane);
+    absorb(st, v, id, live, lane, L);
     const float lv = __shfl_sync(0xffffffffu, st.v, live - 1);
     if (lv >= last_v) {
       last_v = lv;
@@ -414,30 +417,25 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     uint32_t lanes = __ballot_sync(0xffffffffu, most >= look);
     if (lanes) {
       __syncwarp();  // the lanes' copies
-      const int base = (lo + b * kThreads * kUnroll + warp * 32) * V - ahead;
+      // a lane's vectors, 32 of their values one a lane
+      T* const near = reinterpret_cast<T*>(mine - lane + lane / V * kThreads) + lane % V;
+      const int id0 = (lo + b * kThreads * kUnroll + warp * 32 + lane / V * kThreads) * V - ahead + lane % V;
 #pragma unroll 1
-      do {  // a lane's vectors, 32 of their values one a lane
+      do {
         const int src = __ffs(lanes) - 1;
         lanes &= lanes - 1;
-        T* p = reinterpret_cast<T*>(mine + src - lane + lane / V * kThreads) + lane % V;
 #pragma unroll
-        for (int g = 0; g < kUnroll * V; g += 32, p += 32 * kThreads) {
+        for (int g = 0; g < kUnroll * V; g += 32) {
+          T* const p = near + src * V + g * kThreads;
           const float v = kUnroll * V >= 32 || lane < kUnroll * V ? to_f32(*p) : -INFINITY;
-          uint32_t who = __ballot_sync(0xffffffffu, v >= last_v && v < INFINITY);
-#pragma unroll 1
-          while (who) {
-            const int j = __ffs(who) - 1;
-            who &= who - 1;
-            const float c = __shfl_sync(0xffffffffu, v, j);
-            if (lane == waiting) {
-              wait_v = c;
-              wait_id = base + ((g + j) / V * kThreads + src) * V + j % V;
+          const uint32_t who = __ballot_sync(0xffffffffu, v >= last_v);
+          if (who) {
+            if (v >= last_v) {
+              wait[waiting + __popc(who & ((1u << lane) - 1u))] = make_int2(__float_as_int(v), id0 + src * V + g * kThreads);
+              *p = from_f32<T>(-INFINITY);
             }
-            if (lane == j) *p = from_f32<T>(-INFINITY);
-            if (++waiting == 32) {
-              settle();
-              who &= __ballot_sync(0xffffffffu, v >= last_v);
-            }
+            waiting += __popc(who);
+            if (waiting >= 32) settle();
           }
         }
       } while (lanes);
@@ -488,6 +486,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     }
   }
 
+  __syncwarp();
+  float wait_v = -INFINITY;
+  int wait_id = 0x7fffffff;
+  if (lane < waiting) {
+    wait_v = __int_as_float(wait[lane].x);
+    wait_id = wait[lane].y;
+  }
   join(meeting, st, wait_v, wait_id, bound, live, warp, lane, L);
   if (cluster > 1) {
     if (tid == 0) {
