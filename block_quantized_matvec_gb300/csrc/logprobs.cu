@@ -14,9 +14,9 @@
 // of the sums, one that leaves it is added to them, also where lists are merged at
 // the end; what remains besides the sums is the list, whose first is m.
 //
-// What it spends: about 44 instructions for 8 logits of 16 bits (a maximum in
+// What it spends: about 42 instructions for 8 logits of 16 bits (a maximum in
 // pairs, conversions, two packed fp32 operations and an ex2 each), so the row comes
-// through a ring of asynchronous copies, each thread's own, and CTAs are small: four
+// through a ring of asynchronous copies, each thread's own, and CTAs are small: six
 // rows an SM, which wait for one another at no barrier.  Lists are entered rarely:
 // from its first batch of vectors, and again from three times as many and so on, each
 // CTA finds a bound that `live` values reach, by counting its threads' largest ones
@@ -27,6 +27,9 @@
 //
 // A row is shared out to the CTAs of a cluster where rows are few; the first one
 // reads the others' lists and sums from their shared memory.
+//
+// Measured with 20 alternatives: 2048 x 151936 bf16 117 us (5.3 TB/s; instructions
+// bound it, 58% of the issue slots), 1 x 151936 fp32 9 us (latency).
 #include <cfloat>
 
 #include <cooperative_groups.h>

@@ -19,7 +19,7 @@
 // as many experts as are needed reach the need-th of those, and the few that do are
 // put one to a lane, which counts how many come before it.  Where many are equal and
 // more than 32 reach it, the best is taken k times over.  (8192 tokens, 8 of 256 in
-// groups: every lane's experts sorted and the best taken k times 17.3 us.)
+// groups: 15.6 us; with every lane's experts sorted and the best taken k times 17.3.)
 #include <cfloat>
 
 #include "layer.cuh"
