@@ -9,16 +9,16 @@
 // Which expert comes first is decided as in 64 bits.  Without bias and groups
 // the logits' own order decides, exactly.  Otherwise values are made in fp32,
 // whose error is at most kUlps of the score and of the sum; where two neighbours
-// in the order (or the last group in and the first one out) lie nearer to one
-// another than that, the warp makes the values that can matter again in 64 bits
-// and chooses by those.
+// in the order, whose logits or biases differ (or the last group in and the first one
+// out), lie nearer to one another than that, the warp makes the values that can matter
+// again in 64 bits and chooses by those.
 //
 // A warp per token; lane L holds the experts L * kPer .. + kPer - 1, so a lower
 // lane means a lower id.  Bound by instructions, not by the few bytes.  The lanes'
-// best ones are sorted (values alone: a shuffle and a minimum or maximum a step);
-// as many experts as are needed reach the need-th of those, and the few that do are
-// put one to a lane, which counts how many come before it.  Where many are equal and
-// more than 32 reach it, the best is taken k times over.  (8192 tokens, 8 of 256 in
+// best ones are sorted (values alone: a shuffle and a minimum or maximum a step); at
+// least k experts reach the k-th of those, and the few that do, within their errors,
+// are put one to a lane, which counts how many come before it.  Where more than 32
+// do, the best is taken k times over first.  (8192 tokens, 8 of 256 in
 // groups: 15.6 us; with every lane's experts sorted and the best taken k times 17.3.)
 #include <cfloat>
 
@@ -308,25 +308,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
     }
   }
 
-  // the k best, in order, and the one after the last; lane j keeps choice j
-  int mine = -1, next = -1;
-  float mv = -INFINITY, nv = -INFINITY;
-  const int need = exact ? a.k : a.k + 1;
-  int n = 33;  // experts that reach the bound
-  if (need <= 32) {
-    // as many lanes' best ones reach the need-th largest of them
-    float best = v[0];
+  // what a value's error stays within; with a bias an expert of any score, up to 1, can stand at a value
+  auto error = [&](float value) { return kUlps * ((a.bias ? 1.0f : fabsf(value)) + fabsf(value)) + 0x1p-120f; };
+
+  // As many lanes' best ones reach the k-th largest of them, and so do all that can be among the k, within their errors.
+  float best = v[0];
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) best = fmaxf(best, v[i]);
+  for (int i = 1; i < kPer; ++i) best = fmaxf(best, v[i]);
 #pragma unroll
-    for (int m = 2; m <= 32; m *= 2)
+  for (int m = 2; m <= 32; m *= 2)
 #pragma unroll
-      for (int o = m / 2; o; o >>= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, best, o);
-        best = !(lane & o) == !(lane & m) ? fmaxf(best, other) : fminf(best, other);
-      }
-    const float bound = fmaxf(__shfl_sync(0xffffffffu, best, need - 1), -FLT_MAX);
-    n = 0;
+    for (int o = m / 2; o; o >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, best, o);
+      best = !(lane & o) == !(lane & m) ? fmaxf(best, other) : fminf(best, other);
+    }
+  float bound = __shfl_sync(0xffffffffu, best, a.k - 1);
+  auto collect = [&]() {
+    bound = fmaxf(bound, -FLT_MAX);
+    if (!exact && bound < INFINITY) bound = fmaxf(bound - 3.0f * error(bound), -FLT_MAX);  // a bias can be infinite
+    int n = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint32_t m = __ballot_sync(0xffffffffu, v[i] >= bound);
@@ -335,7 +335,41 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
       n += __popc(m);
     }
     __syncwarp();
+    return n;
+  };
+  int n = collect();
+
+  int mine = -1;  // lane j's choice j
+  if (n > 32) {
+    // Fewer lanes than k have any, or many are equal: the best of all lanes, k times, for the k-th itself.
+    float left[kPer], kth = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) left[i] = v[i];
+#pragma unroll 1
+    for (int j = 0; j < a.k; ++j) {
+      float m = left[0];
+      int at = 0;
+#pragma unroll
+      for (int i = 1; i < kPer; ++i)
+        if (left[i] > m) m = left[i], at = i;
+      kth = warp_max(m);
+      if (kth == -INFINITY) break;
+      const int who = __ffs(__ballot_sync(0xffffffffu, m == kth)) - 1;
+      const int id = __shfl_sync(0xffffffffu, first + at, who);
+      if (lane == j) mine = id;
+      if (lane == who) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i == at) left[i] = -INFINITY;
+      }
+    }
+    if (!exact) {
+      __syncwarp();
+      bound = kth;
+      n = collect();
+    }
   }
+  bool close = n > 32 && !exact;  // two that are too near to tell
   if (n <= 32) {  // mostly: one a lane, which counts those before it
     const int2 e = found[warp][lane < n ? lane : 0];
     int rank = 0;
@@ -347,63 +381,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
     __syncwarp();
     if (lane < n) found[warp][rank] = e;
     __syncwarp();
-    const int2 c = found[warp][lane], after = found[warp][a.k & 31];
-    if (lane < min(n, a.k)) mine = c.y, mv = __int_as_float(c.x);
-    if (a.k < n) next = after.y, nv = __int_as_float(after.x);
-  } else {
-    float left[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) left[i] = v[i];
-#pragma unroll 1
-    for (int j = 0; j < need; ++j) {
-      float m = left[0];
-      int at = 0;
-#pragma unroll
-      for (int i = 1; i < kPer; ++i)
-        if (left[i] > m) m = left[i], at = i;
-      const float b = warp_max(m);
-      if (b == -INFINITY) break;
-      const int who = __ffs(__ballot_sync(0xffffffffu, m == b)) - 1;
-      const int id = __shfl_sync(0xffffffffu, first + at, who);
-      if (j == a.k) {
-        nv = b;
-        next = id;
-      } else if (lane == j) {
-        mine = id;
-        mv = b;
-      }
-      if (lane == who) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (i == at) left[i] = -INFINITY;
-      }
+    const int2 c = found[warp][lane < n ? lane : 0];
+    mine = lane < min(n, a.k) ? c.y : -1;
+    if (!exact) {
+      // Neighbours in the order, down to the last that is within the errors of the last choice.  Equal logits
+      // with equal biases are equal in 64 bits too; what comes after them is the last one's neighbour.
+      const float cv = __int_as_float(c.x), next = __shfl_down_sync(0xffffffffu, cv, 1);
+      const float last = __shfl_sync(0xffffffffu, cv, max(min(n, a.k) - 1, 0));
+      const int id = __shfl_down_sync(0xffffffffu, c.y, 1);
+      if (lane + 1 < n && cv - next <= error(cv) + error(next) && (lane < a.k || last - next <= error(last) + error(next)))
+        close = to_f32(row[c.y]) != to_f32(row[id]) || (a.bias && a.bias[c.y] != a.bias[id]);
     }
   }
-  float mx = mine >= 0 ? to_f32(row[mine]) : -INFINITY;
-  if (!exact) {
-    const float fv = __shfl_down_sync(0xffffffffu, mv, 1);
-    const int fi = __shfl_down_sync(0xffffffffu, mine, 1);
-    const float v1 = lane == a.k - 1 ? nv : fv;
-    const int i1 = lane == a.k - 1 ? next : fi;
-    bool close = false;
-    if (mine >= 0 && i1 >= 0) {
-      const float x1 = to_f32(row[i1]), b0 = a.bias ? a.bias[mine] : 0.0f, b1 = a.bias ? a.bias[i1] : 0.0f;
-      const float slack = kUlps * (score(mx) + fabsf(mv) + score(x1) + fabsf(v1)) + 0x1p-120f;
-      close = mv - v1 <= slack && !(mx == x1 && b0 == b1);
-    }
-    if (__any_sync(0xffffffffu, close)) {
-      // what can still be among the k: everything within the errors of the last choice
-      const float last = __shfl_sync(0xffffffffu, mv, a.k - 1), least = last - 2.0f * kUlps * (2.0f + 2.0f * fabsf(last));
-      float may[kPer], cut[kPer];
+  if (__any_sync(0xffffffffu, close)) {
+    float may[kPer], cut[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        may[i] = v[i];
-        cut[i] = least < INFINITY ? least : -INFINITY;  // also where a bias is infinite
-      }
-      mine = choose_wide<T, kPer>(a, RouteRow{row, lane, group_size, softmax_top, total}, may, cut, scratch);
-      mx = mine >= 0 ? to_f32(row[mine]) : -INFINITY;
+    for (int i = 0; i < kPer; ++i) {
+      may[i] = v[i];
+      cut[i] = bound;
     }
+    mine = choose_wide<T, kPer>(a, RouteRow{row, lane, group_size, softmax_top, total}, may, cut, scratch);
   }
+  const float mx = mine >= 0 ? to_f32(row[mine]) : -INFINITY;
 
   float w = 0.0f;
   if (a.renormalize) {

@@ -82,6 +82,22 @@ def test_values_that_32_bits_cannot_tell_apart(scoring):
         check_route(near.cuda(), 8, scoring, torch.zeros(E).cuda(), groups, top)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_values_alike_of_scores_that_are_not(scoring):
+    """Half of the experts with small scores and exact values, half with large scores that a bias brings to the same
+    values: the errors of the second lie between the gaps of the first."""
+    rng = np.random.default_rng(11)
+    for E in (16, 64, 256):
+        x = rng.normal(size=(60, E)).astype(np.float32)
+        x[:, ::2] = np.float32(-7) + rng.integers(0, 4, (60, E // 2)).astype(np.float32) * np.float32(2.0 ** -21)
+        xd = x.astype(np.float64)
+        s = 1 / (1 + np.exp(-xd)) if scoring == "sigmoid" else np.exp(xd) / np.exp(xd).sum(-1, keepdims=True)
+        for row in range(0, 60, 12):
+            b = np.where(np.arange(E) % 2, s[row, 0] - s[row], 0.0).astype(np.float32)
+            check_route(torch.from_numpy(x).cuda(), min(8, E // 2), scoring, torch.from_numpy(b).cuda())
+            check_route(torch.from_numpy(x).cuda(), 4, scoring, torch.from_numpy(b).cuda(), 4, 2)
+
+
 def test_masked_experts_and_rows():
     gen = torch.Generator("cuda").manual_seed(3)
     x = torch.randn((12, 64), device="cuda", generator=gen)
