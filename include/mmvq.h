@@ -585,7 +585,8 @@ MMVQ_API int mmvq_route_topk(int dtype, const void* logits, int64_t ld, int n_to
  * position of slot t*k + j in the lists of the same topk (token_offsets
  * [n_experts+1], slot_of, from mmvq_route_groups or mmvq_expert_ffn).  residual,
  * shared and out are of dtype, ldr/lds/ldo >= H elements from row to row;
- * residual and shared may be NULL, and out may be either of them.  Slots with
+ * residual and shared may be NULL, and out may be either of them, but not overlap
+ * y nor any other input.  Slots with
  * expert -1 add nothing; other ids outside [0, n_experts), and slots that the
  * lists do not hold, add nothing and set *status to MMVQ_ERR_ROUTING.
  * Limits: n_tokens*k <= 65536, k <= 256, n_experts <= 4096, H <= 2^24.
