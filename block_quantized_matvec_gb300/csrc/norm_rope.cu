@@ -31,12 +31,15 @@ __device__ __forceinline__ float2 turn(uint64_t phase) {
   return quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
-// cos and sin of pair i's angle at token t; no angle where its axis is none.
+// What stands in the place of a cosine where a pair does not turn.
+constexpr float kNoTurn = 2.0f;
+
+// cos and sin of pair i's angle at token t; kNoTurn where its axis is none.
 __device__ __forceinline__ float2 pair_turn(const NormRope& a, int i, int64_t t) {
   const int64_t axis = a.table[a.rot / 2 + i];
   if (axis < 0 || axis >= a.n_axes) {
     if (a.status) *a.status = MMVQ_ERR_SHAPE;
-    return make_float2(1.0f, 0.0f);
+    return make_float2(kNoTurn, 0.0f);
   }
   return turn((uint64_t)a.table[i] * (uint64_t)(int64_t)a.positions[axis * a.ld_positions + t]);
 }
@@ -82,9 +85,11 @@ __global__ void __launch_bounds__(128) norm_rope_any_kernel(const NormRope a) {
     const int i = lane + 32 * j;
     if (i < half) {
       const float2 w = pair_turn(a, i, t);
-      const float p = v[j][0] * w.x - v[j][1] * w.y, q = v[j][0] * w.y + v[j][1] * w.x;
-      v[j][0] = p;
-      v[j][1] = q;
+      if (w.x != kNoTurn) {
+        const float p = v[j][0] * w.x - v[j][1] * w.y, q = v[j][0] * w.y + v[j][1] * w.x;
+        v[j][0] = p;
+        v[j][1] = q;
+      }
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) y[at[j][e]] = from_f32<T>(v[j][e]);
@@ -135,8 +140,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const
   __syncwarp();
 
   // weights of values i of v0 and v1, and with them the turn of their pair:
-  // out0 = x0 * aa - x1 * ab, out1 = x0 * ba + x1 * bb
+  // out0 = x0 * aa - x1 * ab, out1 = x0 * ba + x1 * bb.  A value that does not turn takes nothing of its
+  // neighbour, not even 0 times what is infinite or no number.
   float aa[V], ab[V], ba[V], bb[V];
+  uint32_t turned = 0;    // bit i: pair i turns
+  bool all_turn = false;  // all pairs of the warp's lanes do
   auto weigh = [&](const float* weight) {
     float w[2 * V];
 #pragma unroll
@@ -152,13 +160,15 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int pair = !kInterleaved ? u * V + i : i < V / 2 ? v0 / 2 + i : v1 / 2 + i - V / 2;
-      const float2 c = pair < half ? turns[warp][pair] : make_float2(1.0f, 0.0f);
+      float2 c = pair < half ? turns[warp][pair] : make_float2(kNoTurn, 0.0f);
+      if (c.x != kNoTurn) turned |= 1u << i; else c.x = 1.0f;
       const float w0 = kInterleaved ? w[2 * i] : w[i], w1 = kInterleaved ? w[2 * i + 1] : w[V + i];
       aa[i] = w0 * c.x;
       ab[i] = w1 * c.y;
       ba[i] = w0 * c.y;
       bb[i] = w1 * c.x;
     }
+    all_turn = __all_sync(0xffffffffu, turned == (1u << V) - 1u);
   };
 
 #pragma unroll 1
@@ -180,12 +190,16 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const
       scale = rsqrtf(sum * (1.0f / D) + a.eps);
     }
     float out[2 * V];
+    auto rotate = [&](auto whole) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int i0 = kInterleaved ? 2 * i : i, i1 = kInterleaved ? 2 * i + 1 : V + i;
-      out[i0] = scale * (v[i0] * aa[i] - v[i1] * ab[i]);
-      out[i1] = scale * (v[i0] * ba[i] + v[i1] * bb[i]);
-    }
+      for (int i = 0; i < V; ++i) {
+        const int i0 = kInterleaved ? 2 * i : i, i1 = kInterleaved ? 2 * i + 1 : V + i;
+        const bool with = whole.value || ((turned >> i) & 1);
+        out[i0] = scale * (with ? v[i0] * aa[i] - v[i1] * ab[i] : v[i0] * aa[i]);
+        out[i1] = scale * (with ? v[i0] * ba[i] + v[i1] * bb[i] : v[i1] * bb[i]);
+      }
+    };
+    if (all_turn) rotate(std::true_type{}); else rotate(std::false_type{});
     const RopeHeads& r = step < q_steps ? a.q : a.k;
     const int h = (step < q_steps ? step : step - q_steps) * kRows + mine;
     if (h < r.heads) {
