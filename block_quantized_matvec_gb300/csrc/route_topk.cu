@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
     const bool kept = real && rank < a.top_groups;
     const float in = -warp_max(kept ? -two : -INFINITY), out = warp_max(real && !kept ? two : -INFINITY);
     uint32_t keep = __ballot_sync(0xffffffffu, kept);  // bit of a group's lanes, or of the group
-    if (out > -INFINITY && in - out <= 2.0f * kUlps * warp_max(size)) {  // too near to tell
+    // too near to tell, or a sum of two biases that fp32 does not hold
+    const bool beyond = real && b1 > -INFINITY && !(fabsf(two) < INFINITY);
+    if (__any_sync(0xffffffffu, beyond) || (out > -INFINITY && in - out <= 2.0f * kUlps * warp_max(size))) {
       float may[kPer], cut[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
