@@ -537,6 +537,22 @@ int mmvq_read_device_fault(int* fault, mmvq_stream_t stream) {
 
 // ------------------------------------- the layer's steps between the products
 
+// Whether no two rows of dim values, `ld` elements from token to token and `h` from head to head,
+// share any.  Mostly a token's heads, or a head's tokens, lie within a stride of the others; else,
+// of two heads i apart, those tokens lie nearest that are i * h / ld apart.
+static bool rows_lie_apart(int64_t ld, int64_t h, int n_tokens, int n_heads, int dim) {
+  if ((n_tokens > 1 && n_heads > 0 && ld < dim) || (n_heads > 1 && h < dim)) return false;
+  if (n_tokens <= 1 || n_heads <= 1) return true;
+  if (ld >= (__int128)(n_heads - 1) * h + dim || h >= (__int128)(n_tokens - 1) * ld + dim) return true;
+  for (int i = 1; i < n_heads; ++i) {
+    const __int128 far = (__int128)i * h, down = far / ld < n_tokens - 1 ? far / ld : n_tokens - 1;
+    if (far - down * ld < dim) return false;
+    if (down < n_tokens - 1 && (down + 1) * ld - far < dim) return false;
+    if (down == n_tokens - 1) break;  // all tokens lie before this head's first one, and the next heads'
+  }
+  return true;
+}
+
 int mmvq_norm_rope(int dtype, const void* q, int64_t ldq, int64_t hq, int n_heads, const void* k,
                    int64_t ldk, int64_t hk, int n_kv_heads, int head_dim, int n_tokens,
                    const int32_t* positions, int64_t ld_positions, int n_axes,
@@ -553,9 +569,8 @@ int mmvq_norm_rope(int dtype, const void* q, int64_t ldq, int64_t hq, int n_head
   if (ldq < 0 || hq < 0 || ldk < 0 || hk < 0 || ldyq < 0 || hyq < 0 || ldyk < 0 || hyk < 0)
     return MMVQ_ERR_SHAPE;
   if ((int64_t)n_tokens * (n_heads + n_kv_heads) >= (int64_t)1 << 32) return MMVQ_ERR_SHAPE;
-  // rows that are written lie apart
-  if ((n_tokens > 1 && (ldyq < head_dim || (n_kv_heads > 0 && ldyk < head_dim))) ||
-      (n_heads > 1 && hyq < head_dim) || (n_kv_heads > 1 && hyk < head_dim))
+  if (!rows_lie_apart(ldyq, hyq, n_tokens, n_heads, head_dim) ||
+      !rows_lie_apart(ldyk, hyk, n_tokens, n_kv_heads, head_dim))
     return MMVQ_ERR_SHAPE;
   if (flags & ~(MMVQ_ROPE_INTERLEAVED | MMVQ_ROPE_NO_NORM)) return MMVQ_ERR_SHAPE;
   if (!(eps >= 0.0f) || !(eps < INFINITY)) return MMVQ_ERR_SHAPE;

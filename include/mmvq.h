@@ -530,7 +530,7 @@ MMVQ_API int64_t mmvq_kv4_attention_workspace_bytes(int head_dim);
  * position.  q [n_tokens][n_heads][head_dim] and k [n_tokens][n_kv_heads]
  * [head_dim], ldq/ldk elements from token to token and hq/hk from head to head
  * (>= 0, the values of a head side by side); yq, yk the same with their own
- * strides, whose rows lie apart (MMVQ_ERR_SHAPE where a stride is below head_dim);
+ * strides, whose rows lie apart (MMVQ_ERR_SHAPE where two of one tensor share a value);
  * they may be q and k themselves (same strides; no other overlap).
  * n_kv_heads = 0: queries alone.  z = x / sqrt(mean(x^2) + eps) * weight over
  * the head's values, their squares within fp32 (q_weight, k_weight: fp32 [head_dim], NULL for ones;
