@@ -656,13 +656,15 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 
 
 def _on(t: torch.Tensor, stream):
-    """The number of a tensor's device, which has to be the one that the call runs on, and the
-    stream's handle."""
+    """The number of a tensor's device, which has to be the current one (a launch elsewhere fails)
+    and the stream's, and the stream's handle."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if dev != (_current_device() if stream is None else stream.device_index):
+    if stream is not None and dev != stream.device_index:
         raise ValueError("the tensors are on another device than the call's stream")
+    if dev != _current_device():
+        raise ValueError("the tensors are on another device than the current one (torch.cuda.device)")
     if stream is None and _raw_stream is not None:
         return dev, _raw_stream(dev)
     return dev, _stream(stream)
