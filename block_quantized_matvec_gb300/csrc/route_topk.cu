@@ -8,10 +8,14 @@
 //
 // Which expert comes first is decided as in 64 bits.  Without bias and groups
 // the logits' own order decides, exactly.  Otherwise values are made in fp32,
-// whose error is at most kUlps of the score and of the sum; where two neighbours
-// in the order, whose logits or biases differ (or the last group in and the first one
-// out), lie nearer to one another than that, the warp makes the values that can matter
-// again in 64 bits and chooses by those.
+// whose error is at most kUlps of the score and of the sum, but for the rounding
+// of a softmax's argument x - top, up to 64 half units where they are far apart.
+// That one needs no room: without bias, as rounding keeps the order, two arguments are
+// in the order of their logits or equal, and what is equal is too near to tell; with a
+// bias, and for groups, errors count absolutely, and d exp(-d) stays below 0.37.
+// Where two neighbours in the order, whose logits or biases differ (or the last group
+// in and the first one out), lie nearer to one another than that, the warp makes the
+// values that can matter again in 64 bits and chooses by those.
 //
 // A warp per token; lane L holds the experts L * kPer .. + kPer - 1, so a lower
 // lane means a lower id.  Bound by instructions, not by the few bytes.  The lanes'
@@ -182,7 +186,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const __gr
   auto score = [&](float l) { return a.sigmoid ? sigmoid(l) : __fdividef(expf(l - softmax_top), total); };
   const bool grouped = a.top_groups < a.n_groups;
   const bool exact = !a.bias && !grouped;  // the logits' order is the scores'
-  // what a value's fp32 error stays within: exp, sum, quotient and the sum with the bias
+  // what a value's fp32 error stays within, its argument's rounding aside: exp (2 half units), the sum (kPer + 5
+  // additions, its terms' own 2, their arguments' 7: the mean of d is at most log 1024), the quotient 4, the sum with
+  // the bias 1, and what is left of the argument's own 1
   constexpr float kUlps = (kPer + 24) * 0x1p-24f;
 
   float x[kPer];
