@@ -18,8 +18,8 @@
 // pairs, conversions, two packed fp32 operations and an ex2 each), so the row comes
 // through a ring of asynchronous copies, each thread's own, and CTAs are small: six
 // rows an SM, which wait for one another at no barrier.  Lists are entered rarely:
-// from its first batch of vectors, and again from three times as many and so on, each
-// CTA finds a bound that `live` values reach, by counting its threads' largest ones
+// from its first batch of vectors, and again from 3, 9, 33, ... of them, each CTA finds
+// a bound that `live` values reach, by counting its threads' largest ones
 // in 64 bins; a warp looks closer only where the largest of a batch reaches the bound
 // or its list's last, and then at a lane's vectors one value a lane.  (Code for that
 // unrolled over the batch's values took 688 us for 2048 rows of 151936 in place of
@@ -50,7 +50,7 @@ constexpr float kFar = 0x1p100f;  // |x log2(e)| from which on C is taken off fi
 constexpr int kStages = 2;   // batches of the ring
 constexpr int kBins = 64;    // of the bound's count
 constexpr int kLeast = 8;    // a list's entries, however few are asked for
-constexpr int kAgain = 4;    // the bound is found again after three times as many batches as before
+constexpr int kAgain = 4;    // the bound is found in batch 0, 2, and each time that many times as far on
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
@@ -481,7 +481,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
       }
       st.s2 = __fadd2_rn(st.s2, s2);
       st.t2 = __fadd2_rn(st.t2, t2);
-    } else {  // logits so large, or a scale so small, that the type has no such value
+    } else {
+      // Logits so large, or a scale so small, that the type has no such value: for fp16 scales below about 0.0016
+      // (2048 x 151936 at 0.0015: 247 us, at 1: 113; 301 x 50021: 20.9 and 15.7).
 #pragma unroll 1
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll 1

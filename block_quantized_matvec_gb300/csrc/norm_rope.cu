@@ -7,7 +7,8 @@
 // turns, and sin and cos are taken of a remainder within an eighth of a turn.
 //
 // Rows are read and written once and little is computed, so memory bounds the
-// kernel where there are many (16385 tokens of 40 x 128 bf16: 55.5 us, 6.05 TB/s).
+// kernel where there are many (16385 tokens of 40 x 128 bf16, in a replayed graph: 53.4 us,
+// 6.3 TB/s; neighbours 52.7; fp32 103.5 and 103.2).
 // norm_rope_vec_kernel: a lane holds two 16-byte vectors of a row, where i turns with
 // i + rot/2 two that are rot/2 apart, so that D / (2 * 16 bytes) lanes share a row and
 // only the mean square crosses lanes.  A warp stays with a token: its lanes share out
@@ -15,7 +16,9 @@
 // pairs for all heads, four numbers a pair; rows come through a ring of asynchronous
 // copies (80.7 us with one row's loads ahead).
 // Halves that are no multiple of a vector and rows off 16 bytes take
-// norm_rope_any_kernel: a warp per row, two values at a time.
+// norm_rope_any_kernel: a warp per row, two values at a time, its token's angles made
+// for every head anew, so instructions bound it (the same prompt with 84 values turning
+// 226 us).  Few tokens cost it nothing (64 of them 2.5 us, by vectors 2.9).
 #include "layer.cuh"
 #include "typed.cuh"
 
@@ -141,7 +144,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 3) norm_rope_vec_kernel(const
 
   // weights of values i of v0 and v1, and with them the turn of their pair:
   // out0 = x0 * aa - x1 * ab, out1 = x0 * ba + x1 * bb.  A value that does not turn takes nothing of its
-  // neighbour, not even 0 times what is infinite or no number.
+  // neighbour, not even 0 times what is infinite or no number (7596 tokens of 26 x 256 bf16, 64 of them
+  // turning, 35.7 -> 36.5 us; a branch by lanes in place of the selection 37.0).
   float aa[V], ab[V], ba[V], bb[V];
   uint32_t turned = 0;    // bit i: pair i turns
   bool all_turn = false;  // all pairs of the warp's lanes do

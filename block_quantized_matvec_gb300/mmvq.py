@@ -773,7 +773,7 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     """RMS norm of every head of q [n, heads, head_dim] and k [n, kv heads, head_dim] (None:
     queries alone), times q_weight and k_weight [head_dim] fp32 (None: ones), then the rotation by
     the token's position -> (q, k), contiguous or written to out (which may be q and k themselves).
-    positions: int32 [n], or [axes, n]; table: rope_table; eps=None leaves the norm out;
+    positions: int32 [n], or [axes, n]; table: rope_table; eps=None leaves the norm and the weights out;
     interleaved pairs neighbours instead of halves.  (mmvq_norm_rope)"""
     dev, on = _on(q, stream)
     n, heads, dim = q.shape

@@ -610,7 +610,9 @@ MMVQ_API int mmvq_combine_experts(int dtype, const float* y, int64_t n_positions
  * logprobs -inf, entropy 0, no alternatives.  A row with NaN or +inf: NaN, ids
  * -1, and *status is set to MMVQ_ERR_VALUE.  A token outside [0, vocab) has
  * logprob NaN and sets *status to MMVQ_ERR_ROUTING.
- * Limits: vocab <= 2^24, n_tokens <= 65536, top <= 32, 2^-64 <= scale < 2^64.
+ * Limits: vocab <= 2^24, n_tokens <= 65536, top <= 32, 2^-64 <= scale < 2^64.  Few rows
+ * of a long vocabulary are shared out to clusters of up to 16 CTAs: the whole GPU places
+ * them, a part of one that does not answers MMVQ_ERR_CUDA.
  */
 MMVQ_API int mmvq_token_logprobs(int dtype, const void* logits, int64_t ld, int n_rows, int vocab,
                                  float scale, const int32_t* tokens, int n_tokens, int top,
