@@ -10,7 +10,7 @@
 // eight) in order, one a lane, and the sums over all others, of 2^y and 2^y y with
 // y = (x - C) log2(e) - R: R is near the list's last, so that terms are summed at
 // their own size also where the first stands far above, and C is 0 but where
-// x log2(e) would leave fp32's range.  A logit that enters the list is taken out
+// x log2(e) is so large that R would be a unit off; there C is the list's last and R 0.  A logit that enters the list is taken out
 // of the sums, one that leaves it is added to them, also where lists are merged at
 // the end; what remains besides the sums is the list, whose first is m.
 //
@@ -46,7 +46,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // How far above R the list's last may stand, in powers of two, before R follows:
 // the entropy's sum cancels by that much at most.
 constexpr float kSlack = 3.0f;
-constexpr float kFar = 0x1p100f;  // |x log2(e)| from which on C is taken off first
+// |x log2(e)| from which on C is taken off first: R, rounded, is off by half its unit, 1 from here on, which the
+// entropy's sum cancels by; 128 of them, from 2^31 on, are an exponent that fp32 does not hold.
+constexpr float kFar = 0x1p24f;
 constexpr int kStages = 2;   // batches of the ring
 constexpr int kBins = 64;    // of the bound's count
 constexpr int kLeast = 8;    // a list's entries, however few are asked for
@@ -446,11 +448,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
     }
 
     if (st.R == -INFINITY) continue;  // all there was is in the list
-    // what is so small that it adds nothing, and -inf, enter as one finite value of that kind
-    const float2 R2 = make_float2(-st.R, -st.R);
-    const T least = from_f32<T>(fmaxf((st.R - 160.0f) * one_over_L, std::is_same<T, __half>::value ? -65504.0f : -3.0e38f));
-    if (st.C == 0.0f && fmaf(to_f32(least), L, -st.R) <= -150.0f) {
-      // a batch's sums by themselves: however long the row, few additions follow one another
+    // what is so small that it adds nothing, and -inf, enter as one finite value of that kind; far from 0 a 128th below C is
+    const bool far = st.C != 0.0f;
+    const float2 R2 = make_float2(-st.R, -st.R), C2 = make_float2(-st.C, -st.C);
+    const T least = from_f32<T>(fmaxf(far ? st.C - fabsf(st.C) * 0x1p-7f : (st.R - 160.0f) * one_over_L,
+                                      std::is_same<T, __half>::value ? -65504.0f : -3.0e38f));
+    // a batch's sums by themselves: however long the row, few additions follow one another
+    auto stream = [&](auto is_far) {
       float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -473,7 +477,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
         }
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-          const float2 y = __ffma2_rn(make_float2(v[i], v[i + 1]), L2, R2);
+          const float2 x2 = make_float2(v[i], v[i + 1]);
+          const float2 y = is_far.value ? __fmul2_rn(__fadd2_rn(x2, C2), L2) : __ffma2_rn(x2, L2, R2);
           const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
           s2 = __fadd2_rn(s2, e);
           t2 = __ffma2_rn(e, y, t2);
@@ -481,6 +486,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
       }
       st.s2 = __fadd2_rn(st.s2, s2);
       st.t2 = __fadd2_rn(st.t2, t2);
+    };
+    if (fmaf(to_f32(least) - st.C, L, -st.R) <= -150.0f) {
+      if (far) stream(std::true_type{}); else stream(std::false_type{});
     } else {
       // Logits so large, or a scale so small, that the type has no such value: for fp16 scales below about 0.0016
       // (2048 x 151936 at 0.0015: 247 us, at 1: 113; 301 x 50021: 20.9 and 15.7).
