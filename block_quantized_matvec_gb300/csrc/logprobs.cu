@@ -487,10 +487,12 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : kWarps == 4 ? 
       st.s2 = __fadd2_rn(st.s2, s2);
       st.t2 = __fadd2_rn(st.t2, t2);
     };
-    if (fmaf(to_f32(least) - st.C, L, -st.R) <= -150.0f) {
+    const float least_y = fmaf(to_f32(least) - st.C, L, -st.R);
+    if (least_y <= -150.0f && least_y > -INFINITY) {
       if (far) stream(std::true_type{}); else stream(std::false_type{});
     } else {
-      // Logits so large, or a scale so small, that the type has no such value: for fp16 scales below about 0.0016
+      // Logits so large, or a scale so small, that the type has no such value, or a scale so large that it is infinitely
+      // far off: for fp16 scales below about 0.0016
       // (2048 x 151936 at 0.0015: 247 us, at 1: 113; 301 x 50021: 20.9 and 15.7).
 #pragma unroll 1
       for (int u = 0; u < kUnroll; ++u)

@@ -94,3 +94,32 @@ def test_a_few_tokens_above_a_finite_mask(dtype, mask):
             at = torch.randint(0, V, (d, allowed), device="cuda", generator=gen)
             x.scatter_(1, at, torch.randn((d, allowed), device="cuda", generator=gen) * 3)
             check(x.to(TYPES[dtype]).repeat(n // d, 1), 1.0, distinct=d)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("power", [10, 19, 30, 50, 63])
+@pytest.mark.parametrize("n,V", [(1, 349), (3, 50021), (700, 300), (200, 2600)])
+def test_differences_that_fp32_does_not_hold(dtype, power, n, V):
+    """Scales that put the next number below infinitely far: what is not equal to the largest has no probability."""
+    gen = torch.Generator("cuda").manual_seed(V)
+    low = torch.finfo(TYPES[dtype]).min
+    x = torch.randn((5, V), device="cuda", generator=gen)
+    x[1] *= 6e3 if dtype == "f16" else 1e30
+    x[2] = x[2].masked_fill(torch.rand(V, device="cuda", generator=gen) < 0.7, low)
+    x[3] = x[1].masked_fill(torch.rand(V, device="cuda", generator=gen) < 0.5, low)
+    x[4] = low * 0.9
+    x = x.to(TYPES[dtype]).repeat(-(-n // 5), 1)[:n]
+    for top in (1, 20):
+        if n > 1:
+            check(x, 2.0 ** power, top, distinct=5)
+    if n == 1:
+        for i in range(5):
+            check(rows_of(dtype, V, i, low), 2.0 ** power)
+
+
+def rows_of(dtype, V, i, low):
+    gen = torch.Generator("cuda").manual_seed(V + i)
+    x = torch.randn((1, V), device="cuda", generator=gen) * (6e3 if dtype == "f16" else 1e30) ** (i % 2)
+    if i > 1:
+        x = x.masked_fill(torch.rand(V, device="cuda", generator=gen) < 0.7, low)
+    return x.to(TYPES[dtype])
